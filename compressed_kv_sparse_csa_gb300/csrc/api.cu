@@ -6,12 +6,14 @@
 #include <cstring>
 
 #include "ds4x_internal.cuh"
+#include "paged.cuh"
 
 using namespace ds4x;
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool aligned16(const void *p) { return aligned_to(p, 16); }
 
 // Per-device cache of the architecture check: 0 unknown, 1 GB300, 2 other.
 std::atomic<int> g_arch_ok[64];
@@ -340,6 +342,115 @@ int ds4x_index_score_topk_prefill(const uint8_t *idx_rows, int64_t n_rows, const
   if (a != DS4X_OK) return a;
   return from_cuda(launch_score_prefill(idx_rows, n_rows, q_codes, q_scales, w, n_queries, causal_base, k, out_idx,
                                         out_score, ws, stream));
+}
+
+namespace {
+
+// The cache's arguments, common to the paged calls.
+int paged_cache(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const void *ws, PagedCache *c) {
+  if (pages == nullptr || table == nullptr || cu_tokens == nullptr || ws == nullptr) return DS4X_EINVAL;
+  if (!aligned16(pages) || !aligned16(ws)) return DS4X_EINVAL;
+  if (!aligned_to(table, 4) || !aligned_to(cu_tokens, 4)) return DS4X_EINVAL;
+  if (n_pages < 1 || n_pages > int64_t(INT32_MAX) || n_seqs < 1 || n_seqs == INT32_MAX || seq_pages < 1)
+    return DS4X_EINVAL;
+  int lg = 4;
+  while (lg < 8 && (1 << lg) != page_rows) ++lg;
+  if ((1 << lg) != page_rows) return DS4X_EINVAL;
+  if ((int64_t(seq_pages) << lg) > int64_t(INT32_MAX) || table_stride < seq_pages) return DS4X_EINVAL;
+  *c = PagedCache{const_cast<uint8_t *>(pages), n_pages, table, table_stride, cu_tokens, n_seqs, seq_pages, lg};
+  return DS4X_OK;
+}
+
+// A row array of n vectors of `dim` elements, `stride` elements apart, in whole 16 bytes.
+bool paged_vectors(const void *p, int32_t type, int64_t stride, int64_t dim) {
+  if (p == nullptr || !aligned16(p) || (type != DS4X_F32 && type != DS4X_BF16)) return false;
+  return stride >= dim && stride <= (int64_t(1) << 40) && stride % (type == DS4X_BF16 ? 8 : 4) == 0;
+}
+
+int paged_attn(PagedAttn &a, const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
+               int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, void *ws,
+               size_t ws_bytes, ds4x_stream_t stream) {
+  const int e = paged_cache(pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, &a.c);
+  if (e != DS4X_OK) return e;
+  if (a.n_tokens < 1 || a.n_tokens > DS4X_PAGED_MAX_TOKENS || a.n_heads < 1 || a.n_heads > DS4X_PAGED_MAX_HEADS)
+    return DS4X_EINVAL;
+  const int64_t vec = int64_t(a.n_heads) * DS4X_KV_DIM;
+  if (!paged_vectors(a.q, DS4X_BF16, a.q_stride, vec) || !paged_vectors(a.out, DS4X_BF16, a.out_stride, vec))
+    return DS4X_EINVAL;
+  if (a.lse != nullptr && !aligned_to(a.lse, 4)) return DS4X_EINVAL;
+  // a token's heads may be computed apart, so its output must not lie where its query does
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(a.q), o0 = reinterpret_cast<uintptr_t>(a.out);
+  const uintptr_t q1 = q0 + 2 * uintptr_t(a.q_stride * (a.n_tokens - 1) + vec);
+  const uintptr_t o1 = o0 + 2 * uintptr_t(a.out_stride * (a.n_tokens - 1) + vec);
+  if (q0 < o1 && o0 < q1) return DS4X_EINVAL;
+  if (ws_bytes < paged_attn_ws_bytes()) return DS4X_EWORKSPACE;
+  const int arch = check_arch();
+  if (arch != DS4X_OK) return arch;
+  return from_cuda(launch_paged_attn(a, ws, stream));
+}
+
+}  // namespace
+
+int ds4x_paged_append(uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                      int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                      const void *kv_in, int32_t in_type, int64_t in_stride, int64_t n_tokens, const int64_t *pos,
+                      const float *inv_freq, int32_t rope_style, void *ws, size_t ws_bytes, ds4x_stream_t stream) {
+  PagedCache c;
+  const int e = paged_cache(pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, &c);
+  if (e != DS4X_OK) return e;
+  if (row0 == nullptr || !aligned_to(row0, 8) || !aligned_to(pos, 8) || !aligned_to(inv_freq, 4)) return DS4X_EINVAL;
+  if (!paged_vectors(kv_in, in_type, in_stride, DS4X_KV_DIM)) return DS4X_EINVAL;
+  if (n_tokens < 1 || n_tokens > int64_t(INT32_MAX)) return DS4X_EINVAL;
+  if (rope_style != DS4X_ROPE_INTERLEAVED && rope_style != DS4X_ROPE_HALVES) return DS4X_EINVAL;
+  if (ws_bytes < kWsHeaderBytes) return DS4X_EWORKSPACE;
+  const int arch = check_arch();
+  if (arch != DS4X_OK) return arch;
+  return from_cuda(launch_paged_append(c, row0, kv_in, in_type == DS4X_BF16, in_stride, n_tokens, pos, inv_freq,
+                                       rope_style == DS4X_ROPE_HALVES, ws, stream));
+}
+
+int ds4x_paged_gather(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                      int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                      void *out, int32_t out_type, int64_t out_stride, int64_t n_tokens, void *ws, size_t ws_bytes,
+                      ds4x_stream_t stream) {
+  PagedCache c;
+  const int e = paged_cache(pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, &c);
+  if (e != DS4X_OK) return e;
+  if (row0 == nullptr || !aligned_to(row0, 8)) return DS4X_EINVAL;
+  if (!paged_vectors(out, out_type, out_stride, DS4X_KV_DIM)) return DS4X_EINVAL;
+  if (n_tokens < 1 || n_tokens > int64_t(INT32_MAX)) return DS4X_EINVAL;
+  if (ws_bytes < kWsHeaderBytes) return DS4X_EWORKSPACE;
+  const int arch = check_arch();
+  if (arch != DS4X_OK) return arch;
+  return from_cuda(launch_paged_gather(c, row0, out, out_type == DS4X_BF16, out_stride, n_tokens, ws, stream));
+}
+
+size_t ds4x_paged_attn_workspace(void) { return paged_attn_ws_bytes(); }
+
+int ds4x_paged_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                    int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row_begin,
+                    const int64_t *row_end, int32_t n_tokens, int32_t n_heads, const uint16_t *q_bf16,
+                    int64_t q_stride, float softmax_scale, uint16_t *out_bf16, int64_t out_stride, float *lse,
+                    void *ws, size_t ws_bytes, ds4x_stream_t stream) {
+  if (row_end == nullptr || !aligned_to(row_end, 8) || !aligned_to(row_begin, 8)) return DS4X_EINVAL;
+  PagedAttn a{PagedCache{}, row_begin, row_end, nullptr, nullptr, 0, n_tokens, n_heads, q_bf16, q_stride,
+              softmax_scale, out_bf16, out_stride, lse};
+  return paged_attn(a, pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, ws_bytes,
+                    stream);
+}
+
+int ds4x_paged_sparse_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
+                           int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens,
+                           const int64_t *n_rows, const int32_t *idx, int32_t k, int32_t n_tokens, int32_t n_heads,
+                           const uint16_t *q_bf16, int64_t q_stride, float softmax_scale, uint16_t *out_bf16,
+                           int64_t out_stride, float *lse, void *ws, size_t ws_bytes, ds4x_stream_t stream) {
+  if (n_rows == nullptr || idx == nullptr || !aligned_to(n_rows, 8) || !aligned_to(idx, 4)) return DS4X_EINVAL;
+  if (k < 1 || k > DS4X_PAGED_MAX_LIST) return DS4X_EINVAL;
+  PagedAttn a{PagedCache{}, nullptr, nullptr, n_rows, idx, k, n_tokens, n_heads, q_bf16, q_stride,
+              softmax_scale, out_bf16, out_stride, lse};
+  return paged_attn(a, pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, ws_bytes,
+                    stream);
 }
 
 }  // extern "C"

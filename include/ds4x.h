@@ -458,6 +458,154 @@ int ds4x_dense_attn_decode(const uint8_t *kv_rows, int64_t n_rows, const uint16_
                            float softmax_scale, uint16_t *out_bf16, float *lse, void *ws,
                            size_t ws_bytes, ds4x_stream_t stream);
 
+/* ---- Paged cache in 4 bits ------------------------------------------------
+ *
+ * The KV rows of many sequences in pages of one pool, a row in 368 bytes: the
+ * 512-value vector of ds4x_sparse_attn_decode (key and value at once, shared
+ * by all heads) with its 448 non-RoPE values in E2M1.  The pages describe the
+ * path for 583-byte rows in one array a session; this form of it is the
+ * library's own, for serving many sequences whose lengths are not known
+ * beforehand and for histories that 583 bytes a row make too large.
+ *
+ * A row:
+ *   448 E2M1 codes, two a byte, the even element in the low nibble, with one
+ *   UE8M0 scale per 32 elements: x = code * 2^(b - 127)
+ *   64 FP16 RoPE values with one UE8M0 scale for all: x = h * 2^(b - 127)
+ * The RoPE part's exponent is at least every block's, so it is the row's
+ * largest (the attention widens a row relative to it).
+ *
+ * A page of R = page_rows rows (16, 32, 64, 128 or 256) is three planes:
+ *   u8  [R][224] codes;  fp16 [R][64] RoPE values;
+ *   u8  [R][16]  scales: the 14 blocks', the RoPE part's, a zero byte
+ * pages is u8 [n_pages][R * 368], 16-byte aligned.  table is i32 [n_seqs][..],
+ * table_stride entries between sequences, of which seq_pages are used: row j
+ * of sequence s lies in page table[s][j / R] at j % R, j < seq_pages * R.
+ * Entries that no call reaches may hold anything.
+ *
+ * Tokens are ragged over the sequences: cu_tokens is i32 [n_seqs + 1],
+ * non-decreasing, cu_tokens[0] = 0; sequence s has the tokens cu_tokens[s] ..
+ * cu_tokens[s + 1] - 1 of a call, any number of them.  Tokens from
+ * cu_tokens[n_seqs] up to n_tokens are padding: nothing of theirs is read or
+ * written.  cu_tokens and every array beside it are device memory, so a
+ * captured call follows their contents.
+ *
+ * A row that the table places nowhere (a row below 0 or beyond seq_pages * R,
+ * a page outside [0, n_pages)) is left out and flags DS4X_EDEVICE in the
+ * status word at the head of ws (256 bytes, zero before first use:
+ * ds4x_workspace_init / ds4x_workspace_status).
+ *
+ * Common errors: DS4X_EINVAL (a null or misaligned pointer, a size or stride
+ * outside its range), DS4X_EWORKSPACE, DS4X_EARCH, DS4X_ECUDA.  seq_pages *
+ * page_rows and n_pages are at most 2^31 - 1.
+ */
+enum {
+  DS4X_PAGED_ROW_BYTES = 368,
+  DS4X_PAGED_MAX_PAGE_ROWS = 256,
+  DS4X_PAGED_MAX_HEADS = 128,
+  DS4X_PAGED_MAX_TOKENS = 65535, /* an attention call's tokens */
+  DS4X_PAGED_MAX_LIST = 8192     /* rows a token lists */
+};
+
+enum { DS4X_F32 = 0, DS4X_BF16 = 1 };                         /* element types  */
+enum { DS4X_ROPE_INTERLEAVED = 0, DS4X_ROPE_HALVES = 1 };     /* rotated pairs  */
+
+/*
+ * Writes new rows: rotates the RoPE part at its position, quantises, packs
+ * and places each token's row in its sequence's pages.
+ *
+ *   row0       i64 [n_seqs]: token j of sequence s (j = 0 for its first of
+ *              this call) becomes the sequence's row row0[s] + j
+ *   kv_in      f32 or bf16 (in_type) [n_tokens][512], in_stride elements from
+ *              token to token (>= 512, a multiple of 8 (bf16) or 4 (f32))
+ *   n_tokens   1 .. 2^31 - 1
+ *   pos        i64 [n_tokens] positions, or NULL: a row's position is its
+ *              number in the sequence
+ *   inv_freq   f32 [32]: pair i turns by pos * inv_freq[i] radians (the turn
+ *              is formed in 64-bit fixed point, so far positions lose
+ *              nothing); NULL: no rotation.  A negative frequency turns back.
+ *   rope_style DS4X_ROPE_INTERLEAVED: pair i is RoPE elements 2 i, 2 i + 1;
+ *              DS4X_ROPE_HALVES: elements i, 32 + i
+ *
+ * Scales: for each 32-value block the least e in [-96, 96] with amax <= 6 *
+ * 2^e, codes to nearest, ties to even, the sign kept; for the RoPE part the
+ * largest of those and the least e in [-96, 96] with amax <= 8 * 2^e, values
+ * rounded to FP16 (nearest even, saturating).  The codes and the blocks'
+ * scales are bit-exact with that rule.
+ *
+ * A page that two sequences of one call both write is the caller's error:
+ * each of its rows holds bytes of either token.
+ */
+int ds4x_paged_append(uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                      int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                      const void *kv_in, int32_t in_type, int64_t in_stride, int64_t n_tokens, const int64_t *pos,
+                      const float *inv_freq, int32_t rope_style, void *ws, size_t ws_bytes, ds4x_stream_t stream);
+
+/*
+ * Reads rows back: out[t] is the row row0[s] + j of token t's place (as
+ * ds4x_paged_append places it), dequantised.
+ *
+ *   out        f32 or bf16 (out_type; bf16 rounds to nearest even)
+ *              [n_tokens][512], out_stride elements from token to token
+ *              (>= 512, a multiple of 8 (bf16) or 4 (f32)); zeros where the
+ *              table places no row
+ */
+int ds4x_paged_gather(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                      int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                      void *out, int32_t out_type, int64_t out_stride, int64_t n_tokens, void *ws, size_t ws_bytes,
+                      ds4x_stream_t stream);
+
+/* Workspace bytes of both attentions below (the same for every size). */
+size_t ds4x_paged_attn_workspace(void);
+
+/*
+ * Attention of each token over the rows [row_begin, row_end) of its sequence:
+ * decoding (a token a sequence), several new tokens a sequence, a prompt's
+ * chunk (row_end rising token by token: causal), a sliding window (row_begin).
+ *
+ *   l_hj = softmax_scale * (q_h . v_j);  o_h = sum_j softmax_j(l_h)_j v_j;
+ *   lse_h = log sum_j e^(l_hj)
+ *
+ *   row_begin  i64 [n_tokens] or NULL (0); row_end i64 [n_tokens].  A token
+ *              with row_end <= row_begin sees nothing: zeros, lse -inf
+ *   n_tokens   1 .. DS4X_PAGED_MAX_TOKENS
+ *   n_heads    1 .. DS4X_PAGED_MAX_HEADS
+ *   q_bf16     bf16 [n_tokens][n_heads][512], q_stride elements from token to
+ *              token (>= n_heads * 512, a multiple of 8)
+ *   out_bf16   bf16 [n_tokens][n_heads][512], out_stride likewise; must not
+ *              overlap q_bf16
+ *   lse        f32 [n_tokens][n_heads] or NULL
+ *   ws         >= ds4x_paged_attn_workspace() bytes, zero-filled before first
+ *              use; not for two calls that may overlap on the GPU (two
+ *              captured graphs that may run at once need one each)
+ *
+ * Rows outside the range are never read, so what unwritten rows hold does not
+ * matter.  Results do not depend on the order in which the GPU works.
+ */
+int ds4x_paged_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                    int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row_begin,
+                    const int64_t *row_end, int32_t n_tokens, int32_t n_heads, const uint16_t *q_bf16,
+                    int64_t q_stride, float softmax_scale, uint16_t *out_bf16, int64_t out_stride, float *lse,
+                    void *ws, size_t ws_bytes, ds4x_stream_t stream);
+
+/*
+ * Attention of each token over its own list of its sequence's rows (the
+ * indexer's top-k: ds4x_index_score_topk and its batched and prefill forms
+ * write such lists).
+ *
+ *   n_rows     i64 [n_seqs]: the sequence's rows
+ *   idx        i32 [n_tokens][k]: rows in any order, each entry counted (a row
+ *              listed twice weighs twice); -1 entries are skipped; others
+ *              outside [0, n_rows[s]) are skipped and flag DS4X_EDEVICE
+ *   k          1 .. DS4X_PAGED_MAX_LIST
+ *   the rest as ds4x_paged_attn; a token whose list holds no row gets zeros
+ *   and -inf
+ */
+int ds4x_paged_sparse_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
+                           int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens,
+                           const int64_t *n_rows, const int32_t *idx, int32_t k, int32_t n_tokens, int32_t n_heads,
+                           const uint16_t *q_bf16, int64_t q_stride, float softmax_scale, uint16_t *out_bf16,
+                           int64_t out_stride, float *lse, void *ws, size_t ws_bytes, ds4x_stream_t stream);
+
 /* ---- Packed-row checkpoints (host memory, no CUDA call) -----------------
  *
  * A checkpoint holds, per layer, the native packed rows: the raw sliding
