@@ -1,139 +1,872 @@
-// Attention over the paged 4-bit cache.
+// Attention over the paged 4-bit cache on the tensor cores.
 //
 //   l_hj = scale * (q_h . v_j),  o_h = sum_j softmax_j(l_h)_j v_j,
 //   lse_h = log sum_j e^(l_hj)
 //
 // over a token's rows: the range [row_begin, row_end) of its sequence, or its
-// own list of rows.  A CTA takes one token and eight heads, a head a warp (16
-// of the 512 values a lane): tiles of 32 rows are widened to fp32 in shared
-// memory, read by all eight warps, and each warp runs the softmax online with
-// a running maximum and sum in fp32.
+// own list of rows.  A unit is a token and up to 64 of its heads; its rows come
+// in tiles of 64.  Two tcgen05.mma (kind::f16, fp16 operands, fp32 sums in
+// tensor memory) a tile:
+//
+//   S^T[64 rows][heads] = V'[64 rows][512] . Q'[heads][512]^T
+//   O^T[512 dims][heads] += V'^T[512][64 rows] . P^T[64 rows][heads]
+//
+// V' is the tile's rows widened once to fp16, in shared memory, as eight
+// 128-byte-swizzled panels of 64 dims (16-byte chunk c of row r at c ^ (r % 8)):
+// the first product reads them K-major, the second the same bytes MN-major.
+//
+// Exact operands.  Row j's exponent E_j is its RoPE part's, the row's largest:
+// V'_j = v_j 2^-E_j, at most 8, is exact in fp16 while a block's scale lies
+// within 2^14 of 2^E_j (smaller blocks round at 2^-25 of 2^E_j); the RoPE part's
+// fp16 values are V' as they are.  Q' = q 2^c in fp16, c taking the unit's
+// largest |q| into [2^14, 2^15): a bf16 value is exact down to 2^-32 of it.
+//
+// Softmax in the log2 domain, online, with the row's exponent kept apart:
+// x_j = l_j log2 e + E_j, w_j = 2^(x_j - m) is what multiplies V'_j, and the
+// denominator is sum_j w_j 2^-E_j.  m is a head's running maximum of x, lazily: it
+// moves (and O^T and the sums are rescaled) only when a tile's x exceeds it by
+// more than 8, so w stays below 2^8.  w enters the second product as fp16 (half
+// a step is 2^-12 to 2^-11 of it, an eighth of the bf16 output's own step; hi +
+// lo parts would double that product); sums are fp32.  E_j is within +-96, so
+// the denominator stays inside fp32 for 2^22 rows.
+//
+// Work split.  All units' tiles, in order, are cut into one run a CTA (one CTA
+// an SM), so any mix of lengths fills the GPU; a cut that falls near a unit's
+// end moves there.  A unit that one CTA covers goes straight to the output; the
+// parts of the others go to the workspace in fp32, normalised, with their
+// log-sum-exp, and paged_combine_kernel joins them in a fixed order.  The cuts
+// depend on the lengths alone, so results do not depend on timing.
+//
+// Roles (25 warps).  W (warps 0-15): two groups of 8 warps take the tiles in
+// turn, each with its own V' buffer, and load their next tile's 16-byte words
+// into registers as soon as the last is widened (two tiles are in flight); both
+// convert Q' when a unit begins.  X (16-23): the softmax, four 16-row quarters
+// of S^T by two halves of the heads, and the unit's output.  M (24): one thread
+// issues the products, S of two tiles, then O of the two: while one tile's
+// products run the other is widened or in its softmax.
+//
+// Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
+// wait blocks, so every role runs to its end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace ds4x {
 namespace {
 
-constexpr int kHeadsCta = 8;
-constexpr int kThreads = kHeadsCta * 32;
-constexpr int kTile = 32;
+using namespace ptx;
 
-struct Smem {
-  float v[kTile][DS4X_KV_DIM];
-  int ok[kTile];
+constexpr int kDim = DS4X_KV_DIM;  // 512
+constexpr int kTile = 64;          // rows a tile
+constexpr int kHeads = 64;         // heads a unit, at most
+constexpr int kWWarps = 16, kXWarps = 8;
+constexpr int kWThreads = 32 * kWWarps, kXThreads = 32 * kXWarps;
+constexpr int kThreads = kWThreads + kXThreads + 32;
+constexpr int kMaxCtas = 160;
+constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
+constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
+constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.0f;
+constexpr int kNoRow = INT32_MIN;  // rowe of a row that is not there
+constexpr float kNoMax = -3e38f;   // a head's maximum before its first row
+enum { kBarQ = 1, kBarX = 2 };     // named barriers
+
+struct __align__(1024) Smem {
+  uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
+  uint8_t v[2][kTile * kDim * 2];   // V': 8 panels of 8 KB, two tiles
+  uint8_t p[2][kTile * kHeads * 2]; // P^T: one panel, two tiles
+  int rowe[2][kTile];               // E_j, or kNoRow
+  float red[4][kHeads];
+  float alpha[kHeads];
+  float mh[kHeads], hinv[kHeads];
+  float qbase[2];                   // scale log2 e 2^-c, by segment parity
+  uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
+  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2], qfull, qfree, drain;
+  long long scan[kThreads / 32];
+  long long cut0, cut1;             // the CTA's run of tiles
+  int unit0, off0;                  // where it begins: tile off0 of unit unit0
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Smem) + 1024 - 16 <= 232448, "shared-memory budget");
+
+// The workspace behind its header.  Part 2 c: CTA c's share of a unit that an
+// earlier CTA began; part 2 c + 1: of one that it begins and a later one ends.
+struct Parts {
+  int32_t unit[2 * kMaxCtas];            // the part's unit, or -1
+  float lse2[2 * kMaxCtas][kHeads];      // log2 of the denominator
+  float o[2 * kMaxCtas][kHeads][kDim];   // normalised
 };
 
-__device__ __forceinline__ float pow2_byte(uint32_t b) {
-  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+struct Args {
+  PagedAttn a;
+  int32_t groups;     // head groups a token
+  int32_t group;      // heads a group (the last may have fewer)
+  int32_t n_cols;     // `group` rounded up to 16: the products' N
+};
+
+__device__ __forceinline__ unsigned long long globaltimer() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
 }
 
-__global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedAttn a, WsHeader *hdr) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void wait_bar(Smem &sm, unsigned long long *bar, uint32_t parity, WsHeader *hdr) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return;
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait(b, parity)) {
+    if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
+    if (globaltimer() - t0 > kTimeoutNs) {
+      atomicExch(&hdr->status, int32_t(DS4X_ETIMEOUT));
+      *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+      return;
+    }
+  }
+}
+
+// Shared-memory descriptor, 128-byte swizzle.  K-major: sbo = distance of
+// 8-row groups.  MN-major: lbo = distance of 64-wide panels along M (N), sbo =
+// distance of 8-row groups along K.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// 16 lanes x 32 columns: register 4 j + 2 r + c of lane T holds lane T / 4 + 8 r,
+// column 8 j + 2 (T % 4) + c.
+__device__ __forceinline__ void tc_ld_16x256_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
+// 2^e as fp16 bits for e <= 0 (0 below the smallest subnormal 2^-24).
+__device__ __forceinline__ uint32_t pow2_half_bits(int e) {
+  if (e >= -14) return uint32_t(e + 15) << 10;
+  return e >= -24 ? 1u << (e + 24) : 0u;
+}
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A token's rows: n of them, from row r0 of its sequence (or of its list).
+struct Rows {
+  int64_t r0;
+  int32_t n;
+};
+__device__ __forceinline__ Rows token_rows(const PagedAttn &a, int t) {
+  if (a.idx != nullptr) return Rows{0, a.k};
+  // no further than the table goes (a range past it is flagged by find_cuts)
+  const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
+  const int64_t b = a.row_begin != nullptr ? max(int64_t(0), int64_t(__ldcg(a.row_begin + t))) : 0;
+  const int64_t e = min(room, int64_t(__ldcg(a.row_end + t)));
+  return Rows{b, int32_t(max(int64_t(0), e - b))};
+}
+// A token without a row still has a tile (of rows that are not there): it writes the zeros.
+__device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
+
+// Walks the CTA's run of tiles (numbered from 0 locally), a unit's share at a time.
+struct Walk {
+  int unit, off;   // the share's unit, and its first tile within it
+  int i0, i1;      // the share's tiles, locally
+  int tiles;       // the unit's tiles
+  int64_t r0;
+  int n;
+  __device__ __forceinline__ void load(const Args &g, int total) {
+    const Rows r = token_rows(g.a, unit / g.groups);
+    r0 = r.r0;
+    n = r.n;
+    tiles = rows_tiles(n);
+    i1 = int(min(int64_t(total), int64_t(i0) + tiles - off));
+  }
+  __device__ __forceinline__ void begin(const Args &g, const Smem &sm, int total) {
+    unit = sm.unit0;
+    off = sm.off0;
+    i0 = 0;
+    load(g, total);
+  }
+  __device__ __forceinline__ void next(const Args &g, int total) {
+    ++unit;
+    off = 0;
+    i0 = i1;
+    load(g, total);
+  }
+};
+
+// Where this lane's row of a tile lies.
+struct RowAt {
+  const uint8_t *page;  // null: no row
+  int at;
+};
+
+// ---- the cuts ------------------------------------------------------------------
+
+// The run of CTA c of g: unit0, off0, cut0, cut1.  All threads.
+__device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
+  const PagedAttn &a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x, h = blockIdx.y * kHeadsCta + warp;
-  const int32_t s = paged_seq_of(a.c, t, lane);
-  if (s < 0) return;
-  int64_t r0 = 0, n;
+  const int n = max(0, min(a.n_tokens, __ldcg(a.c.cu + a.c.n_seqs)));
+  const int per = (n + kThreads - 1) / kThreads;
+  const int t0 = min(n, tid * per), t1 = min(n, t0 + per);
+  long long mine = 0;
+  for (int t = t0; t < t1; ++t) {
+    mine += (long long)(rows_tiles(token_rows(a, t).n)) * g.groups;
+    if (blockIdx.x == 0 && a.idx == nullptr && __ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
+      atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  if (tid == 0) sm.unit0 = sm.off0 = 0;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long v = sm.scan[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  // every CTA of the first G has a tile (total < 2^43 and G <= 160: no overflow)
+  const long long G = max(1ll, min((long long)gridDim.x, total)), tol = total / (16 * G);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const long long x = (long long)(blockIdx.x + e) * total / G;
+    if (x >= total) {
+      if (tid == 0) (e ? sm.cut1 : sm.cut0) = total;
+      continue;
+    }
+    if (x < before || x >= before + mine) continue;
+    long long p = before;  // tile x lies in this thread's tokens
+    for (int t = t0; t < t1; ++t) {
+      const int tiles = rows_tiles(token_rows(a, t).n);
+      const long long w = (long long)(tiles)*g.groups;
+      if (x < p + w) {
+        const long long k = (x - p) / tiles;
+        int unit = t * g.groups + int(k);
+        long long off = (x - p) - k * tiles, at = x;
+        if (off <= tol) {
+          at -= off;
+          off = 0;
+        } else if (tiles - off <= tol) {
+          at += tiles - off;
+          off = 0;
+          ++unit;
+        }
+        if (e == 0) {
+          sm.cut0 = at;
+          sm.unit0 = unit;
+          sm.off0 = int(off);
+        } else {
+          sm.cut1 = at;
+        }
+        break;
+      }
+      p += w;
+    }
+  }
+  __syncthreads();
+}
+
+// ---- W: widening ----------------------------------------------------------------
+
+// The row of a tile that this lane helps to widen: the tile's row `r` (0 .. 63).
+__device__ __forceinline__ RowAt find_row(const Args &g, const Walk &w, int seq, int64_t n_rows, int tile, int r,
+                                          WsHeader *hdr) {
+  const PagedAttn &a = g.a;
+  const int64_t pos = int64_t(tile) * kTile + r;
+  if (pos >= w.n || seq < 0) return RowAt{nullptr, 0};
+  int64_t row = w.r0 + pos;
   if (a.idx != nullptr) {
-    n = a.k;
+    row = __ldcg(a.idx + int64_t(w.unit / g.groups) * a.k + pos);
+    if (row == -1) return RowAt{nullptr, 0};
+    if (row >= n_rows) row = -2;
+  }
+  const PagedRow p = paged_row(a.c, seq, row);
+  if (p.page == nullptr) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  return RowAt{p.page, p.at};
+}
+
+// This lane's 16-byte words of its row: three whole blocks' codes, half of the
+// lanes one more, two of the RoPE part's eight, the scale record.
+struct Raw {
+  uint4 c[4], t[2], sc;
+  int ok;
+};
+__device__ __forceinline__ void load_raw(const PagedCache &c, const RowAt &r, int sub, Raw &w) {
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  w.ok = r.page != nullptr;
+  if (w.ok) {
+    const PagedRow p{r.page, r.at};
+    const uint4 *co = reinterpret_cast<const uint4 *>(r.page + paged_code_off(p));
+    const uint4 *ta = reinterpret_cast<const uint4 *>(r.page + paged_tail_off(c, p));
+    w.sc = __ldcg(reinterpret_cast<const uint4 *>(r.page + paged_scale_off(c, p)));
+    w.c[0] = __ldcg(co + sub);
+    w.c[1] = __ldcg(co + 4 + sub);
+    w.c[2] = __ldcg(co + 8 + sub);
+    w.c[3] = sub < 2 ? __ldcg(co + 12 + sub) : z;
+    w.t[0] = __ldcg(ta + sub);
+    w.t[1] = __ldcg(ta + 4 + sub);
   } else {
-    r0 = a.row_begin != nullptr ? max(int64_t(0), int64_t(__ldcg(a.row_begin + t))) : 0;
-    // no further than the table goes (a range past it is the caller's error)
-    const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2, end = __ldcg(a.row_end + t);
-    if (end > room && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-    n = max(int64_t(0), min(end, room) - r0);
+    w.sc = w.c[0] = w.c[1] = w.c[2] = w.c[3] = w.t[0] = w.t[1] = z;
   }
-  const int64_t n_rows = a.idx != nullptr ? __ldcg(a.n_rows + s) : 0;
-  float q[16], o[16], m = -INFINITY, sum = 0.0f;
+}
+
+// Block b of row r: 32 codes times 2^(scale - E) to V'.
+__device__ __forceinline__ void widen_block(uint32_t v, int r, int b, const uint4 &c, int d) {
+  const uint32_t f = pow2_half_bits(d) * 0x10001u;
+  const uint32_t base = v + uint32_t(b >> 1) * 8192u + uint32_t(r) * 128u;
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    q[i] = h < a.n_heads ? __uint_as_float(uint32_t(a.q[t * a.q_stride + h * DS4X_KV_DIM + 32 * i + lane]) << 16) : 0.0f;
-    o[i] = 0.0f;
+  for (int u = 0; u < 4; ++u) {
+    uint32_t h0, h1, h2, h3;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+        : "r"(w[u]));
+    sts16(base + (uint32_t(((b & 1) * 4 + u) ^ (r & 7)) << 4), hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f),
+          hmul2_bits(h3, f));
   }
-  for (int64_t j0 = 0; j0 < n; j0 += kTile) {
-    __syncthreads();
-    for (int j = warp; j < kTile; j += kHeadsCta) {
-      PagedRow p{nullptr, 0};
-      if (j0 + j < n) {
-        int64_t r = r0 + j0 + j;
-        bool bad = false;
-        if (a.idx != nullptr) {
-          r = __ldcg(a.idx + int64_t(t) * a.k + j0 + j);
-          bad = r < -1 || r >= n_rows;
-        }
-        if (!bad && r >= 0) p = paged_row(a.c, s, r);
-        if (p.page == nullptr && (bad || r >= 0) && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-      }
-      if (lane == 0) sm.ok[j] = p.page != nullptr;
-      if (p.page == nullptr) continue;
-      const uint8_t *sc = p.page + paged_scale_off(a.c, p), *co = p.page + paged_code_off(p);
+}
+
+__device__ __forceinline__ void widen(Smem &sm, int buf, int r, int sub, const Raw &w) {
+  const uint32_t v = smem_u32(sm.v[buf]);
+  const int E = int((w.sc.w >> 16) & 0xffu);
+  const uint32_t sh = 8 * sub;
+  widen_block(v, r, sub, w.c[0], min(0, int((w.sc.x >> sh) & 0xffu) - E));
+  widen_block(v, r, 4 + sub, w.c[1], min(0, int((w.sc.y >> sh) & 0xffu) - E));
+  widen_block(v, r, 8 + sub, w.c[2], min(0, int((w.sc.z >> sh) & 0xffu) - E));
+  if (sub < 2) widen_block(v, r, 12 + sub, w.c[3], min(0, int((w.sc.w >> sh) & 0xffu) - E));
+  const uint32_t base = v + 7u * 8192u + uint32_t(r) * 128u;
 #pragma unroll
-      for (int i = 0; i < 7; ++i) {  // byte 32 i + lane: elements 64 i + 2 lane, + 1
-        const uint32_t b = __ldcg(co + 32 * i + lane);
-        const float f = pow2_byte(__ldcg(sc + 2 * i + (lane >> 4)));
+  for (int u = 0; u < 2; ++u)
+    sts16(base + (uint32_t((4 * u + sub) ^ (r & 7)) << 4), w.t[u].x, w.t[u].y, w.t[u].z, w.t[u].w);
+  if (sub == 0) sm.rowe[buf][r] = w.ok ? E - 127 : kNoRow;
+}
+
+// Q' of a unit: warp w converts heads 4 w .. 4 w + 3, lane L the 16-byte chunks
+// L and 32 + L of each; heads that the unit does not have are zeros.
+__device__ __forceinline__ void load_query(const Args &g, const Walk &w, int warp, int lane, uint4 (&qv)[8]) {
+  const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
+  const int heads = min(g.group, g.a.n_heads - h0);
+  const uint16_t *q = g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0) * kDim;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t c4 = (b >> (4 * u)) & 15u;
-          const float x = __half2float(__ushort_as_half(uint16_t((c4 & 7u) << 9))) * 16384.0f;
-          sm.v[j][64 * i + 2 * lane + u] = (c4 & 8u ? -x : x) * f;
+  for (int i = 0; i < 8; ++i) {
+    const int h = 4 * warp + (i >> 1);
+    qv[i] = h < heads ? __ldcg(reinterpret_cast<const uint4 *>(q + h * kDim) + 32 * (i & 1) + lane) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void convert_query(const Args &g, Smem &sm, int seg, int warp, int lane, const uint4 (&qv)[8],
+                                              WsHeader *hdr) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  const int slot = seg % 3;
+  if (lane == 0) atomicMax(&sm.qmax[slot], m);
+  // the next unit's slot: its last readers (three units ago) passed the previous barrier
+  if (threadIdx.x == 0) sm.qmax[(seg + 1) % 3] = 0;
+  named_bar_sync(kBarQ, kWThreads);
+  const int e = int(*reinterpret_cast<volatile uint32_t *>(&sm.qmax[slot]) >> 7);  // the largest exponent field
+  const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
+  const float f = pow2f(c);
+  // the previous unit's last first product is done (so is the softmax of the unit before it, qbase's last reader)
+  if (seg > 0) wait_bar(sm, &sm.qfree, (seg - 1) & 1, hdr);
+  if (threadIdx.x == 0) sm.qbase[seg & 1] = g.a.scale * kLog2e * pow2f(-c);
+  const uint32_t qa = smem_u32(sm.q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int h = 4 * warp + (i >> 1), C = 32 * (i & 1) + lane;
+    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
+    sts16(qa + uint32_t(C >> 3) * 8192u + uint32_t(h) * 128u + (uint32_t((C & 7) ^ (h & 7)) << 4), o[0], o[1], o[2],
+          o[3]);
+  }
+}
+
+__device__ __forceinline__ void role_w(const Args &g, Smem &sm, int total, WsHeader *hdr) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int buf = warp >> 3;                  // the group and its V' buffer
+  const int r = 8 * (warp & 7) + (lane & 7);  // the tile's row that this lane helps to widen
+  const int sub = lane >> 3;
+  // the look-ahead: the walk two tiles on
+  Walk la;
+  la.begin(g, sm, total);
+  int seq = paged_seq_of(g.a.c, la.unit / g.groups, lane);
+  int64_t n_rows = g.a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(g.a.n_rows + seq)) : 0;
+  auto look = [&](int i) {  // the lane's row of tile i
+    if (i >= total) return RowAt{nullptr, 0};
+    while (i >= la.i1) {
+      la.next(g, total);
+      seq = paged_seq_of(g.a.c, la.unit / g.groups, lane);
+      n_rows = g.a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(g.a.n_rows + seq)) : 0;
+    }
+    return find_row(g, la, seq, n_rows, la.off + (i - la.i0), r, hdr);
+  };
+  Raw raw;
+  int i = buf;
+  load_raw(g.a.c, look(i), sub, raw);
+  RowAt next = look(i + 2);
+  Walk w;
+  w.begin(g, sm, total);
+  for (int seg = 0;; ++seg) {
+    {
+      uint4 qv[8];
+      load_query(g, w, warp, lane, qv);
+      convert_query(g, sm, seg, warp, lane, qv, hdr);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
+    }
+    for (; i < w.i1; i += 2) {
+      if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
+      widen(sm, buf, r, sub, raw);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
+      load_raw(g.a.c, next, sub, raw);
+      next = look(i + 4);
+    }
+    if (w.i1 >= total) break;
+    w.next(g, total);
+  }
+}
+
+// ---- M: the products ---------------------------------------------------------------
+
+__device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, int total, WsHeader *hdr) {
+  const uint32_t q_a = smem_u32(sm.q), v_a = smem_u32(sm.v[0]), p_a = smem_u32(sm.p[0]);
+  const uint32_t idS = idesc_f16(kTile, uint32_t(g.n_cols), 0, 0);  // V' K-major, Q' K-major
+  const uint32_t idO = idesc_f16(128, uint32_t(g.n_cols), 1, 1);    // V'^T MN-major, P^T MN-major
+  const uint64_t dS_b = desc_sw128(q_a, 16, 1024);
+  Walk w;
+  w.begin(g, sm, total);
+  auto issue_s = [&](int i) {
+    const int b = i & 1;
+    wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
+    tc_fence_after();
+    const uint64_t dS_a = desc_sw128(v_a + 65536u * b, 16, 1024);
+    // K step ks: 16 dims, 32 bytes into panel ks / 4 (descriptor addresses count 16 bytes)
+#pragma unroll
+    for (int ks = 0; ks < kDim / 16; ++ks)
+      mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)),
+                 dS_b + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)), idS, ks > 0 ? 1u : 0u);
+    tc_commit(smem_u32(&sm.sfull[b]));
+    if (i + 1 == w.i1) tc_commit(smem_u32(&sm.qfree));
+  };
+  auto issue_o = [&](int i) {
+    const int b = i & 1;
+    wait_bar(sm, &sm.pfull[b], (i >> 1) & 1, hdr);
+    tc_fence_after();
+    const uint64_t dO_a = desc_sw128(v_a + 65536u * b, 8192, 1024), dO_b = desc_sw128(p_a + 8192u * b, 8192, 1024);
+    const uint32_t acc = i > w.i0 ? 1u : 0u;
+    // M tile mi: panels 2 mi, 2 mi + 1; K step ks: 16 rows (2 KB)
+#pragma unroll
+    for (int mi = 0; mi < kDim / 128; ++mi)
+#pragma unroll
+      for (int ks = 0; ks < kTile / 16; ++ks)
+        mma_f16_ss(tmem + kOCol + 64u * mi, dO_a + uint64_t(1024 * mi + 128 * ks), dO_b + uint64_t(128 * ks), idO,
+                   ks > 0 ? 1u : acc);
+    tc_commit(smem_u32(&sm.pvdone[b]));
+  };
+  for (int seg = 0;; ++seg) {
+    wait_bar(sm, &sm.qfull, seg & 1, hdr);
+    for (int i = w.i0; i < w.i1; i += 2) {
+      issue_s(i);
+      if (i + 1 < w.i1) issue_s(i + 1);
+      issue_o(i);
+      if (i + 1 < w.i1) issue_o(i + 1);
+    }
+    if (w.i1 >= total) break;
+    w.next(g, total);
+  }
+  tc_commit(smem_u32(&sm.drain));  // nothing may still write this CTA's memory when it exits
+  wait_bar(sm, &sm.drain, 0, hdr);
+}
+
+// ---- X: softmax and output ------------------------------------------------------------
+
+__device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, int total, Parts *parts, WsHeader *hdr) {
+  const PagedAttn &a = g.a;
+  const int lane = threadIdx.x & 31, xw = (threadIdx.x >> 5) - kWWarps, xt = threadIdx.x - kWThreads;
+  const int qd = xw & 3, half = xw >> 2;        // tile rows 16 qd .., heads 32 half ..
+  const bool busy = 32 * half < g.n_cols;
+  const int r0 = 16 * qd + (lane >> 2);         // this lane's rows r0 and r0 + 8
+  const int hb = 32 * half + 2 * (lane & 3);    // this lane's heads hb + 8 j + c
+  const uint32_t lane_base = uint32_t(32 * qd) << 16;
+  Walk w;
+  w.begin(g, sm, total);
+  for (int seg = 0;; ++seg) {
+    float m[8], sum[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = kNoMax, sum[k] = 0.0f;
+    for (int i = w.i0; i < w.i1; ++i) {
+      const int b = i & 1;
+      wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
+      tc_fence_after();
+      const float base = sm.qbase[seg & 1];
+      float x[16], er[2];  // x[4 j + 2 row + c]; the rows' E_j
+      float over = -INFINITY, under = 0.0f;
+      if (busy) {
+        uint32_t s[16];
+        tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
+        const int e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
+        // a row that is not there: x = -inf, weight 0
+        const float f[2] = {e0 == kNoRow ? 0.0f : base * pow2f(e0), e1 == kNoRow ? 0.0f : base * pow2f(e1)};
+        const float ef[2] = {e0 == kNoRow ? -INFINITY : float(e0), e1 == kNoRow ? -INFINITY : float(e1)};
+        er[0] = e0 == kNoRow ? 0.0f : float(e0);
+        er[1] = e1 == kNoRow ? 0.0f : float(e1);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          x[k] = fmaf(__uint_as_float(s[k]), f[(k >> 1) & 1], ef[(k >> 1) & 1]);
+          const float d = x[k] - m[2 * (k >> 2) + (k & 1)];
+          over = fmaxf(over, d);
+          under = fminf(under, d);
         }
       }
-      const uint32_t w = __ldcg(reinterpret_cast<const uint32_t *>(p.page + paged_tail_off(a.c, p)) + lane);
-      const float f = pow2_byte(__ldcg(sc + kPgTailScale));
-      sm.v[j][DS4X_KV_NOPE + 2 * lane] = __half2float(__ushort_as_half(uint16_t(w))) * f;
-      sm.v[j][DS4X_KV_NOPE + 2 * lane + 1] = __half2float(__ushort_as_half(uint16_t(w >> 16))) * f;
+      if (named_bar_or(kBarX, kXThreads, over > kLazy)) {
+        // some head's maximum moves: each head's maximum over the tile
+        if (busy) {
+          float mx[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            mx[k] = fmaxf(x[4 * (k >> 1) + (k & 1)], x[4 * (k >> 1) + 2 + (k & 1)]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+          }
+          if (lane < 4)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sm.red[qd][hb + 8 * (k >> 1) + (k & 1)] = mx[k];
+        }
+        named_bar_sync(kBarX, kXThreads);
+        if (busy) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int h = hb + 8 * (k >> 1) + (k & 1);
+            const float mt = fmaxf(fmaxf(sm.red[0][h], sm.red[1][h]), fmaxf(sm.red[2][h], sm.red[3][h]));
+            float al = 1.0f;
+            if (mt > m[k] + kLazy) {
+              al = ex2(m[k] - mt);  // 0 from kNoMax
+              const float half_al = ex2(0.5f * (m[k] - mt));  // (rows far apart in size: al itself may underflow)
+              sum[k] = sum[k] * half_al * half_al;
+              m[k] = mt;
+              under = -INFINITY;
+            }
+            if (qd == 0 && lane < 4) sm.alpha[h] = al;
+          }
+        }
+        named_bar_sync(kBarX, kXThreads);
+        if (i > w.i0 && busy) {
+          // O^T of the unit so far, once the previous tile's product is done
+          wait_bar(sm, &sm.pvdone[b ^ 1], ((i - 1) >> 1) & 1, hdr);
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < 2 * kDim / 128; ++k) {
+            const uint32_t ta = tmem + lane_base + kOCol + 64u * (k >> 1) + 32u * half + 16u * (k & 1);
+            uint32_t o[16];
+            tc_ld_x16(ta, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              o[u] = __float_as_uint(__uint_as_float(o[u]) * sm.alpha[32 * half + 16 * (k & 1) + u]);
+            tc_st_x16(ta, o);
+          }
+          tc_wait_st();
+        }
+      }
+      if (busy) {
+        const uint32_t pa = smem_u32(sm.p[b]) + 4u * (lane & 3);
+        // a weight far below 1 may underflow although its part of the denominator,
+        // 2^-E_j as large, does not: then that is formed by itself
+        const bool apart = __any_sync(0xffffffffu, under < -100.0f);
+        const float inv[2] = {pow2f(-int(er[0])), pow2f(-int(er[1]))};
+        if (apart) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            sum[2 * (k >> 2) + (k & 1)] += ex2(x[k] - m[2 * (k >> 2) + (k & 1)] - er[(k >> 1) & 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int row = 0; row < 2; ++row) {
+            const float w0 = ex2(x[4 * j + 2 * row] - m[2 * j]), w1 = ex2(x[4 * j + 2 * row + 1] - m[2 * j + 1]);
+            if (!apart) {
+              sum[2 * j] = fmaf(w0, inv[row], sum[2 * j]);
+              sum[2 * j + 1] = fmaf(w1, inv[row], sum[2 * j + 1]);
+            }
+            const int rr = r0 + 8 * row;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(pa + uint32_t(rr) * 128u +
+                                                        (uint32_t((4 * half + j) ^ (rr & 7)) << 4)),
+                         "r"(half2_bits(w0, w1))
+                         : "memory");
+          }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[b]));
+    }
+    // ---- the unit's share is done: sums over the rows, then the output ------------------
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+    }
+    named_bar_sync(kBarX, kXThreads);  // the last readers of red, mh and hinv are done
+    if (busy && lane < 4) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int h = hb + 8 * (k >> 1) + (k & 1);
+        sm.red[qd][h] = sum[k];
+        if (qd == 0) sm.mh[h] = m[k];
+      }
+    }
+    named_bar_sync(kBarX, kXThreads);
+    const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
+    const int heads = min(g.group, a.n_heads - h0);
+    const bool whole = w.off == 0 && w.i1 - w.i0 == w.tiles;
+    const int part = 2 * int(blockIdx.x) + (w.off == 0 ? 1 : 0);
+    if (xt < g.n_cols) {
+      const float tot = (sm.red[0][xt] + sm.red[1][xt]) + (sm.red[2][xt] + sm.red[3][xt]);
+      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) : 0.0f;
+      const float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
+      if (xt < heads) {
+        if (!whole)
+          parts->lse2[part][xt] = l2;
+        else if (a.lse != nullptr)
+          a.lse[int64_t(t) * a.n_heads + h0 + xt] = l2 * 0.6931471805599453f;
+      }
+    }
+    if (xt == 0 && !whole) parts->unit[part] = w.unit;
+    named_bar_sync(kBarX, kXThreads);
+    wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1], ((w.i1 - 1) >> 1) & 1, hdr);
+    tc_fence_after();
+    if (busy) {
+#pragma unroll 1
+      for (int k = 0; k < 2 * kDim / 128; ++k) {
+        uint32_t o[16];
+        const int hc = 32 * half + 16 * (k & 1);  // heads hc .. hc + 15
+        const int d = 128 * (k >> 1) + 32 * qd + lane;
+        tc_ld_x16(tmem + lane_base + kOCol + 64u * (k >> 1) + uint32_t(hc), o);
+        tc_wait_ld();
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = __uint_as_float(o[u]) * sm.hinv[hc + u];
+        if (!whole) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u)
+            if (hc + u < heads) parts->o[part][hc + u][d] = v[u];
+        } else {
+          // neighbouring lanes swap one of two heads, so each stores two dims of one head
+          uint16_t *out = a.out + int64_t(t) * a.out_stride + int64_t(h0) * kDim;
+          const int odd = lane & 1;
+#pragma unroll
+          for (int u = 0; u < 16; u += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[u] : v[u + 1], 1);
+            const __nv_bfloat162 pr =
+                odd ? __floats2bfloat162_rn(got, v[u + 1]) : __floats2bfloat162_rn(v[u], got);
+            const int h = hc + u + odd;
+            if (h < heads) *reinterpret_cast<__nv_bfloat162 *>(out + h * kDim + (d & ~1)) = pr;
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    if (w.i1 >= total) break;
+    w.next(g, total);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *__restrict__ parts,
+                                                                 WsHeader *__restrict__ hdr) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sm.vfull[b]), kWWarps / 2);
+      mbar_init(smem_u32(&sm.sfull[b]), 1);
+      mbar_init(smem_u32(&sm.pfull[b]), kXWarps);
+      mbar_init(smem_u32(&sm.pvdone[b]), 1);
+    }
+    mbar_init(smem_u32(&sm.qfull), kWWarps);
+    mbar_init(smem_u32(&sm.qfree), 1);
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort_flag = 0;
+    sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWWarps + kXWarps) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  // Launched as a programmatic dependent: nothing above touches global memory.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < 2) parts->unit[2 * blockIdx.x + tid] = -1;
+  tc_fence_before();
+  find_cuts(g, sm, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const long long run = sm.cut1 - sm.cut0;
+  if (run > INT32_MAX && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  const int total = int(min(run, (long long)(INT32_MAX - 8)));
+  if (total > 0) {
+    if (warp < kWWarps) {
+      role_w(g, sm, total, hdr);
+    } else if (warp < kWWarps + kXWarps) {
+      role_x(g, sm, tmem, total, parts, hdr);
+    } else {
+      if ((tid & 31) == 0) role_m(g, sm, tmem, total, hdr);
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWWarps + kXWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that several CTAs share: an item is a unit's
+// head and 128 dims; four groups of 128 threads take the parts in turn, summed
+// in a fixed order.
+constexpr int kJoinDims = 128, kJoinGroups = 4, kJoinThreads = kJoinDims * kJoinGroups;
+
+__global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(Args g, const Parts *__restrict__ parts, int ctas) {
+  __shared__ int unit[2 * kMaxCtas];
+  __shared__ int first[kMaxCtas], n_first;  // the CTAs that begin a shared unit
+  __shared__ float wt[kMaxCtas + 1], osum[kJoinGroups][kJoinDims], lsum;
+  const int tid = threadIdx.x, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = tid; i < 2 * ctas; i += kJoinThreads) unit[i] = __ldcg(parts->unit + i);
+  __syncthreads();
+  if (tid < 32) {
+    int n = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const bool is = c0 + lane < ctas && unit[2 * (c0 + lane) + 1] >= 0;
+      const uint32_t b = __ballot_sync(0xffffffffu, is);
+      if (is) first[n + __popc(b & ((1u << lane) - 1))] = c0 + lane;
+      n += __popc(b);
+    }
+    if (lane == 0) n_first = n;
+  }
+  __syncthreads();
+  constexpr int kQuarters = kDim / kJoinDims;
+  for (int item = blockIdx.x; item < n_first * kHeads * kQuarters; item += gridDim.x) {
+    const int c0 = first[item / (kHeads * kQuarters)], h = item / kQuarters % kHeads, q = item % kQuarters;
+    const int u = unit[2 * c0 + 1];
+    const int t = u / g.groups, h0 = (u % g.groups) * g.group;
+    if (h >= min(g.group, g.a.n_heads - h0)) continue;
+    int n = 1;  // parts: c0's 2 c0 + 1, then 2 c of the CTAs behind it
+    while (c0 + n < ctas && unit[2 * (c0 + n)] == u) ++n;
+    auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+    if (tid < 32) {
+      float m = -INFINITY;
+      for (int k = lane; k < n; k += 32) m = fmaxf(m, wt[k] = __ldcg(&parts->lse2[slot(k)][h]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float s = 0.0f;
+      for (int k = lane; k < n; k += 32) {
+        const float e = wt[k] == -INFINITY ? 0.0f : exp2f(wt[k] - m);
+        wt[k] = e;
+        s += e;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) {
+        lsum = s;
+        if (q == 0 && g.a.lse != nullptr)
+          g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+      }
     }
     __syncthreads();
-    for (int j = 0; j < kTile && j0 + j < n; ++j) {
-      if (!sm.ok[j]) continue;
-      float v[16], d = 0.0f;
+    const int dd = tid % kJoinDims, gr = tid / kJoinDims, d = kJoinDims * q + dd;
+    float o = 0.0f;
+    int k = gr;
+    for (; k + 7 * kJoinGroups < n; k += 8 * kJoinGroups) {
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[i] = sm.v[j][32 * i + lane];
-        d = fmaf(q[i], v[i], d);
-      }
+      for (int e = 0; e < 8; ++e) v[e] = __ldcg(&parts->o[slot(k + e * kJoinGroups)][h][d]);
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
-      const float l = d * a.scale, mn = fmaxf(m, l);
-      const float al = expf(m - mn), p = expf(l - mn);
-      m = mn;
-      sum = fmaf(sum, al, p);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], al, p * v[i]);
+      for (int e = 0; e < 8; ++e) o = fmaf(wt[k + e * kJoinGroups], v[e], o);
     }
+    for (; k < n; k += kJoinGroups) o = fmaf(wt[k], __ldcg(&parts->o[slot(k)][h][d]), o);
+    osum[gr][dd] = o;
+    __syncthreads();
+    if (gr == 0) {
+      const float tot = (osum[0][dd] + osum[1][dd]) + (osum[2][dd] + osum[3][dd]);
+      g.a.out[int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d] =
+          __bfloat16_as_ushort(__float2bfloat16_rn(lsum > 0.0f ? tot / lsum : 0.0f));
+    }
+    __syncthreads();
   }
-  if (h >= a.n_heads) return;
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    a.out[t * a.out_stride + h * DS4X_KV_DIM + 32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-  if (lane == 0 && a.lse != nullptr) a.lse[int64_t(t) * a.n_heads + h] = sum > 0.0f ? m + logf(sum) : -INFINITY;
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes() { return kWsHeaderBytes; }
+size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts); }
 
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  const int smem = int(sizeof(Smem));
+  // the dynamic shared memory is at least 16-byte aligned: room to round it up to 1024
+  const int smem = int(sizeof(Smem)) + 1024 - 16;
   cudaError_t e = set_max_smem_once(paged_attn_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(a.n_tokens), unsigned((a.n_heads + kHeadsCta - 1) / kHeadsCta));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel, a, reinterpret_cast<WsHeader *>(ws));
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0};
+  g.group = (a.n_heads + g.groups - 1) / g.groups;
+  g.n_cols = (g.group + 15) / 16 * 16;
+  // no more CTAs than there can be tiles
+  const int64_t rows = a.idx != nullptr ? a.k : int64_t(a.c.seq_pages) << a.c.page_log2;
+  const int64_t most = int64_t(a.n_tokens) * g.groups * ((rows + kTile - 1) / kTile);
+  const int ctas = int(most < sms ? most : sms) < kMaxCtas ? int(most < sms ? most : sms) : kMaxCtas;
+  WsHeader *hdr = static_cast<WsHeader *>(ws);
+  Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
+  e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_combine_kernel, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
+                    static_cast<const Parts *>(parts), ctas);
 }
 
 }  // namespace ds4x
