@@ -18,7 +18,7 @@
 // Exact operands.  Row j's exponent E_j is its RoPE part's, the row's largest:
 // V'_j = v_j 2^-E_j, at most 8, is exact in fp16 while a block's scale lies
 // within 2^14 of 2^E_j (smaller blocks round at 2^-25 of 2^E_j); the RoPE part's
-// fp16 values are V' as they are.  Q' = q 2^c in fp16, c taking the unit's
+// fp16 values are V' as they are.  Q'_h = q_h 2^c_h in fp16, c_h taking the head's
 // largest |q| into [2^14, 2^15): a bf16 value is exact down to 2^-32 of it.
 //
 // Softmax in the log2 domain, online, with the row's exponent kept apart:
@@ -37,13 +37,14 @@
 // log-sum-exp, and paged_combine_kernel joins them in a fixed order.  The cuts
 // depend on the lengths alone, so results do not depend on timing.
 //
-// Roles (25 warps).  W (warps 0-15): two groups of 8 warps take the tiles in
-// turn, each with its own V' buffer, and load their next tile's 16-byte words
-// into registers as soon as the last is widened (two tiles are in flight); both
-// convert Q' when a unit begins.  X (16-23): the softmax, four 16-row quarters
-// of S^T by two halves of the heads, and the unit's output.  M (24): one thread
-// issues the products, S of two tiles, then O of the two: while one tile's
-// products run the other is widened or in its softmax.
+// Roles (20 warps: registers are handed out to warps by fours).  L (warps 0-1):
+// finds the rows of the tiles to come (list entry, page table), four tiles
+// ahead.  W (4-11): widens the tiles into two V' buffers in turn, with the 16-byte
+// words of the next two tiles on their way into registers meanwhile.  X (12-19):
+// the softmax, four 16-row quarters of S^T by two halves of the heads; when a
+// unit ends, the next one's Q' first, then the output.  M (2): one thread issues
+// the products, S of two tiles, then O of the two: while one tile's products run
+// the other is widened or in its softmax.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
@@ -61,9 +62,11 @@ using namespace ptx;
 constexpr int kDim = DS4X_KV_DIM;  // 512
 constexpr int kTile = 64;          // rows a tile
 constexpr int kHeads = 64;         // heads a unit, at most
-constexpr int kWWarps = 16, kXWarps = 8;
-constexpr int kWThreads = 32 * kWWarps, kXThreads = 32 * kXWarps;
-constexpr int kThreads = kWThreads + kXThreads + 32;
+constexpr int kLWarps = 2, kMWarp = 2;               // warp 3 has no role
+constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 12, kXWarps = 8;
+constexpr int kXThreads = 32 * kXWarps;
+constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 640
+constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
 constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
@@ -72,19 +75,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 constexpr int kNoRow = INT32_MIN;  // rowe of a row that is not there
 constexpr float kNoMax = -3e38f;   // a head's maximum before its first row
-enum { kBarQ = 1, kBarX = 2 };     // named barriers
+enum { kBarX = 1 };               // named barrier
 
 struct __align__(1024) Smem {
   uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
   uint8_t v[2][kTile * kDim * 2];   // V': 8 panels of 8 KB, two tiles
   uint8_t p[2][kTile * kHeads * 2]; // P^T: one panel, two tiles
   int rowe[2][kTile];               // E_j, or kNoRow
+  int2 found[kAhead][kTile];        // a row's page (-1: no row) and its number there
   float red[4][kHeads];
   float alpha[kHeads];
   float mh[kHeads], hinv[kHeads];
-  float qbase[2];                   // scale log2 e 2^-c, by segment parity
-  uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
-  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2], qfull, qfree, drain;
+  float qbase[2][kHeads];           // scale log2 e 2^-c_h, by segment parity
+  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2], lfull[kAhead], lfree[kAhead], qfull, drain;
   long long scan[kThreads / 32];
   long long cut0, cut1;             // the CTA's run of tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
@@ -134,6 +137,15 @@ __device__ __forceinline__ void wait_bar(Smem &sm, unsigned long long *bar, uint
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// One lane of a converged warp, chosen so that the compiler knows the branch to
+// be one thread's: its MMA descriptors then stay in uniform registers (an issuer
+// picked by lane number took 78 cycles an MMA beside busy warps, this one 32).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // 16 lanes x 32 columns: register 4 j + 2 r + c of lane T holds lane T / 4 + 8 r,
@@ -215,19 +227,13 @@ struct Walk {
   }
 };
 
-// Where this lane's row of a tile lies.
-struct RowAt {
-  const uint8_t *page;  // null: no row
-  int at;
-};
-
 // ---- the cuts ------------------------------------------------------------------
 
 // The run of CTA c of g: unit0, off0, cut0, cut1.  All threads.
 __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   const PagedAttn &a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = max(0, min(a.n_tokens, __ldcg(a.c.cu + a.c.n_seqs)));
+  const int n = max(0, min(a.n_tokens, __ldcg(a.c.cu + a.c.n_seqs)));  // tokens behind are padding
   const int per = (n + kThreads - 1) / kThreads;
   const int t0 = min(n, tid * per), t1 = min(n, t0 + per);
   long long mine = 0;
@@ -292,39 +298,62 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   __syncthreads();
 }
 
-// ---- W: widening ----------------------------------------------------------------
+// ---- L: finding rows ------------------------------------------------------------
 
-// The row of a tile that this lane helps to widen: the tile's row `r` (0 .. 63).
-__device__ __forceinline__ RowAt find_row(const Args &g, const Walk &w, int seq, int64_t n_rows, int tile, int r,
-                                          WsHeader *hdr) {
+__device__ __forceinline__ void role_l(const Args &g, Smem &sm, int total, WsHeader *hdr) {
   const PagedAttn &a = g.a;
-  const int64_t pos = int64_t(tile) * kTile + r;
-  if (pos >= w.n || seq < 0) return RowAt{nullptr, 0};
-  int64_t row = w.r0 + pos;
-  if (a.idx != nullptr) {
-    row = __ldcg(a.idx + int64_t(w.unit / g.groups) * a.k + pos);
-    if (row == -1) return RowAt{nullptr, 0};
-    if (row >= n_rows) row = -2;
+  const int lane = threadIdx.x & 31, r = threadIdx.x;  // the tile's row that this lane finds
+  Walk w;
+  w.begin(g, sm, total);
+  for (;;) {
+    const int t = w.unit / g.groups;
+    const int seq = paged_seq_of(a.c, t, lane);
+    const int64_t n_rows = a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(a.n_rows + seq)) : 0;
+    for (int i = w.i0; i < w.i1; ++i) {
+      const int64_t pos = int64_t(w.off + (i - w.i0)) * kTile + r;
+      int2 at = make_int2(-1, 0);
+      if (pos < w.n && seq >= 0) {
+        int64_t row = w.r0 + pos;
+        if (a.idx != nullptr) {
+          row = __ldcg(a.idx + int64_t(t) * a.k + pos);
+          if (row >= n_rows) row = -2;
+        }
+        if (row != -1) {  // (-1: an entry that names no row; a range has none)
+          const int64_t j = row >> a.c.page_log2;
+          if (row >= 0 && j < a.c.seq_pages) {
+            const int32_t page = __ldcg(a.c.table + int64_t(seq) * a.c.table_stride + j);
+            if (page >= 0 && page < a.c.n_pages) at = make_int2(page, int(row & ((1 << a.c.page_log2) - 1)));
+          }
+          if (at.x < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+        }
+      }
+      const int slot = i % kAhead;
+      if (i >= kAhead) wait_bar(sm, &sm.lfree[slot], (i / kAhead - 1) & 1, hdr);
+      sm.found[slot][r] = at;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.lfull[slot]));
+    }
+    if (w.i1 >= total) break;
+    w.next(g, total);
   }
-  const PagedRow p = paged_row(a.c, seq, row);
-  if (p.page == nullptr) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-  return RowAt{p.page, p.at};
 }
 
-// This lane's 16-byte words of its row: three whole blocks' codes, half of the
+// ---- W: widening ----------------------------------------------------------------
+
+// A lane's 16-byte words of its row: three whole blocks' codes, half of the
 // lanes one more, two of the RoPE part's eight, the scale record.
 struct Raw {
   uint4 c[4], t[2], sc;
   int ok;
 };
-__device__ __forceinline__ void load_raw(const PagedCache &c, const RowAt &r, int sub, Raw &w) {
+__device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int sub, Raw &w) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  w.ok = r.page != nullptr;
+  w.ok = at.x >= 0;
   if (w.ok) {
-    const PagedRow p{r.page, r.at};
-    const uint4 *co = reinterpret_cast<const uint4 *>(r.page + paged_code_off(p));
-    const uint4 *ta = reinterpret_cast<const uint4 *>(r.page + paged_tail_off(c, p));
-    w.sc = __ldcg(reinterpret_cast<const uint4 *>(r.page + paged_scale_off(c, p)));
+    const PagedRow p{c.pages + (int64_t(at.x) << c.page_log2) * DS4X_PAGED_ROW_BYTES, at.y};
+    const uint4 *co = reinterpret_cast<const uint4 *>(p.page + paged_code_off(p));
+    const uint4 *ta = reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p));
+    w.sc = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_scale_off(c, p)));
     w.c[0] = __ldcg(co + sub);
     w.c[1] = __ldcg(co + 4 + sub);
     w.c[2] = __ldcg(co + 8 + sub);
@@ -369,99 +398,33 @@ __device__ __forceinline__ void widen(Smem &sm, int buf, int r, int sub, const R
   if (sub == 0) sm.rowe[buf][r] = w.ok ? E - 127 : kNoRow;
 }
 
-// Q' of a unit: warp w converts heads 4 w .. 4 w + 3, lane L the 16-byte chunks
-// L and 32 + L of each; heads that the unit does not have are zeros.
-__device__ __forceinline__ void load_query(const Args &g, const Walk &w, int warp, int lane, uint4 (&qv)[8]) {
-  const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
-  const int heads = min(g.group, g.a.n_heads - h0);
-  const uint16_t *q = g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0) * kDim;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int h = 4 * warp + (i >> 1);
-    qv[i] = h < heads ? __ldcg(reinterpret_cast<const uint4 *>(q + h * kDim) + 32 * (i & 1) + lane) : make_uint4(0, 0, 0, 0);
-  }
-}
-
-__device__ __forceinline__ void convert_query(const Args &g, Smem &sm, int seg, int warp, int lane, const uint4 (&qv)[8],
-                                              WsHeader *hdr) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  const int slot = seg % 3;
-  if (lane == 0) atomicMax(&sm.qmax[slot], m);
-  // the next unit's slot: its last readers (three units ago) passed the previous barrier
-  if (threadIdx.x == 0) sm.qmax[(seg + 1) % 3] = 0;
-  named_bar_sync(kBarQ, kWThreads);
-  const int e = int(*reinterpret_cast<volatile uint32_t *>(&sm.qmax[slot]) >> 7);  // the largest exponent field
-  const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
-  const float f = pow2f(c);
-  // the previous unit's last first product is done (so is the softmax of the unit before it, qbase's last reader)
-  if (seg > 0) wait_bar(sm, &sm.qfree, (seg - 1) & 1, hdr);
-  if (threadIdx.x == 0) sm.qbase[seg & 1] = g.a.scale * kLog2e * pow2f(-c);
-  const uint32_t qa = smem_u32(sm.q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int h = 4 * warp + (i >> 1), C = 32 * (i & 1) + lane;
-    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-    uint32_t o[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
-    sts16(qa + uint32_t(C >> 3) * 8192u + uint32_t(h) * 128u + (uint32_t((C & 7) ^ (h & 7)) << 4), o[0], o[1], o[2],
-          o[3]);
-  }
-}
-
 __device__ __forceinline__ void role_w(const Args &g, Smem &sm, int total, WsHeader *hdr) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int buf = warp >> 3;                  // the group and its V' buffer
-  const int r = 8 * (warp & 7) + (lane & 7);  // the tile's row that this lane helps to widen
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
+  const int r = 8 * warp + (lane & 7);  // the tile's row that this lane helps to widen
   const int sub = lane >> 3;
-  // the look-ahead: the walk two tiles on
-  Walk la;
-  la.begin(g, sm, total);
-  int seq = paged_seq_of(g.a.c, la.unit / g.groups, lane);
-  int64_t n_rows = g.a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(g.a.n_rows + seq)) : 0;
-  auto look = [&](int i) {  // the lane's row of tile i
-    if (i >= total) return RowAt{nullptr, 0};
-    while (i >= la.i1) {
-      la.next(g, total);
-      seq = paged_seq_of(g.a.c, la.unit / g.groups, lane);
-      n_rows = g.a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(g.a.n_rows + seq)) : 0;
-    }
-    return find_row(g, la, seq, n_rows, la.off + (i - la.i0), r, hdr);
+  auto load = [&](int i, Raw &w) {
+    if (i >= total) return;
+    const int slot = i % kAhead;
+    wait_bar(sm, &sm.lfull[slot], (i / kAhead) & 1, hdr);
+    const int2 at = sm.found[slot][r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.lfree[slot]));
+    load_raw(g.a.c, at, sub, w);
   };
-  Raw raw;
-  int i = buf;
-  load_raw(g.a.c, look(i), sub, raw);
-  RowAt next = look(i + 2);
-  Walk w;
-  w.begin(g, sm, total);
-  for (int seg = 0;; ++seg) {
-    {
-      uint4 qv[8];
-      load_query(g, w, warp, lane, qv);
-      convert_query(g, sm, seg, warp, lane, qv, hdr);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
-    }
-    for (; i < w.i1; i += 2) {
-      if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
-      widen(sm, buf, r, sub, raw);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
-      load_raw(g.a.c, next, sub, raw);
-      next = look(i + 4);
-    }
-    if (w.i1 >= total) break;
-    w.next(g, total);
+  auto tile = [&](int i, int buf, Raw &w) {
+    if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
+    widen(sm, buf, r, sub, w);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
+    load(i + 2, w);
+  };
+  Raw raw[2];
+  load(0, raw[0]);
+  load(1, raw[1]);
+  for (int i = 0; i < total; i += 2) {
+    tile(i, 0, raw[0]);
+    if (i + 1 < total) tile(i + 1, 1, raw[1]);
   }
 }
 
@@ -485,7 +448,6 @@ __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, i
       mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)),
                  dS_b + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)), idS, ks > 0 ? 1u : 0u);
     tc_commit(smem_u32(&sm.sfull[b]));
-    if (i + 1 == w.i1) tc_commit(smem_u32(&sm.qfree));
   };
   auto issue_o = [&](int i) {
     const int b = i & 1;
@@ -519,25 +481,82 @@ __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, i
 
 // ---- X: softmax and output ------------------------------------------------------------
 
+// Q' of a unit: warp w of X converts heads 8 w .. 8 w + 7 in two batches, lane L
+// the 16-byte chunks L and 32 + L of each; heads that the unit does not have are
+// zeros.
+__device__ __forceinline__ void load_query(const Args &g, int unit, int h4, int lane, uint4 (&qv)[8]) {
+  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
+  const int heads = min(g.group, g.a.n_heads - h0);
+  const uint16_t *q = g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0) * kDim;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int h = h4 + (i >> 1);
+    qv[i] = h < heads ? __ldcg(reinterpret_cast<const uint4 *>(q + h * kDim) + 32 * (i & 1) + lane) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void convert_query(const Args &g, Smem &sm, int seg, int h4, int lane,
+                                              const uint4 (&qv)[8]) {
+  const uint32_t qa = smem_u32(sm.q);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // head h4 + k
+    const uint32_t w8[8] = {qv[2 * k].x,     qv[2 * k].y,     qv[2 * k].z,     qv[2 * k].w,
+                            qv[2 * k + 1].x, qv[2 * k + 1].y, qv[2 * k + 1].z, qv[2 * k + 1].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m = max(m, max(w8[u] & 0x7fffu, (w8[u] >> 16) & 0x7fffu));
+    const int e = int(__reduce_max_sync(0xffffffffu, m) >> 7);  // the largest exponent field
+    const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
+    const float f = pow2f(c);
+    const int h = h4 + k;
+    if (lane == 0) sm.qbase[seg & 1][h] = g.a.scale * kLog2e * pow2f(-c);
+    uint32_t o[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      o[u] = half2_bits(__uint_as_float(w8[u] << 16) * f, __uint_as_float(w8[u] & 0xffff0000u) * f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int C = 32 * i + lane;
+      sts16(qa + uint32_t(C >> 3) * 8192u + uint32_t(h) * 128u + (uint32_t((C & 7) ^ (h & 7)) << 4), o[4 * i],
+            o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+  }
+}
+
+__device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, int seg, int xw, int lane) {
+  uint4 qa[8], qb[8];
+  load_query(g, unit, 8 * xw, lane, qa);
+  load_query(g, unit, 8 * xw + 4, lane, qb);
+  convert_query(g, sm, seg, 8 * xw, lane, qa);
+  convert_query(g, sm, seg, 8 * xw + 4, lane, qb);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
+}
+
 __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, int total, Parts *parts, WsHeader *hdr) {
   const PagedAttn &a = g.a;
-  const int lane = threadIdx.x & 31, xw = (threadIdx.x >> 5) - kWWarps, xt = threadIdx.x - kWThreads;
+  const int lane = threadIdx.x & 31, xw = (threadIdx.x >> 5) - kXWarp0, xt = threadIdx.x - 32 * kXWarp0;
   const int qd = xw & 3, half = xw >> 2;        // tile rows 16 qd .., heads 32 half ..
   const bool busy = 32 * half < g.n_cols;
   const int r0 = 16 * qd + (lane >> 2);         // this lane's rows r0 and r0 + 8
   const int hb = 32 * half + 2 * (lane & 3);    // this lane's heads hb + 8 j + c
   const uint32_t lane_base = uint32_t(32 * qd) << 16;
+  make_query(g, sm, sm.unit0, 0, xw, lane);
   Walk w;
   w.begin(g, sm, total);
   for (int seg = 0;; ++seg) {
-    float m[8], sum[8];
+    float m[8], sum[8], base[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) m[k] = kNoMax, sum[k] = 0.0f;
     for (int i = w.i0; i < w.i1; ++i) {
       const int b = i & 1;
       wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
       tc_fence_after();
-      const float base = sm.qbase[seg & 1];
+      if (i == w.i0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) base[k] = sm.qbase[seg & 1][hb + 8 * (k >> 1) + (k & 1)];
+      }
       float x[16], er[2];  // x[4 j + 2 row + c]; the rows' E_j
       float over = -INFINITY, under = 0.0f;
       if (busy) {
@@ -545,15 +564,16 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
         tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
         const int e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
         // a row that is not there: x = -inf, weight 0
-        const float f[2] = {e0 == kNoRow ? 0.0f : base * pow2f(e0), e1 == kNoRow ? 0.0f : base * pow2f(e1)};
+        const float f[2] = {e0 == kNoRow ? 0.0f : pow2f(e0), e1 == kNoRow ? 0.0f : pow2f(e1)};
         const float ef[2] = {e0 == kNoRow ? -INFINITY : float(e0), e1 == kNoRow ? -INFINITY : float(e1)};
         er[0] = e0 == kNoRow ? 0.0f : float(e0);
         er[1] = e1 == kNoRow ? 0.0f : float(e1);
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          x[k] = fmaf(__uint_as_float(s[k]), f[(k >> 1) & 1], ef[(k >> 1) & 1]);
-          const float d = x[k] - m[2 * (k >> 2) + (k & 1)];
+          const int h = 2 * (k >> 2) + (k & 1);
+          x[k] = fmaf(__uint_as_float(s[k]), base[h] * f[(k >> 1) & 1], ef[(k >> 1) & 1]);
+          const float d = x[k] - m[h];
           over = fmaxf(over, d);
           under = fminf(under, d);
         }
@@ -640,7 +660,10 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[b]));
     }
-    // ---- the unit's share is done: sums over the rows, then the output ------------------
+    // ---- the unit's share is done -------------------------------------------------------
+    // the next unit's Q' (this one's last first product is done: its softmax is)
+    if (w.i1 < total) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
+    // sums over the rows, then the output
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
 #pragma unroll
@@ -718,19 +741,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&sm.vfull[b]), kWWarps / 2);
+      mbar_init(smem_u32(&sm.vfull[b]), kWWarps);
       mbar_init(smem_u32(&sm.sfull[b]), 1);
       mbar_init(smem_u32(&sm.pfull[b]), kXWarps);
       mbar_init(smem_u32(&sm.pvdone[b]), 1);
     }
-    mbar_init(smem_u32(&sm.qfull), kWWarps);
-    mbar_init(smem_u32(&sm.qfree), 1);
+    for (int k = 0; k < kAhead; ++k) {
+      mbar_init(smem_u32(&sm.lfull[k]), kLWarps);
+      mbar_init(smem_u32(&sm.lfree[k]), kWWarps);
+    }
+    mbar_init(smem_u32(&sm.qfull), kXWarps);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
-    sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
     fence_mbar_init();
   }
-  if (warp == kWWarps + kXWarps) {
+  if (warp == kMWarp) {
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
@@ -746,18 +771,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   if (run > INT32_MAX && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   const int total = int(min(run, (long long)(INT32_MAX - 8)));
   if (total > 0) {
-    if (warp < kWWarps) {
-      role_w(g, sm, total, hdr);
-    } else if (warp < kWWarps + kXWarps) {
+    if (warp >= kXWarp0) {
       role_x(g, sm, tmem, total, parts, hdr);
-    } else {
-      if ((tid & 31) == 0) role_m(g, sm, tmem, total, hdr);
+    } else if (warp >= kWWarp0) {
+      role_w(g, sm, total, hdr);
+    } else if (warp < kLWarps) {
+      role_l(g, sm, total, hdr);
+    } else if (warp == kMWarp) {
+      if (elect_one()) role_m(g, sm, tmem, total, hdr);
       __syncwarp();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWWarps + kXWarps) {
+  if (warp == kMWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
