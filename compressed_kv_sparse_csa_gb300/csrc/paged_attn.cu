@@ -12,13 +12,14 @@
 //   O^T[512 dims][heads] += V'^T[512][64 rows] . P^T[64 rows][heads]
 //
 // V' is the tile's rows widened once to fp16, in shared memory, as eight
-// 128-byte-swizzled panels of 64 dims (16-byte chunk c of row r at c ^ (r % 8)):
-// the first product reads them K-major, the second the same bytes MN-major.
+// 128-byte-swizzled panels of 64 dims (16-byte chunk c of row r at c ^ (r % 8); which
+// dims, see v_chunk): the first product reads them K-major, the second the same
+// bytes MN-major.
 //
 // Exact operands.  Row j's exponent E_j is its RoPE part's, the row's largest:
 // V'_j = v_j 2^-E_j, at most 8, is exact in fp16 while a block's scale lies
 // within 2^14 of 2^E_j (smaller blocks round at 2^-25 of 2^E_j); the RoPE part's
-// fp16 values are V' as they are.  Q'_h = q_h 2^c_h in fp16, c_h taking the head's
+// fp16 values are V' as they are.  Q' = q 2^c in fp16, c taking the unit's
 // largest |q| into [2^14, 2^15): a bf16 value is exact down to 2^-32 of it.
 //
 // Softmax in the log2 domain, online, with the row's exponent kept apart:
@@ -37,14 +38,16 @@
 // log-sum-exp, and paged_combine_kernel joins them in a fixed order.  The cuts
 // depend on the lengths alone, so results do not depend on timing.
 //
-// Roles (20 warps: registers are handed out to warps by fours).  L (warps 0-1):
-// finds the rows of the tiles to come (list entry, page table), four tiles
-// ahead.  W (4-11): widens the tiles into two V' buffers in turn, with the 16-byte
-// words of the next two tiles on their way into registers meanwhile.  X (12-19):
-// the softmax, four 16-row quarters of S^T by two halves of the heads; when a
-// unit ends, the next one's Q' first, then the output.  M (2): one thread issues
-// the products, S of two tiles, then O of the two: while one tile's products run
-// the other is widened or in its softmax.
+// Roles (28 warps).  L (warps 0-1): finds the rows of the tiles to come (list
+// entry, page table), four tiles ahead.  W (4-19): two groups of 8 warps widen the
+// tiles in turn, each into its own V' buffer, with the 16-byte words of its next
+// tile on their way into registers meanwhile.  (One group with the words of two
+// tiles in flight waits for the newer ones too: a load's scoreboard counts both.)
+// X (20-27): the softmax, four 16-row quarters of S^T by two halves of the heads;
+// when a unit ends, the next one's Q' first, then the output.  M (2): one thread
+// issues the products, S of two tiles, then O of the two: while one tile's products
+// run the other is widened or in its softmax.  Registers go from L, M and W to X
+// (setmaxnreg): the softmax must not spill, because local loads queue behind W's.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
@@ -63,9 +66,12 @@ constexpr int kDim = DS4X_KV_DIM;  // 512
 constexpr int kTile = 64;          // rows a tile
 constexpr int kHeads = 64;         // heads a unit, at most
 constexpr int kLWarps = 2, kMWarp = 2;               // warp 3 has no role
-constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 12, kXWarps = 8;
+constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 20, kXWarps = 8;  // W: kWWarps a group, two groups
 constexpr int kXThreads = 32 * kXWarps;
-constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 640
+constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 896
+// registers a thread: at launch, then by role
+constexpr int kRegs = 72, kRegsLM = 56, kRegsW = 64, kRegsX = 96;
+static_assert(4 * kRegsLM + 2 * kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
@@ -74,7 +80,6 @@ constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 constexpr int kNoRow = INT32_MIN;  // rowe of a row that is not there
-constexpr float kNoMax = -3e38f;   // a head's maximum before its first row
 enum { kBarX = 1 };               // named barrier
 
 struct __align__(1024) Smem {
@@ -86,7 +91,8 @@ struct __align__(1024) Smem {
   float red[4][kHeads];
   float alpha[kHeads];
   float mh[kHeads], hinv[kHeads];
-  float qbase[2][kHeads];           // scale log2 e 2^-c_h, by segment parity
+  float qbase[2];                   // scale log2 e 2^-c, by segment parity
+  uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
   unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2], lfull[kAhead], lfree[kAhead], qfull, drain;
   long long scan[kThreads / 32];
   long long cut0, cut1;             // the CTA's run of tiles
@@ -139,6 +145,16 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// Registers a thread of this warpgroup from here on (all four warps).
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // One lane of a converged warp, chosen so that the compiler knows the branch to
 // be one thread's: its MMA descriptors then stay in uniform registers (an issuer
 // picked by lane number took 78 cycles an MMA beside busy warps, this one 32).
@@ -178,9 +194,6 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // A token's rows: n of them, from row r0 of its sequence (or of its list).
@@ -340,95 +353,108 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, int total, WsHea
 
 // ---- W: widening ----------------------------------------------------------------
 
-// A lane's 16-byte words of its row: three whole blocks' codes, half of the
-// lanes one more, two of the RoPE part's eight, the scale record.
+// Eight lanes (a quarter-warp) take a row at a time, so that each of its loads is
+// a row's 128 consecutive bytes: lane l of them the codes of block l, those of
+// block 8 + l (l < 6) and chunk l of the RoPE part.  (Eight lanes on eight rows
+// took 21 passes of the load pipe an instruction instead of 4 to 8.)  To store a
+// block's words without bank conflicts the chunks of 8 values are dealt to V''s
+// panels by word, not by block: word u of block b < 8 is chunk b of panel u; word u
+// of block 8 + l is number l + 6 u of the 24 chunks of panels 4 to 6; the RoPE part
+// is panel 7.  Q' is laid out alike, and the output's dims are put back.
+__device__ __forceinline__ int v_chunk(int C) {  // where chunk C (values 8 C ..) lies: 8 panel + chunk
+  if (C < 32) return 8 * (C & 3) + (C >> 2);
+  if (C < 56) return 32 + ((C - 32) >> 2) + 6 * (C & 3);
+  return C;
+}
+__device__ __forceinline__ int v_chunk_back(int P) {  // the C of place P
+  if (P < 32) return 4 * (P & 7) + (P >> 3);
+  if (P < 56) return 32 + 4 * ((P - 32) % 6) + (P - 32) / 6;
+  return P;
+}
+
 struct Raw {
-  uint4 c[4], t[2], sc;
+  uint4 a, b, t, sc;
   int ok;
 };
-__device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int sub, Raw &w) {
+__device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int l, Raw &w) {
   const uint4 z = make_uint4(0, 0, 0, 0);
   w.ok = at.x >= 0;
   if (w.ok) {
     const PagedRow p{c.pages + (int64_t(at.x) << c.page_log2) * DS4X_PAGED_ROW_BYTES, at.y};
-    const uint4 *co = reinterpret_cast<const uint4 *>(p.page + paged_code_off(p));
-    const uint4 *ta = reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p));
+    const uint4 *co = reinterpret_cast<const uint4 *>(p.page + paged_code_off(p)) + l;
     w.sc = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_scale_off(c, p)));
-    w.c[0] = __ldcg(co + sub);
-    w.c[1] = __ldcg(co + 4 + sub);
-    w.c[2] = __ldcg(co + 8 + sub);
-    w.c[3] = sub < 2 ? __ldcg(co + 12 + sub) : z;
-    w.t[0] = __ldcg(ta + sub);
-    w.t[1] = __ldcg(ta + 4 + sub);
+    w.a = __ldcg(co);
+    w.b = l < 6 ? __ldcg(co + 8) : z;
+    w.t = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p)) + l);
   } else {
-    w.sc = w.c[0] = w.c[1] = w.c[2] = w.c[3] = w.t[0] = w.t[1] = z;
+    w.sc = w.a = w.b = w.t = z;
   }
 }
 
-// Block b of row r: 32 codes times 2^(scale - E) to V'.
-__device__ __forceinline__ void widen_block(uint32_t v, int r, int b, const uint4 &c, int d) {
-  const uint32_t f = pow2_half_bits(d) * 0x10001u;
-  const uint32_t base = v + uint32_t(b >> 1) * 8192u + uint32_t(r) * 128u;
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    uint32_t h0, h1, h2, h3;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
-        : "r"(w[u]));
-    sts16(base + (uint32_t(((b & 1) * 4 + u) ^ (r & 7)) << 4), hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f),
-          hmul2_bits(h3, f));
-  }
+// Eight codes times the factor pair f, as fp16.
+__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t f) {
+  uint32_t h0, h1, h2, h3;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+      : "r"(w));
+  return make_uint4(hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f), hmul2_bits(h3, f));
 }
-
-__device__ __forceinline__ void widen(Smem &sm, int buf, int r, int sub, const Raw &w) {
-  const uint32_t v = smem_u32(sm.v[buf]);
+__device__ __forceinline__ void widen(uint8_t *row, int r7, int l, const uint32_t (&off_b)[4], const Raw &w) {
   const int E = int((w.sc.w >> 16) & 0xffu);
-  const uint32_t sh = 8 * sub;
-  widen_block(v, r, sub, w.c[0], min(0, int((w.sc.x >> sh) & 0xffu) - E));
-  widen_block(v, r, 4 + sub, w.c[1], min(0, int((w.sc.y >> sh) & 0xffu) - E));
-  widen_block(v, r, 8 + sub, w.c[2], min(0, int((w.sc.z >> sh) & 0xffu) - E));
-  if (sub < 2) widen_block(v, r, 12 + sub, w.c[3], min(0, int((w.sc.w >> sh) & 0xffu) - E));
-  const uint32_t base = v + 7u * 8192u + uint32_t(r) * 128u;
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-    sts16(base + (uint32_t((4 * u + sub) ^ (r & 7)) << 4), w.t[u].x, w.t[u].y, w.t[u].z, w.t[u].w);
-  if (sub == 0) sm.rowe[buf][r] = w.ok ? E - 127 : kNoRow;
+  const uint32_t sh = 8 * (l & 3);
+  const uint32_t fa = pow2_half_bits(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> sh) & 0xffu) - E)) * 0x10001u;
+  uint8_t *pa = row + ((l ^ r7) << 4);
+  *reinterpret_cast<uint4 *>(pa) = widen8(w.a.x, fa);
+  *reinterpret_cast<uint4 *>(pa + 8192) = widen8(w.a.y, fa);
+  *reinterpret_cast<uint4 *>(pa + 2 * 8192) = widen8(w.a.z, fa);
+  *reinterpret_cast<uint4 *>(pa + 3 * 8192) = widen8(w.a.w, fa);
+  *reinterpret_cast<uint4 *>(pa + 7 * 8192) = w.t;
+  if (l < 6) {
+    const uint32_t fb = pow2_half_bits(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> sh) & 0xffu) - E)) * 0x10001u;
+    *reinterpret_cast<uint4 *>(row + (off_b[0] ^ (r7 << 4))) = widen8(w.b.x, fb);
+    *reinterpret_cast<uint4 *>(row + (off_b[1] ^ (r7 << 4))) = widen8(w.b.y, fb);
+    *reinterpret_cast<uint4 *>(row + (off_b[2] ^ (r7 << 4))) = widen8(w.b.z, fb);
+    *reinterpret_cast<uint4 *>(row + (off_b[3] ^ (r7 << 4))) = widen8(w.b.w, fb);
+  }
 }
 
 __device__ __forceinline__ void role_w(const Args &g, Smem &sm, int total, WsHeader *hdr) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
-  const int r = 8 * warp + (lane & 7);  // the tile's row that this lane helps to widen
-  const int sub = lane >> 3;
-  auto load = [&](int i, Raw &w) {
+  const int buf = warp / kWWarps;        // the group and its V' buffer
+  const int l = lane & 7, q = lane >> 3;
+  const int r = 8 * (warp % kWWarps) + q;  // the tile's rows that this lane helps to widen: r and r + 4
+  uint32_t off_b[4];                     // block 8 + l's words, within a row
+#pragma unroll
+  for (int u = 0; u < 4; ++u) off_b[u] = uint32_t(4 + ((l + 6 * u) >> 3)) * 8192u + (uint32_t((l + 6 * u) & 7) << 4);
+  Raw raw[2];
+  auto load = [&](int i) {
     if (i >= total) return;
     const int slot = i % kAhead;
     wait_bar(sm, &sm.lfull[slot], (i / kAhead) & 1, hdr);
-    const int2 at = sm.found[slot][r];
+    const int2 at0 = sm.found[slot][r], at1 = sm.found[slot][r + 4];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.lfree[slot]));
-    load_raw(g.a.c, at, sub, w);
+    load_raw(g.a.c, at0, l, raw[0]);
+    load_raw(g.a.c, at1, l, raw[1]);
   };
-  auto tile = [&](int i, int buf, Raw &w) {
+  uint8_t *row = sm.v[buf] + r * 128;
+  load(buf);
+  for (int i = buf; i < total; i += 2) {
     if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
-    widen(sm, buf, r, sub, w);
-    fence_proxy_async_smem();
+    widen(row, q, l, off_b, raw[0]);
+    widen(row + 4 * 128, q + 4, l, off_b, raw[1]);
+    if (l < 2) sm.rowe[buf][r + 4 * l] = (l ? raw[1].ok : raw[0].ok) ? int(((l ? raw[1].sc.w : raw[0].sc.w) >> 16) & 0xffu) - 127 : kNoRow;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
-    load(i + 2, w);
-  };
-  Raw raw[2];
-  load(0, raw[0]);
-  load(1, raw[1]);
-  for (int i = 0; i < total; i += 2) {
-    tile(i, 0, raw[0]);
-    if (i + 1 < total) tile(i + 1, 1, raw[1]);
+    load(i + 2);
   }
 }
 
-// ---- M: the products ---------------------------------------------------------------
+// ---- M: the products (and the proxy fence between what W and X stored and what the
+// tensor core reads: here, behind the barrier that orders their stores, because a
+// fence in W would wait for W's loads in flight) ---------------------------------------------------------------
 
 __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, int total, WsHeader *hdr) {
   const uint32_t q_a = smem_u32(sm.q), v_a = smem_u32(sm.v[0]), p_a = smem_u32(sm.p[0]);
@@ -440,6 +466,7 @@ __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, i
   auto issue_s = [&](int i) {
     const int b = i & 1;
     wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
+    fence_proxy_async_smem();
     tc_fence_after();
     const uint64_t dS_a = desc_sw128(v_a + 65536u * b, 16, 1024);
     // K step ks: 16 dims, 32 bytes into panel ks / 4 (descriptor addresses count 16 bytes)
@@ -452,6 +479,7 @@ __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, i
   auto issue_o = [&](int i) {
     const int b = i & 1;
     wait_bar(sm, &sm.pfull[b], (i >> 1) & 1, hdr);
+    fence_proxy_async_smem();
     tc_fence_after();
     const uint64_t dO_a = desc_sw128(v_a + 65536u * b, 8192, 1024), dO_b = desc_sw128(p_a + 8192u * b, 8192, 1024);
     const uint32_t acc = i > w.i0 ? 1u : 0u;
@@ -481,55 +509,57 @@ __device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, i
 
 // ---- X: softmax and output ------------------------------------------------------------
 
-// Q' of a unit: warp w of X converts heads 8 w .. 8 w + 7 in two batches, lane L
-// the 16-byte chunks L and 32 + L of each; heads that the unit does not have are
-// zeros.
-__device__ __forceinline__ void load_query(const Args &g, int unit, int h4, int lane, uint4 (&qv)[8]) {
-  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
-  const int heads = min(g.group, g.a.n_heads - h0);
-  const uint16_t *q = g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0) * kDim;
+// Q' of a unit: warp w of X converts heads 8 w .. 8 w + 7, lane L the 16-byte
+// chunks L and 32 + L of each; heads that the unit does not have are zeros.  Read
+// twice (for the largest value, then to convert: from L2), two heads at a time, so
+// that the unit's sums stay in registers meanwhile.
+__device__ __forceinline__ void load_query(const uint4 *q, int h, int heads, uint4 (&qv)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int h = h4 + (i >> 1);
-    qv[i] = h < heads ? __ldcg(reinterpret_cast<const uint4 *>(q + h * kDim) + 32 * (i & 1) + lane) : make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i) qv[i] = h + (i >> 1) < heads ? __ldcg(q + 64 * h + 32 * i) : make_uint4(0, 0, 0, 0);
 }
-
-__device__ __forceinline__ void convert_query(const Args &g, Smem &sm, int seg, int h4, int lane,
-                                              const uint4 (&qv)[8]) {
-  const uint32_t qa = smem_u32(sm.q);
+__device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, int seg, int xw, int lane) {
+  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
+  const int heads = min(g.group, g.a.n_heads - h0) - 8 * xw;  // of this warp's
+  const uint4 *q =
+      reinterpret_cast<const uint4 *>(g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0 + 8 * xw) * kDim) + lane;
+  uint32_t m = 0;
+#pragma unroll 2
+  for (int h = 0; h < 8; h += 2) {
+    uint4 qv[4];
+    load_query(q, h, heads, qv);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {  // head h4 + k
-    const uint32_t w8[8] = {qv[2 * k].x,     qv[2 * k].y,     qv[2 * k].z,     qv[2 * k].w,
-                            qv[2 * k + 1].x, qv[2 * k + 1].y, qv[2 * k + 1].z, qv[2 * k + 1].w};
-    uint32_t m = 0;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = max(m, max(w8[u] & 0x7fffu, (w8[u] >> 16) & 0x7fffu));
-    const int e = int(__reduce_max_sync(0xffffffffu, m) >> 7);  // the largest exponent field
-    const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
-    const float f = pow2f(c);
-    const int h = h4 + k;
-    if (lane == 0) sm.qbase[seg & 1][h] = g.a.scale * kLog2e * pow2f(-c);
-    uint32_t o[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      o[u] = half2_bits(__uint_as_float(w8[u] << 16) * f, __uint_as_float(w8[u] & 0xffff0000u) * f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int C = 32 * i + lane;
-      sts16(qa + uint32_t(C >> 3) * 8192u + uint32_t(h) * 128u + (uint32_t((C & 7) ^ (h & 7)) << 4), o[4 * i],
-            o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
     }
   }
-}
-
-__device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, int seg, int xw, int lane) {
-  uint4 qa[8], qb[8];
-  load_query(g, unit, 8 * xw, lane, qa);
-  load_query(g, unit, 8 * xw + 4, lane, qb);
-  convert_query(g, sm, seg, 8 * xw, lane, qa);
-  convert_query(g, sm, seg, 8 * xw + 4, lane, qb);
-  fence_proxy_async_smem();
+  m = __reduce_max_sync(0xffffffffu, m);
+  const int slot = seg % 3;
+  if (lane == 0) atomicMax(&sm.qmax[slot], m);
+  // the next unit's slot: its last readers (three units ago) passed the previous unit's barrier
+  if (xw == 0 && lane == 0) sm.qmax[(seg + 1) % 3] = 0;
+  named_bar_sync(kBarX, kXThreads);
+  const int e = int(*reinterpret_cast<volatile uint32_t *>(&sm.qmax[slot]) >> 7);  // the largest exponent field
+  const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
+  const float f = pow2f(c);
+  if (xw == 0 && lane == 0) sm.qbase[seg & 1] = g.a.scale * kLog2e * pow2f(-c);
+#pragma unroll 2
+  for (int h2 = 0; h2 < 8; h2 += 2) {
+    uint4 qv[4];
+    load_query(q, h2, heads, qv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = 8 * xw + h2 + (i >> 1), P = v_chunk(32 * (i & 1) + lane);
+      const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
+      *reinterpret_cast<uint4 *>(sm.q + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
 }
@@ -546,68 +576,66 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
   Walk w;
   w.begin(g, sm, total);
   for (int seg = 0;; ++seg) {
-    float m[8], sum[8], base[8];
+    float m[8], sum[8];  // head hb + 8 j + c: 2 j + c
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = kNoMax, sum[k] = 0.0f;
+    for (int k = 0; k < 8; ++k) m[k] = 0.0f, sum[k] = 0.0f;
+    float base = 0.0f;
+    bool fresh = busy;  // no row so far (a row is there for all heads or for none): m is 0 and not a maximum yet
     for (int i = w.i0; i < w.i1; ++i) {
       const int b = i & 1;
       wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
       tc_fence_after();
-      if (i == w.i0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) base[k] = sm.qbase[seg & 1][hb + 8 * (k >> 1) + (k & 1)];
-      }
-      float x[16], er[2];  // x[4 j + 2 row + c]; the rows' E_j
+      float d[16], er[2];  // x - m of row r0 + 8 r: d[4 j + 2 r + c]; the rows' E_j
       float over = -INFINITY, under = 0.0f;
+      if (i == w.i0) base = sm.qbase[seg & 1];
       if (busy) {
         uint32_t s[16];
         tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
         const int e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
         // a row that is not there: x = -inf, weight 0
-        const float f[2] = {e0 == kNoRow ? 0.0f : pow2f(e0), e1 == kNoRow ? 0.0f : pow2f(e1)};
+        const float f[2] = {e0 == kNoRow ? 0.0f : base * pow2f(e0), e1 == kNoRow ? 0.0f : base * pow2f(e1)};
         const float ef[2] = {e0 == kNoRow ? -INFINITY : float(e0), e1 == kNoRow ? -INFINITY : float(e1)};
         er[0] = e0 == kNoRow ? 0.0f : float(e0);
         er[1] = e1 == kNoRow ? 0.0f : float(e1);
         tc_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int h = 2 * (k >> 2) + (k & 1);
-          x[k] = fmaf(__uint_as_float(s[k]), base[h] * f[(k >> 1) & 1], ef[(k >> 1) & 1]);
-          const float d = x[k] - m[h];
-          over = fmaxf(over, d);
-          under = fminf(under, d);
+        for (int k = 0; k < 16; ++k)
+          d[k] = fmaf(__uint_as_float(s[k]), f[(k >> 1) & 1], ef[(k >> 1) & 1]) - m[2 * (k >> 2) + (k & 1)];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          over = fmaxf(fmaxf(over, d[k]), d[k + 1]);
+          under = fminf(fminf(under, d[k]), d[k + 1]);
         }
       }
-      if (named_bar_or(kBarX, kXThreads, over > kLazy)) {
+      if (named_bar_or(kBarX, kXThreads, over > kLazy || fresh)) {
         // some head's maximum moves: each head's maximum over the tile
         if (busy) {
-          float mx[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            mx[k] = fmaxf(x[4 * (k >> 1) + (k & 1)], x[4 * (k >> 1) + 2 + (k & 1)]);
+            float mx = fmaxf(d[4 * (k >> 1) + (k & 1)], d[4 * (k >> 1) + 2 + (k & 1)]);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane < 4) sm.red[qd][hb + 8 * (k >> 1) + (k & 1)] = mx;
           }
-          if (lane < 4)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sm.red[qd][hb + 8 * (k >> 1) + (k & 1)] = mx[k];
         }
         named_bar_sync(kBarX, kXThreads);
         if (busy) {
+          bool none = false;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int h = hb + 8 * (k >> 1) + (k & 1);
-            const float mt = fmaxf(fmaxf(sm.red[0][h], sm.red[1][h]), fmaxf(sm.red[2][h], sm.red[3][h]));
-            float al = 1.0f;
-            if (mt > m[k] + kLazy) {
-              al = ex2(m[k] - mt);  // 0 from kNoMax
-              const float half_al = ex2(0.5f * (m[k] - mt));  // (rows far apart in size: al itself may underflow)
-              sum[k] = sum[k] * half_al * half_al;
-              m[k] = mt;
-              under = -INFINITY;
-            }
-            if (qd == 0 && lane < 4) sm.alpha[h] = al;
+            float up = fmaxf(fmaxf(sm.red[0][h], sm.red[1][h]), fmaxf(sm.red[2][h], sm.red[3][h]));
+            none = up == -INFINITY;
+            if (none || !(fresh || up > kLazy)) up = 0.0f;
+            m[k] += up;
+            d[4 * (k >> 1) + (k & 1)] -= up;
+            d[4 * (k >> 1) + 2 + (k & 1)] -= up;
+            const float half_al = ex2(-0.5f * up);  // (rows far apart in size: 2^-up itself may underflow)
+            sum[k] = sum[k] * half_al * half_al;
+            if (qd == 0 && lane < 4) sm.alpha[h] = ex2(-up);
           }
+          fresh = fresh && none;
+          under = -INFINITY;
         }
         named_bar_sync(kBarX, kXThreads);
         if (i > w.i0 && busy) {
@@ -629,33 +657,28 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
         }
       }
       if (busy) {
-        const uint32_t pa = smem_u32(sm.p[b]) + 4u * (lane & 3);
         // a weight far below 1 may underflow although its part of the denominator,
         // 2^-E_j as large, does not: then that is formed by itself
         const bool apart = __any_sync(0xffffffffu, under < -100.0f);
-        const float inv[2] = {pow2f(-int(er[0])), pow2f(-int(er[1]))};
         if (apart) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            sum[2 * (k >> 2) + (k & 1)] += ex2(x[k] - m[2 * (k >> 2) + (k & 1)] - er[(k >> 1) & 1]);
+          for (int k = 0; k < 16; ++k) sum[2 * (k >> 2) + (k & 1)] += ex2(d[k] - er[(k >> 1) & 1]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int k = 0; k < 16; ++k) d[k] = ex2(d[k]);
+        if (!apart) {
+          const float inv[2] = {pow2f(-int(er[0])), pow2f(-int(er[1]))};
 #pragma unroll
-          for (int row = 0; row < 2; ++row) {
-            const float w0 = ex2(x[4 * j + 2 * row] - m[2 * j]), w1 = ex2(x[4 * j + 2 * row + 1] - m[2 * j + 1]);
-            if (!apart) {
-              sum[2 * j] = fmaf(w0, inv[row], sum[2 * j]);
-              sum[2 * j + 1] = fmaf(w1, inv[row], sum[2 * j + 1]);
-            }
-            const int rr = r0 + 8 * row;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(pa + uint32_t(rr) * 128u +
-                                                        (uint32_t((4 * half + j) ^ (rr & 7)) << 4)),
-                         "r"(half2_bits(w0, w1))
-                         : "memory");
-          }
+          for (int k = 0; k < 16; ++k)
+            sum[2 * (k >> 2) + (k & 1)] = fmaf(d[k], inv[(k >> 1) & 1], sum[2 * (k >> 2) + (k & 1)]);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const int rr = r0 + 8 * ((k >> 1) & 1);
+          *reinterpret_cast<uint32_t *>(sm.p[b] + rr * 128 + (((4 * half + (k >> 2)) ^ (rr & 7)) << 4) +
+                                        4 * (lane & 3)) = half2_bits(d[k], d[k + 1]);
+        }
       }
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[b]));
@@ -703,7 +726,7 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
       for (int k = 0; k < 2 * kDim / 128; ++k) {
         uint32_t o[16];
         const int hc = 32 * half + 16 * (k & 1);  // heads hc .. hc + 15
-        const int d = 128 * (k >> 1) + 32 * qd + lane;
+        const int d = 8 * v_chunk_back(16 * (k >> 1) + 4 * qd + (lane >> 3)) + (lane & 7);
         tc_ld_x16(tmem + lane_base + kOCol + 64u * (k >> 1) + uint32_t(hc), o);
         tc_wait_ld();
         float v[16];
@@ -753,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
     mbar_init(smem_u32(&sm.qfull), kXWarps);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
+    sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
     fence_mbar_init();
   }
   if (warp == kMWarp) {
@@ -772,14 +796,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   const int total = int(min(run, (long long)(INT32_MAX - 8)));
   if (total > 0) {
     if (warp >= kXWarp0) {
+      set_regs_up<kRegsX>();
       role_x(g, sm, tmem, total, parts, hdr);
     } else if (warp >= kWWarp0) {
+      set_regs_down<kRegsW>();
       role_w(g, sm, total, hdr);
-    } else if (warp < kLWarps) {
-      role_l(g, sm, total, hdr);
-    } else if (warp == kMWarp) {
-      if (elect_one()) role_m(g, sm, tmem, total, hdr);
-      __syncwarp();
+    } else {
+      set_regs_down<kRegsLM>();
+      if (warp < kLWarps) {
+        role_l(g, sm, total, hdr);
+      } else if (warp == kMWarp) {
+        if (elect_one()) role_m(g, sm, tmem, total, hdr);
+        __syncwarp();
+      }
     }
   }
   tc_fence_before();
