@@ -38,16 +38,17 @@
 // log-sum-exp, and paged_combine_kernel joins them in a fixed order.  The cuts
 // depend on the lengths alone, so results do not depend on timing.
 //
-// Roles (28 warps).  L (warps 0-1): finds the rows of the tiles to come (list
-// entry, page table), four tiles ahead.  W (4-19): two groups of 8 warps widen the
-// tiles in turn, each into its own V' buffer, with the 16-byte words of its next
-// tile on their way into registers meanwhile.  (One group with the words of two
-// tiles in flight waits for the newer ones too: a load's scoreboard counts both.)
+// Roles (28 warps).  L (warp 0): finds the rows of the tiles to come (list entry,
+// page table), four tiles ahead, and asks for them into L2.  W (4-19): widens the
+// tiles into two V' buffers in turn, with the 16-byte words of the next two tiles on
+// their way into registers meanwhile.
 // X (20-27): the softmax, four 16-row quarters of S^T by two halves of the heads;
-// when a unit ends, the next one's Q' first, then the output.  M (2): one thread
-// issues the products, S of two tiles, then O of the two: while one tile's products
-// run the other is widened or in its softmax.  Registers go from L, M and W to X
-// (setmaxnreg): the softmax must not spill, because local loads queue behind W's.
+// when a unit ends, the next one's Q' first, then the output.  M (1-3): issue the
+// products, a thread each for S of the even tiles, S of the odd ones and O: a
+// thread that has committed MMAs is held at its next barrier until they are done,
+// so one thread for all of them left the tensor core idle between tiles.
+// Registers go from L, M and W to X (setmaxnreg): the softmax must not spill,
+// because local loads queue behind W's.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
@@ -65,13 +66,13 @@ using namespace ptx;
 constexpr int kDim = DS4X_KV_DIM;  // 512
 constexpr int kTile = 64;          // rows a tile
 constexpr int kHeads = 64;         // heads a unit, at most
-constexpr int kLWarps = 2, kMWarp = 2;               // warp 3 has no role
-constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 20, kXWarps = 8;  // W: kWWarps a group, two groups
+constexpr int kMWarp0 = 1;                           // S of even tiles, S of odd tiles, O
+constexpr int kWWarp0 = 4, kWWarps = 16, kXWarp0 = 20, kXWarps = 8;
 constexpr int kXThreads = 32 * kXWarps;
 constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 896
 // registers a thread: at launch, then by role
 constexpr int kRegs = 72, kRegsLM = 56, kRegsW = 64, kRegsX = 96;
-static_assert(4 * kRegsLM + 2 * kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
+static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
@@ -97,10 +98,11 @@ struct __align__(1024) Smem {
   long long scan[kThreads / 32];
   long long cut0, cut1;             // the CTA's run of tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
+  int total;                        // its tiles
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(Smem) + 1024 - 16 <= 232448, "shared-memory budget");
+static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
 // The workspace behind its header.  Part 2 c: CTA c's share of a unit that an
 // earlier CTA began; part 2 c + 1: of one that it begins and a later one ends.
@@ -123,15 +125,21 @@ __device__ __forceinline__ unsigned long long globaltimer() {
   return t;
 }
 
+__device__ __noinline__ void wait_failed(Smem &sm, WsHeader *hdr) {
+  atomicExch(&hdr->status, int32_t(DS4X_ETIMEOUT));
+  *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+}
 __device__ __forceinline__ void wait_bar(Smem &sm, unsigned long long *bar, uint32_t parity, WsHeader *hdr) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try_wait(b, parity)) return;
   const unsigned long long t0 = globaltimer();
-  while (!mbar_try_wait(b, parity)) {
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)  // (a try may itself wait a while; the clock is looked at now and then)
+      if (mbar_try_wait(b, parity)) return;
     if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
     if (globaltimer() - t0 > kTimeoutNs) {
-      atomicExch(&hdr->status, int32_t(DS4X_ETIMEOUT));
-      *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+      wait_failed(sm, hdr);
       return;
     }
   }
@@ -180,6 +188,23 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
 // 2^e as fp16 bits for e <= 0 (0 below the smallest subnormal 2^-24).
 __device__ __forceinline__ uint32_t pow2_half_bits(int e) {
@@ -196,6 +221,10 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+
 // A token's rows: n of them, from row r0 of its sequence (or of its list).
 struct Rows {
   int64_t r0;
@@ -207,7 +236,7 @@ __device__ __forceinline__ Rows token_rows(const PagedAttn &a, int t) {
   const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
   const int64_t b = a.row_begin != nullptr ? max(int64_t(0), int64_t(__ldcg(a.row_begin + t))) : 0;
   const int64_t e = min(room, int64_t(__ldcg(a.row_end + t)));
-  return Rows{b, int32_t(max(int64_t(0), e - b))};
+  return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
 }
 // A token without a row still has a tile (of rows that are not there): it writes the zeros.
 __device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
@@ -217,11 +246,10 @@ struct Walk {
   int unit, off;   // the share's unit, and its first tile within it
   int i0, i1;      // the share's tiles, locally
   int tiles;       // the unit's tiles
-  int64_t r0;
-  int n;
+  int r0, n;       // the token's rows
   __device__ __forceinline__ void load(const Args &g, int total) {
     const Rows r = token_rows(g.a, unit / g.groups);
-    r0 = r.r0;
+    r0 = int(r.r0);
     n = r.n;
     tiles = rows_tiles(n);
     i1 = int(min(int64_t(total), int64_t(i0) + tiles - off));
@@ -309,13 +337,20 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
     }
   }
   __syncthreads();
+  if (tid == 0) {
+    const long long run = sm.cut1 - sm.cut0;
+    if (run > INT32_MAX - 8) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));  // (months of work)
+    sm.total = int(min(run, (long long)(INT32_MAX - 8)));
+  }
+  __syncthreads();
 }
 
 // ---- L: finding rows ------------------------------------------------------------
 
-__device__ __forceinline__ void role_l(const Args &g, Smem &sm, int total, WsHeader *hdr) {
+__device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
   const PagedAttn &a = g.a;
-  const int lane = threadIdx.x & 31, r = threadIdx.x;  // the tile's row that this lane finds
+  const int total = sm.total;
+  const int lane = threadIdx.x & 31;  // finds the tile's rows lane and 32 + lane
   Walk w;
   w.begin(g, sm, total);
   for (;;) {
@@ -323,26 +358,42 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, int total, WsHea
     const int seq = paged_seq_of(a.c, t, lane);
     const int64_t n_rows = a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(a.n_rows + seq)) : 0;
     for (int i = w.i0; i < w.i1; ++i) {
-      const int64_t pos = int64_t(w.off + (i - w.i0)) * kTile + r;
-      int2 at = make_int2(-1, 0);
-      if (pos < w.n && seq >= 0) {
-        int64_t row = w.r0 + pos;
-        if (a.idx != nullptr) {
-          row = __ldcg(a.idx + int64_t(t) * a.k + pos);
-          if (row >= n_rows) row = -2;
-        }
-        if (row != -1) {  // (-1: an entry that names no row; a range has none)
-          const int64_t j = row >> a.c.page_log2;
-          if (row >= 0 && j < a.c.seq_pages) {
-            const int32_t page = __ldcg(a.c.table + int64_t(seq) * a.c.table_stride + j);
-            if (page >= 0 && page < a.c.n_pages) at = make_int2(page, int(row & ((1 << a.c.page_log2) - 1)));
-          }
-          if (at.x < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      const int pos = (w.off + (i - w.i0)) * kTile + lane;
+      int row[2];  // -1: none (a table reaches at most row 2^31 - 2)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        row[k] = -1;
+        if (pos < w.n - 32 * k && seq >= 0) {
+          row[k] = a.idx != nullptr ? __ldcg(a.idx + int64_t(t) * a.k + pos + 32 * k) : int(w.r0) + pos + 32 * k;
+          if (a.idx != nullptr && row[k] >= n_rows) row[k] = -2;
         }
       }
+      int2 at[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = row[k] >> a.c.page_log2;
+        const bool in = row[k] >= 0 && j < a.c.seq_pages;
+        const int32_t page = in ? __ldcg(a.c.table + int64_t(seq) * a.c.table_stride + j) : -1;
+        at[k] = make_int2(page < a.c.n_pages ? max(page, -1) : -1, row[k] & ((1 << a.c.page_log2) - 1));
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (row[k] != -1 && at[k].x < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      // toward L2: a row's code lines (224 bytes lie in two or three) and RoPE line
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (at[k].x >= 0) {
+          const PagedRow p{a.c.pages + (int64_t(at[k].x) << a.c.page_log2) * DS4X_PAGED_ROW_BYTES, at[k].y};
+          const uint8_t *co = p.page + paged_code_off(p);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(co));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(co + 112));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(co + 223));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.page + paged_tail_off(a.c, p)));
+        }
       const int slot = i % kAhead;
       if (i >= kAhead) wait_bar(sm, &sm.lfree[slot], (i / kAhead - 1) & 1, hdr);
-      sm.found[slot][r] = at;
+      sm.found[slot][lane] = at[0];
+      sm.found[slot][32 + lane] = at[1];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.lfull[slot]));
     }
@@ -373,13 +424,11 @@ __device__ __forceinline__ int v_chunk_back(int P) {  // the C of place P
 }
 
 struct Raw {
-  uint4 a, b, t, sc;
-  int ok;
+  uint4 a, b, t, sc;  // (the scale record's zero byte: 255 marks a row that is not there)
 };
 __device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int l, Raw &w) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  w.ok = at.x >= 0;
-  if (w.ok) {
+  if (at.x >= 0) {
     const PagedRow p{c.pages + (int64_t(at.x) << c.page_log2) * DS4X_PAGED_ROW_BYTES, at.y};
     const uint4 *co = reinterpret_cast<const uint4 *>(p.page + paged_code_off(p)) + l;
     w.sc = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_scale_off(c, p)));
@@ -387,123 +436,138 @@ __device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int l, Ra
     w.b = l < 6 ? __ldcg(co + 8) : z;
     w.t = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p)) + l);
   } else {
-    w.sc = w.a = w.b = w.t = z;
+    w.a = w.b = w.t = z;
+    w.sc = make_uint4(0, 0, 0, 0xff000000u);
   }
 }
 
-// Eight codes times the factor pair f, as fp16.
-__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t f) {
+// Eight codes times the factor pair f, as fp16, to shared memory.
+__device__ __forceinline__ void widen8(uint32_t addr, uint32_t w, uint32_t f) {
   uint32_t h0, h1, h2, h3;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
       "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
       : "r"(w));
-  return make_uint4(hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f), hmul2_bits(h3, f));
+  sts16(addr, hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f), hmul2_bits(h3, f));
 }
-__device__ __forceinline__ void widen(uint8_t *row, int r7, int l, const uint32_t (&off_b)[4], const Raw &w) {
+// A row (at `row`) of V': x = 16 (row % 8).
+__device__ __forceinline__ void widen(uint32_t row, uint32_t x, int l, const uint32_t (&off_b)[4], const Raw &w) {
   const int E = int((w.sc.w >> 16) & 0xffu);
   const uint32_t sh = 8 * (l & 3);
   const uint32_t fa = pow2_half_bits(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> sh) & 0xffu) - E)) * 0x10001u;
-  uint8_t *pa = row + ((l ^ r7) << 4);
-  *reinterpret_cast<uint4 *>(pa) = widen8(w.a.x, fa);
-  *reinterpret_cast<uint4 *>(pa + 8192) = widen8(w.a.y, fa);
-  *reinterpret_cast<uint4 *>(pa + 2 * 8192) = widen8(w.a.z, fa);
-  *reinterpret_cast<uint4 *>(pa + 3 * 8192) = widen8(w.a.w, fa);
-  *reinterpret_cast<uint4 *>(pa + 7 * 8192) = w.t;
+  const uint32_t pa = row + (uint32_t(l << 4) ^ x);
+  widen8(pa, w.a.x, fa);
+  widen8(pa + 8192, w.a.y, fa);
+  widen8(pa + 2 * 8192, w.a.z, fa);
+  widen8(pa + 3 * 8192, w.a.w, fa);
+  sts16(pa + 7 * 8192, w.t.x, w.t.y, w.t.z, w.t.w);
   if (l < 6) {
     const uint32_t fb = pow2_half_bits(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> sh) & 0xffu) - E)) * 0x10001u;
-    *reinterpret_cast<uint4 *>(row + (off_b[0] ^ (r7 << 4))) = widen8(w.b.x, fb);
-    *reinterpret_cast<uint4 *>(row + (off_b[1] ^ (r7 << 4))) = widen8(w.b.y, fb);
-    *reinterpret_cast<uint4 *>(row + (off_b[2] ^ (r7 << 4))) = widen8(w.b.z, fb);
-    *reinterpret_cast<uint4 *>(row + (off_b[3] ^ (r7 << 4))) = widen8(w.b.w, fb);
+    widen8(row + (off_b[0] ^ x), w.b.x, fb);
+    widen8(row + (off_b[1] ^ x), w.b.y, fb);
+    widen8(row + (off_b[2] ^ x), w.b.z, fb);
+    widen8(row + (off_b[3] ^ x), w.b.w, fb);
   }
 }
 
-__device__ __forceinline__ void role_w(const Args &g, Smem &sm, int total, WsHeader *hdr) {
+__device__ __forceinline__ void role_w(const Args &g, Smem &sm, WsHeader *hdr) {
+  const int total = sm.total;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
-  const int buf = warp / kWWarps;        // the group and its V' buffer
   const int l = lane & 7, q = lane >> 3;
-  const int r = 8 * (warp % kWWarps) + q;  // the tile's rows that this lane helps to widen: r and r + 4
+  const int r = 4 * warp + q;            // the tile's row that this lane helps to widen
   uint32_t off_b[4];                     // block 8 + l's words, within a row
 #pragma unroll
   for (int u = 0; u < 4; ++u) off_b[u] = uint32_t(4 + ((l + 6 * u) >> 3)) * 8192u + (uint32_t((l + 6 * u) & 7) << 4);
-  Raw raw[2];
-  auto load = [&](int i) {
+  const uint32_t row0 = smem_u32(sm.v[0]) + r * 128;
+  auto load = [&](int i, Raw &raw) {
     if (i >= total) return;
     const int slot = i % kAhead;
     wait_bar(sm, &sm.lfull[slot], (i / kAhead) & 1, hdr);
-    const int2 at0 = sm.found[slot][r], at1 = sm.found[slot][r + 4];
+    const int2 at = sm.found[slot][r];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.lfree[slot]));
-    load_raw(g.a.c, at0, l, raw[0]);
-    load_raw(g.a.c, at1, l, raw[1]);
+    load_raw(g.a.c, at, l, raw);
   };
-  uint8_t *row = sm.v[buf] + r * 128;
-  load(buf);
-  for (int i = buf; i < total; i += 2) {
+  auto tile = [&](int i, int buf, Raw &raw) {
     if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
-    widen(row, q, l, off_b, raw[0]);
-    widen(row + 4 * 128, q + 4, l, off_b, raw[1]);
-    if (l < 2) sm.rowe[buf][r + 4 * l] = (l ? raw[1].ok : raw[0].ok) ? int(((l ? raw[1].sc.w : raw[0].sc.w) >> 16) & 0xffu) - 127 : kNoRow;
+    widen(row0 + 65536u * buf, uint32_t(r & 7) << 4, l, off_b, raw);
+    if (l == 0) sm.rowe[buf][r] = raw.sc.w >> 24 ? kNoRow : int((raw.sc.w >> 16) & 0xffu) - 127;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
-    load(i + 2);
+    load(i + 2, raw);
+  };
+  Raw even, odd;
+  load(0, even);
+  load(1, odd);
+  for (int i = 0; i < total; i += 2) {
+    tile(i, 0, even);
+    if (i + 1 < total) tile(i + 1, 1, odd);
   }
 }
 
-// ---- M: the products (and the proxy fence between what W and X stored and what the
-// tensor core reads: here, behind the barrier that orders their stores, because a
-// fence in W would wait for W's loads in flight) ---------------------------------------------------------------
+// ---- M: the products --------------------------------------------------------------
+// The proxy fence between what W and X stored and what the tensor core reads is
+// here, behind the barrier that orders their stores: in W it would wait for W's
+// loads in flight.
 
-__device__ __forceinline__ void role_m(const Args &g, Smem &sm, uint32_t tmem, int total, WsHeader *hdr) {
-  const uint32_t q_a = smem_u32(sm.q), v_a = smem_u32(sm.v[0]), p_a = smem_u32(sm.p[0]);
+// S of the tiles of one parity.
+__device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader *hdr) {
+  const int total = sm.total;
+  const uint32_t tmem = sm.tmem_base;
   const uint32_t idS = idesc_f16(kTile, uint32_t(g.n_cols), 0, 0);  // V' K-major, Q' K-major
-  const uint32_t idO = idesc_f16(128, uint32_t(g.n_cols), 1, 1);    // V'^T MN-major, P^T MN-major
-  const uint64_t dS_b = desc_sw128(q_a, 16, 1024);
+  const uint64_t dS_a = desc_sw128(smem_u32(sm.v[b]), 16, 1024), dS_b = desc_sw128(smem_u32(sm.q), 16, 1024);
   Walk w;
   w.begin(g, sm, total);
-  auto issue_s = [&](int i) {
-    const int b = i & 1;
-    wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
-    fence_proxy_async_smem();
-    tc_fence_after();
-    const uint64_t dS_a = desc_sw128(v_a + 65536u * b, 16, 1024);
-    // K step ks: 16 dims, 32 bytes into panel ks / 4 (descriptor addresses count 16 bytes)
-#pragma unroll
-    for (int ks = 0; ks < kDim / 16; ++ks)
-      mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)),
-                 dS_b + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)), idS, ks > 0 ? 1u : 0u);
-    tc_commit(smem_u32(&sm.sfull[b]));
-  };
-  auto issue_o = [&](int i) {
-    const int b = i & 1;
-    wait_bar(sm, &sm.pfull[b], (i >> 1) & 1, hdr);
-    fence_proxy_async_smem();
-    tc_fence_after();
-    const uint64_t dO_a = desc_sw128(v_a + 65536u * b, 8192, 1024), dO_b = desc_sw128(p_a + 8192u * b, 8192, 1024);
-    const uint32_t acc = i > w.i0 ? 1u : 0u;
-    // M tile mi: panels 2 mi, 2 mi + 1; K step ks: 16 rows (2 KB)
-#pragma unroll
-    for (int mi = 0; mi < kDim / 128; ++mi)
-#pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
-        mma_f16_ss(tmem + kOCol + 64u * mi, dO_a + uint64_t(1024 * mi + 128 * ks), dO_b + uint64_t(128 * ks), idO,
-                   ks > 0 ? 1u : acc);
-    tc_commit(smem_u32(&sm.pvdone[b]));
-  };
   for (int seg = 0;; ++seg) {
     wait_bar(sm, &sm.qfull, seg & 1, hdr);
-    for (int i = w.i0; i < w.i1; i += 2) {
-      issue_s(i);
-      if (i + 1 < w.i1) issue_s(i + 1);
-      issue_o(i);
-      if (i + 1 < w.i1) issue_o(i + 1);
+    for (int i = w.i0 + ((w.i0 ^ b) & 1); i < w.i1; i += 2) {
+      wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
+      fence_proxy_async_smem();
+      tc_fence_after();
+      // K step ks: 16 dims, 32 bytes into panel ks / 4 (descriptor addresses count 16 bytes)
+#pragma unroll
+      for (int ks = 0; ks < kDim / 16; ++ks)
+        mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)),
+                   dS_b + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)), idS, ks > 0 ? 1u : 0u);
+      tc_commit(smem_u32(&sm.sfull[b]));
     }
     if (w.i1 >= total) break;
     w.next(g, total);
   }
   tc_commit(smem_u32(&sm.drain));  // nothing may still write this CTA's memory when it exits
+  wait_bar(sm, &sm.drain, 0, hdr);
+}
+
+// O of every tile, in order.
+__device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
+  const int total = sm.total;
+  const uint32_t tmem = sm.tmem_base;
+  const uint32_t idO = idesc_f16(128, uint32_t(g.n_cols), 1, 1);  // V'^T MN-major, P^T MN-major
+  const uint64_t dO_a0 = desc_sw128(smem_u32(sm.v[0]), 8192, 1024), dO_b0 = desc_sw128(smem_u32(sm.p[0]), 8192, 1024);
+  Walk w;
+  w.begin(g, sm, total);
+  for (;;) {
+    for (int i = w.i0; i < w.i1; ++i) {
+      const int b = i & 1;
+      wait_bar(sm, &sm.pfull[b], (i >> 1) & 1, hdr);
+      fence_proxy_async_smem();
+      tc_fence_after();
+      const uint64_t dO_a = dO_a0 + uint64_t(4096 * b), dO_b = dO_b0 + uint64_t(512 * b);
+      const uint32_t acc = i > w.i0 ? 1u : 0u;
+      // M tile mi: panels 2 mi, 2 mi + 1; K step ks: 16 rows (2 KB)
+#pragma unroll
+      for (int mi = 0; mi < kDim / 128; ++mi)
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks)
+          mma_f16_ss(tmem + kOCol + 64u * mi, dO_a + uint64_t(1024 * mi + 128 * ks), dO_b + uint64_t(128 * ks), idO,
+                     ks > 0 ? 1u : acc);
+      tc_commit(smem_u32(&sm.pvdone[b]));
+    }
+    if (w.i1 >= total) break;
+    w.next(g, total);
+  }
+  tc_commit(smem_u32(&sm.drain));
   wait_bar(sm, &sm.drain, 0, hdr);
 }
 
@@ -564,7 +628,9 @@ __device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, in
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
 }
 
-__device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, int total, Parts *parts, WsHeader *hdr) {
+__device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
+  const int total = sm.total;
+  const uint32_t tmem = sm.tmem_base;
   const PagedAttn &a = g.a;
   const int lane = threadIdx.x & 31, xw = (threadIdx.x >> 5) - kXWarp0, xt = threadIdx.x - 32 * kXWarp0;
   const int qd = xw & 3, half = xw >> 2;        // tile rows 16 qd .., heads 32 half ..
@@ -599,10 +665,13 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
         er[1] = e1 == kNoRow ? 0.0f : float(e1);
         tc_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          d[k] = fmaf(__uint_as_float(s[k]), f[(k >> 1) & 1], ef[(k >> 1) & 1]) - m[2 * (k >> 2) + (k & 1)];
-#pragma unroll
         for (int k = 0; k < 16; k += 2) {
+          const int row = (k >> 1) & 1, h = 2 * (k >> 2);
+          float2 x = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f[row], f[row]),
+                          make_float2(ef[row], ef[row]));
+          x = add2(x, make_float2(-m[h], -m[h + 1]));
+          d[k] = x.x;
+          d[k + 1] = x.y;
           over = fmaxf(fmaxf(over, d[k]), d[k + 1]);
           under = fminf(fminf(under, d[k]), d[k + 1]);
         }
@@ -669,8 +738,13 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
         if (!apart) {
           const float inv[2] = {pow2f(-int(er[0])), pow2f(-int(er[1]))};
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            sum[2 * (k >> 2) + (k & 1)] = fmaf(d[k], inv[(k >> 1) & 1], sum[2 * (k >> 2) + (k & 1)]);
+          for (int k = 0; k < 16; k += 2) {
+            const int row = (k >> 1) & 1, h = 2 * (k >> 2);
+            const float2 t = fma2(make_float2(d[k], d[k + 1]), make_float2(inv[row], inv[row]),
+                                  make_float2(sum[h], sum[h + 1]));
+            sum[h] = t.x;
+            sum[h + 1] = t.y;
+          }
         }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -759,8 +833,9 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, uint32_t tmem, i
 
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *__restrict__ parts,
                                                                  WsHeader *__restrict__ hdr) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (no static shared memory: the dynamic begins at the window's start, as aligned as Smem asks)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -770,16 +845,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
       mbar_init(smem_u32(&sm.pvdone[b]), 1);
     }
     for (int k = 0; k < kAhead; ++k) {
-      mbar_init(smem_u32(&sm.lfull[k]), kLWarps);
+      mbar_init(smem_u32(&sm.lfull[k]), 1);
       mbar_init(smem_u32(&sm.lfree[k]), kWWarps);
     }
     mbar_init(smem_u32(&sm.qfull), kXWarps);
-    mbar_init(smem_u32(&sm.drain), 1);
+    mbar_init(smem_u32(&sm.drain), 3);
     sm.abort_flag = 0;
     sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
     fence_mbar_init();
   }
-  if (warp == kMWarp) {
+  if (warp == kMWarp0) {
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
@@ -790,32 +865,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   tc_fence_before();
   find_cuts(g, sm, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
-  const long long run = sm.cut1 - sm.cut0;
-  if (run > INT32_MAX && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-  const int total = int(min(run, (long long)(INT32_MAX - 8)));
-  if (total > 0) {
+  if (sm.total > 0) {
     if (warp >= kXWarp0) {
       set_regs_up<kRegsX>();
-      role_x(g, sm, tmem, total, parts, hdr);
+      role_x(g, sm, parts, hdr);
     } else if (warp >= kWWarp0) {
       set_regs_down<kRegsW>();
-      role_w(g, sm, total, hdr);
+      role_w(g, sm, hdr);
     } else {
       set_regs_down<kRegsLM>();
-      if (warp < kLWarps) {
-        role_l(g, sm, total, hdr);
-      } else if (warp == kMWarp) {
-        if (elect_one()) role_m(g, sm, tmem, total, hdr);
+      if (warp < kMWarp0) {
+        role_l(g, sm, hdr);
+      } else {
+        if (elect_one()) {
+          if (warp < kMWarp0 + 2)
+            role_s(g, sm, warp - kMWarp0, hdr);
+          else
+            role_o(g, sm, hdr);
+        }
         __syncwarp();
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMWarp) {
+  if (warp == kMWarp0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sm.tmem_base, 512);
   }
 }
 
@@ -901,8 +977,7 @@ size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts); }
 
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  // the dynamic shared memory is at least 16-byte aligned: room to round it up to 1024
-  const int smem = int(sizeof(Smem)) + 1024 - 16;
+  const int smem = int(sizeof(Smem));
   cudaError_t e = set_max_smem_once(paged_attn_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
