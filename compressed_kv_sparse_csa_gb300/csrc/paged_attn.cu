@@ -98,6 +98,7 @@ struct __align__(1024) Smem {
   long long scan[kThreads / 32];
   long long cut0, cut1;             // the CTA's run of tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
+  int row0, rows;                   // that unit's rows
   int total;                        // its tiles
   uint32_t tmem_base;
   int abort_flag;
@@ -136,7 +137,7 @@ __device__ __forceinline__ void wait_bar(Smem &sm, unsigned long long *bar, uint
   for (;;) {
 #pragma unroll 1
     for (int k = 0; k < 64; ++k)  // (a try may itself wait a while; the clock is looked at now and then)
-      if (mbar_try_wait(b, parity)) return;
+      if (mbar_try_wait_sleep(b, parity, 2000)) return;
     if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
     if (globaltimer() - t0 > kTimeoutNs) {
       wait_failed(sm, hdr);
@@ -247,42 +248,48 @@ struct Walk {
   int i0, i1;      // the share's tiles, locally
   int tiles;       // the unit's tiles
   int r0, n;       // the token's rows
-  __device__ __forceinline__ void load(const Args &g, int total) {
-    const Rows r = token_rows(g.a, unit / g.groups);
-    r0 = int(r.r0);
-    n = r.n;
+  __device__ __forceinline__ void set(int row0, int rows, int total) {
+    r0 = row0;
+    n = rows;
     tiles = rows_tiles(n);
     i1 = int(min(int64_t(total), int64_t(i0) + tiles - off));
   }
-  __device__ __forceinline__ void begin(const Args &g, const Smem &sm, int total) {
+  __device__ __forceinline__ void begin(const Smem &sm, int total) {
     unit = sm.unit0;
     off = sm.off0;
     i0 = 0;
-    load(g, total);
+    set(sm.row0, sm.rows, total);
   }
   __device__ __forceinline__ void next(const Args &g, int total) {
     ++unit;
     off = 0;
     i0 = i1;
-    load(g, total);
+    const Rows r = token_rows(g.a, unit / g.groups);
+    set(int(r.r0), r.n, total);
   }
 };
 
 // ---- the cuts ------------------------------------------------------------------
 
-// The run of CTA c of g: unit0, off0, cut0, cut1.  All threads.
+// The run of CTA c of g: unit0, off0, total; the first unit's rows.  All threads.
 __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   const PagedAttn &a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = max(0, min(a.n_tokens, __ldcg(a.c.cu + a.c.n_seqs)));  // tokens behind are padding
-  const int per = (n + kThreads - 1) / kThreads;
-  const int t0 = min(n, tid * per), t1 = min(n, t0 + per);
-  long long mine = 0;
-  for (int t = t0; t < t1; ++t) {
-    mine += (long long)(rows_tiles(token_rows(a, t).n)) * g.groups;
-    if (blockIdx.x == 0 && a.idx == nullptr && __ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
-      atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-  }
+  constexpr int kWarps = kThreads / 32;
+  // a thread takes `per` tokens in a row (of all that there may be: the count of
+  // valid ones is on its way with their rows)
+  const int per = (a.n_tokens + kThreads - 1) / kThreads;
+  const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
+  const int valid = __ldcg(a.c.cu + a.c.n_seqs);  // tokens behind are padding
+  auto tiles_of = [&](int t) { return t < valid ? rows_tiles(token_rows(a, t).n) : 0; };
+  const int first = t0 < t1 ? tiles_of(t0) : 0;
+  long long mine = first;
+  for (int t = t0 + 1; t < t1; ++t) mine += tiles_of(t);
+  mine *= g.groups;
+  if (blockIdx.x == 0 && a.idx == nullptr)
+    for (int t = t0; t < min(t1, valid); ++t)
+      if (__ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
+        atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -290,19 +297,26 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
     if (lane >= o) incl += v;
   }
   if (lane == 31) sm.scan[warp] = incl;
-  if (tid == 0) sm.unit0 = sm.off0 = 0;
+  if (tid == 0) sm.unit0 = sm.off0 = sm.row0 = sm.rows = 0;
   __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const long long v = sm.scan[w];
-    if (w < warp) before += v;
-    total += v;
+  long long ws = lane < kWarps ? sm.scan[lane] : 0;
+  long long wi = ws;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, wi, o);
+    if (lane >= o) wi += v;
   }
-  // every CTA of the first G has a tile (total < 2^43 and G <= 160: no overflow)
-  const long long G = max(1ll, min((long long)gridDim.x, total)), tol = total / (16 * G);
+  const long long total = __shfl_sync(0xffffffffu, wi, 31);
+  const long long before = __shfl_sync(0xffffffffu, wi - ws, warp) + incl - mine;
+  // every CTA of the first G has a tile
+  const unsigned G = unsigned(max(1ll, min((long long)gridDim.x, total)));
+  auto part = [&](unsigned c) {  // c total / G, in 32 bits where they do (total < 2^43, G <= 160)
+    return total < (1 << 24) ? (long long)(c * unsigned(total) / G) : (long long)(c * (unsigned long long)total / G);
+  };
+  const long long tol = total < (1 << 24) ? (long long)(unsigned(total) / (16 * G)) : total / (16 * G);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const long long x = (long long)(blockIdx.x + e) * total / G;
+    const long long x = part(blockIdx.x + e);
     if (x >= total) {
       if (tid == 0) (e ? sm.cut1 : sm.cut0) = total;
       continue;
@@ -310,24 +324,31 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
     if (x < before || x >= before + mine) continue;
     long long p = before;  // tile x lies in this thread's tokens
     for (int t = t0; t < t1; ++t) {
-      const int tiles = rows_tiles(token_rows(a, t).n);
+      const int tiles = t == t0 ? first : tiles_of(t);
       const long long w = (long long)(tiles)*g.groups;
       if (x < p + w) {
-        const long long k = (x - p) / tiles;
-        int unit = t * g.groups + int(k);
-        long long off = (x - p) - k * tiles, at = x;
+        int k = 0;  // the head group
+        long long off = x - p;
+        while (off >= tiles) off -= tiles, ++k;
+        long long at = x;
         if (off <= tol) {
           at -= off;
           off = 0;
         } else if (tiles - off <= tol) {
           at += tiles - off;
           off = 0;
-          ++unit;
+          ++k;
         }
+        if (k == g.groups) k = 0, ++t;
         if (e == 0) {
           sm.cut0 = at;
-          sm.unit0 = unit;
+          sm.unit0 = t * g.groups + k;
           sm.off0 = int(off);
+          if (at < total) {
+            const Rows r = token_rows(a, t);
+            sm.row0 = int(r.r0);
+            sm.rows = r.n;
+          }
         } else {
           sm.cut1 = at;
         }
@@ -352,21 +373,30 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
   const int total = sm.total;
   const int lane = threadIdx.x & 31;  // finds the tile's rows lane and 32 + lane
   Walk w;
-  w.begin(g, sm, total);
+  w.begin(sm, total);
   for (;;) {
     const int t = w.unit / g.groups;
-    const int seq = paged_seq_of(a.c, t, lane);
-    const int64_t n_rows = a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(a.n_rows + seq)) : 0;
+    int seq = -1;
+    int64_t n_rows = 0;
+    bool fresh = true;
     for (int i = w.i0; i < w.i1; ++i) {
       const int pos = (w.off + (i - w.i0)) * kTile + lane;
       int row[2];  // -1: none (a table reaches at most row 2^31 - 2)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         row[k] = -1;
-        if (pos < w.n - 32 * k && seq >= 0) {
-          row[k] = a.idx != nullptr ? __ldcg(a.idx + int64_t(t) * a.k + pos + 32 * k) : int(w.r0) + pos + 32 * k;
-          if (a.idx != nullptr && row[k] >= n_rows) row[k] = -2;
-        }
+        if (pos < w.n - 32 * k)
+          row[k] = a.idx != nullptr ? __ldcg(a.idx + int64_t(t) * a.k + pos + 32 * k) : w.r0 + pos + 32 * k;
+      }
+      if (fresh) {  // (looked up while the first entries are on their way)
+        seq = paged_seq_of(a.c, t, lane);
+        n_rows = a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(a.n_rows + seq)) : 0;
+        fresh = false;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (seq < 0) row[k] = -1;
+        if (a.idx != nullptr && row[k] >= n_rows) row[k] = -2;
       }
       int2 at[2];
 #pragma unroll
@@ -518,7 +548,7 @@ __device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader 
   const uint32_t idS = idesc_f16(kTile, uint32_t(g.n_cols), 0, 0);  // V' K-major, Q' K-major
   const uint64_t dS_a = desc_sw128(smem_u32(sm.v[b]), 16, 1024), dS_b = desc_sw128(smem_u32(sm.q), 16, 1024);
   Walk w;
-  w.begin(g, sm, total);
+  w.begin(sm, total);
   for (int seg = 0;; ++seg) {
     wait_bar(sm, &sm.qfull, seg & 1, hdr);
     for (int i = w.i0 + ((w.i0 ^ b) & 1); i < w.i1; i += 2) {
@@ -546,7 +576,7 @@ __device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
   const uint32_t idO = idesc_f16(128, uint32_t(g.n_cols), 1, 1);  // V'^T MN-major, P^T MN-major
   const uint64_t dO_a0 = desc_sw128(smem_u32(sm.v[0]), 8192, 1024), dO_b0 = desc_sw128(smem_u32(sm.p[0]), 8192, 1024);
   Walk w;
-  w.begin(g, sm, total);
+  w.begin(sm, total);
   for (;;) {
     for (int i = w.i0; i < w.i1; ++i) {
       const int b = i & 1;
@@ -574,29 +604,23 @@ __device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
 // ---- X: softmax and output ------------------------------------------------------------
 
 // Q' of a unit: warp w of X converts heads 8 w .. 8 w + 7, lane L the 16-byte
-// chunks L and 32 + L of each; heads that the unit does not have are zeros.  Read
-// twice (for the largest value, then to convert: from L2), two heads at a time, so
-// that the unit's sums stay in registers meanwhile.
-__device__ __forceinline__ void load_query(const uint4 *q, int h, int heads, uint4 (&qv)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) qv[i] = h + (i >> 1) < heads ? __ldcg(q + 64 * h + 32 * i) : make_uint4(0, 0, 0, 0);
-}
+// chunks L and 32 + L of each; heads that the unit does not have are zeros.  All of
+// a warp's loads are in flight at once (64 registers: the unit's maxima and sums
+// must be in shared memory by then).
 __device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, int seg, int xw, int lane) {
   const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
   const int heads = min(g.group, g.a.n_heads - h0) - 8 * xw;  // of this warp's
   const uint4 *q =
       reinterpret_cast<const uint4 *>(g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0 + 8 * xw) * kDim) + lane;
+  uint4 qv[16];
   uint32_t m = 0;
-#pragma unroll 2
-  for (int h = 0; h < 8; h += 2) {
-    uint4 qv[4];
-    load_query(q, h, heads, qv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+  for (int i = 0; i < 16; ++i) qv[i] = (i >> 1) < heads ? __ldcg(q + 32 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
-    }
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   const int slot = seg % 3;
@@ -608,21 +632,15 @@ __device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, in
   const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
   const float f = pow2f(c);
   if (xw == 0 && lane == 0) sm.qbase[seg & 1] = g.a.scale * kLog2e * pow2f(-c);
-#pragma unroll 2
-  for (int h2 = 0; h2 < 8; h2 += 2) {
-    uint4 qv[4];
-    load_query(q, h2, heads, qv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = 8 * xw + h2 + (i >> 1), P = v_chunk(32 * (i & 1) + lane);
-      const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-      uint32_t o[4];
+  for (int i = 0; i < 16; ++i) {
+    const int h = 8 * xw + (i >> 1), P = v_chunk(32 * (i & 1) + lane);
+    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+    uint32_t o[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
-      *reinterpret_cast<uint4 *>(sm.q + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4)) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    for (int u = 0; u < 4; ++u)
+      o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
+    sts16(smem_u32(sm.q) + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
@@ -640,7 +658,7 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
   const uint32_t lane_base = uint32_t(32 * qd) << 16;
   make_query(g, sm, sm.unit0, 0, xw, lane);
   Walk w;
-  w.begin(g, sm, total);
+  w.begin(sm, total);
   for (int seg = 0;; ++seg) {
     float m[8], sum[8];  // head hb + 8 j + c: 2 j + c
 #pragma unroll
@@ -757,10 +775,7 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[b]));
     }
-    // ---- the unit's share is done -------------------------------------------------------
-    // the next unit's Q' (this one's last first product is done: its softmax is)
-    if (w.i1 < total) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
-    // sums over the rows, then the output
+    // ---- the unit's share is done: sums over the rows ------------------------------------
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
 #pragma unroll
@@ -775,6 +790,8 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
         if (qd == 0) sm.mh[h] = m[k];
       }
     }
+    // the next unit's Q' (this one's last first product is done: its softmax is)
+    if (w.i1 < total) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
     named_bar_sync(kBarX, kXThreads);
     const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
     const int heads = min(g.group, a.n_heads - h0);
@@ -795,32 +812,37 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
     named_bar_sync(kBarX, kXThreads);
     wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1], ((w.i1 - 1) >> 1) & 1, hdr);
     tc_fence_after();
+    // O^T, 32 heads by 128 dims a step.  (The loads of a step are waited for before
+    // the loop goes round: a register that a load is still to write must not be moved.)
     if (busy) {
 #pragma unroll 1
-      for (int k = 0; k < 2 * kDim / 128; ++k) {
-        uint32_t o[16];
-        const int hc = 32 * half + 16 * (k & 1);  // heads hc .. hc + 15
-        const int d = 8 * v_chunk_back(16 * (k >> 1) + 4 * qd + (lane >> 3)) + (lane & 7);
-        tc_ld_x16(tmem + lane_base + kOCol + 64u * (k >> 1) + uint32_t(hc), o);
+      for (int k = 0; k < kDim / 128; ++k) {
+        uint32_t o[2][16];
+        const uint32_t ta = tmem + lane_base + kOCol + 64u * k + 32u * half;
+        tc_ld_x16(ta, o[0]);
+        tc_ld_x16(ta + 16u, o[1]);
+        const int d = 8 * v_chunk_back(16 * k + 4 * qd + (lane >> 3)) + (lane & 7);
         tc_wait_ld();
-        float v[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = __uint_as_float(o[u]) * sm.hinv[hc + u];
-        if (!whole) {
+        for (int j = 0; j < 2; ++j) {
+          const int hc = 32 * half + 16 * j;  // heads hc .. hc + 15
+          if (!whole) {
+            float *po = &parts->o[part][hc][d];
 #pragma unroll
-          for (int u = 0; u < 16; ++u)
-            if (hc + u < heads) parts->o[part][hc + u][d] = v[u];
-        } else {
-          // neighbouring lanes swap one of two heads, so each stores two dims of one head
-          uint16_t *out = a.out + int64_t(t) * a.out_stride + int64_t(h0) * kDim;
-          const int odd = lane & 1;
+            for (int u = 0; u < 16; ++u)
+              if (hc + u < heads) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
+          } else {
+            // neighbouring lanes swap one of two heads, so each stores two dims of one head
+            uint16_t *out = a.out + int64_t(t) * a.out_stride + int64_t(h0 + hc) * kDim;
+            const int odd = lane & 1;
 #pragma unroll
-          for (int u = 0; u < 16; u += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[u] : v[u + 1], 1);
-            const __nv_bfloat162 pr =
-                odd ? __floats2bfloat162_rn(got, v[u + 1]) : __floats2bfloat162_rn(v[u], got);
-            const int h = hc + u + odd;
-            if (h < heads) *reinterpret_cast<__nv_bfloat162 *>(out + h * kDim + (d & ~1)) = pr;
+            for (int u = 0; u < 16; u += 2) {
+              const float v0 = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
+              const float v1 = __uint_as_float(o[j][u + 1]) * sm.hinv[hc + u + 1];
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+              const __nv_bfloat162 pr = odd ? __floats2bfloat162_rn(got, v1) : __floats2bfloat162_rn(v0, got);
+              if (hc + u + odd < heads) *reinterpret_cast<__nv_bfloat162 *>(out + (u + odd) * kDim + (d & ~1)) = pr;
+            }
           }
         }
       }
@@ -895,79 +917,137 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   }
 }
 
-// Joins the parts of the units that several CTAs share: an item is a unit's
-// head and 128 dims; four groups of 128 threads take the parts in turn, summed
-// in a fixed order.
-constexpr int kJoinDims = 128, kJoinGroups = 4, kJoinThreads = kJoinDims * kJoinGroups;
+// Joins the parts of the units that several CTAs share.  A warp takes 128 dims (a
+// float4 a lane) of a head; a block of 16 warps takes four heads where the unit
+// has at most 16 parts, else one head with its parts dealt over four warps (one
+// unit split over every CTA has only 64 heads to go round).  Sums go in a fixed
+// order.
+constexpr int kJoinWarps = 16, kJoinThreads = 32 * kJoinWarps, kJoinFew = 16;
 
-__global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(Args g, const Parts *__restrict__ parts, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, const Parts *__restrict__ parts,
+                                                                         int ctas) {
   __shared__ int unit[2 * kMaxCtas];
-  __shared__ int first[kMaxCtas], n_first;  // the CTAs that begin a shared unit
-  __shared__ float wt[kMaxCtas + 1], osum[kJoinGroups][kJoinDims], lsum;
-  const int tid = threadIdx.x, lane = tid & 31;
+  // the shared units: the CTA that begins each, its parts, the items before it
+  __shared__ int first[kMaxCtas], count[kMaxCtas], item0[kMaxCtas + 1], n_units;
+  __shared__ float wts[kJoinWarps][kMaxCtas];
+  __shared__ float4 part_sum[kJoinWarps][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = tid; i < 2 * ctas; i += kJoinThreads) unit[i] = __ldcg(parts->unit + i);
+  for (int i = tid; i < 2 * kMaxCtas; i += kJoinThreads) unit[i] = i < 2 * ctas ? __ldcg(parts->unit + i) : -1;
   __syncthreads();
-  if (tid < 32) {
+  if (warp == 0) {
+    constexpr int kWords = kMaxCtas / 32;
+    uint32_t more[kWords];  // bit c: CTA c goes on with the unit that the CTA before it went on with
     int n = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const bool is = c0 + lane < ctas && unit[2 * (c0 + lane) + 1] >= 0;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const int c = 32 * k + lane, u = unit[2 * c];
+      more[k] = __ballot_sync(0xffffffffu, c > 0 && u >= 0 && u == unit[2 * c - 2]);
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const int c = 32 * k + lane;
+      const bool is = unit[2 * c + 1] >= 0;
       const uint32_t b = __ballot_sync(0xffffffffu, is);
-      if (is) first[n + __popc(b & ((1u << lane) - 1))] = c0 + lane;
+      if (is) first[n + __popc(b & ((1u << lane) - 1))] = c;
       n += __popc(b);
     }
-    if (lane == 0) n_first = n;
+    __syncwarp();
+    int items = 0;
+    for (int e0 = 0; e0 < n; e0 += 32) {
+      const int e = e0 + lane;
+      int mine = 0;
+      if (e < n) {
+        int c = first[e] + 1;  // the unit's next part is CTA c's, then those of a run of set bits
+        if (c < kMaxCtas && unit[2 * c] == unit[2 * c - 1]) ++c;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          if (c >= 32 * k && c < 32 * k + 32) {
+            const uint32_t clear = ~more[k] >> (c & 31);  // (shifted-in zeros: the word's end)
+            c = clear != 0 ? c + __ffs(int(clear)) - 1 : 32 * k + 32;
+          }
+        count[e] = c - first[e];
+        const int h0 = (unit[2 * first[e] + 1] % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
+        mine = count[e] <= kJoinFew ? (heads + 3) / 4 : heads;
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (e < n) item0[e] = items + incl - mine;
+      items += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      n_units = n;
+      item0[n] = items;
+    }
   }
   __syncthreads();
-  constexpr int kQuarters = kDim / kJoinDims;
-  for (int item = blockIdx.x; item < n_first * kHeads * kQuarters; item += gridDim.x) {
-    const int c0 = first[item / (kHeads * kQuarters)], h = item / kQuarters % kHeads, q = item % kQuarters;
-    const int u = unit[2 * c0 + 1];
-    const int t = u / g.groups, h0 = (u % g.groups) * g.group;
-    if (h >= min(g.group, g.a.n_heads - h0)) continue;
-    int n = 1;  // parts: c0's 2 c0 + 1, then 2 c of the CTAs behind it
-    while (c0 + n < ctas && unit[2 * (c0 + n)] == u) ++n;
-    auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
-    if (tid < 32) {
-      float m = -INFINITY;
-      for (int k = lane; k < n; k += 32) m = fmaxf(m, wt[k] = __ldcg(&parts->lse2[slot(k)][h]));
+  const int items = item0[n_units];
+  for (int item = blockIdx.x, e = 0; item < items; item += gridDim.x) {
+    while (item >= item0[e + 1]) ++e;
+    const int c0 = first[e], n = count[e], u = unit[2 * c0 + 1];
+    const int t = u / g.groups, h0 = (u % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
+    const bool few = n <= kJoinFew;
+    const int quarter = warp & 3, deal = warp >> 2;
+    const int h = few ? 4 * (item - item0[e]) + deal : item - item0[e];
+    const int k0 = few ? 0 : deal, step = few ? 1 : 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < heads) {  // (a block's warps differ in it only where few)
+      auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+      float m = -INFINITY, s = 0.0f;
+      for (int k = lane; k < n; k += 32) m = fmaxf(m, wts[warp][k] = __ldcg(&parts->lse2[slot(k)][h]));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float s = 0.0f;
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       for (int k = lane; k < n; k += 32) {
-        const float e = wt[k] == -INFINITY ? 0.0f : exp2f(wt[k] - m);
-        wt[k] = e;
-        s += e;
+        const float x = wts[warp][k], w = x == -INFINITY ? 0.0f : exp2f(x - m);
+        wts[warp][k] = w;
+        s += w;
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) {
-        lsum = s;
-        if (q == 0 && g.a.lse != nullptr)
-          g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      __syncwarp();
+      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+      const int d0 = 128 * quarter + 4 * lane;
+      for (int k = k0; k < n; k += 8 * step) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k + i * step < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(&parts->o[slot(k + i * step)][h][d0]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k + i * step < n) {
+            const float w = wts[warp][k + i * step] * inv;
+            o.x = fmaf(w, v[i].x, o.x);
+            o.y = fmaf(w, v[i].y, o.y);
+            o.z = fmaf(w, v[i].z, o.z);
+            o.w = fmaf(w, v[i].w, o.w);
+          }
       }
+      if (!few) part_sum[warp][lane] = o;
+      if (lane == 0 && quarter == 0 && (few || deal == 0) && g.a.lse != nullptr)
+        g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
     }
-    __syncthreads();
-    const int dd = tid % kJoinDims, gr = tid / kJoinDims, d = kJoinDims * q + dd;
-    float o = 0.0f;
-    int k = gr;
-    for (; k + 7 * kJoinGroups < n; k += 8 * kJoinGroups) {
-      float v[8];
+    if (!few) {
+      __syncthreads();
+      if (deal == 0)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __ldcg(&parts->o[slot(k + e * kJoinGroups)][h][d]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o = fmaf(wt[k + e * kJoinGroups], v[e], o);
+        for (int k = 1; k < 4; ++k) {
+          const float4 v = part_sum[4 * k + quarter][lane];
+          o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        }
+      __syncthreads();
     }
-    for (; k < n; k += kJoinGroups) o = fmaf(wt[k], __ldcg(&parts->o[slot(k)][h][d]), o);
-    osum[gr][dd] = o;
-    __syncthreads();
-    if (gr == 0) {
-      const float tot = (osum[0][dd] + osum[1][dd]) + (osum[2][dd] + osum[3][dd]);
-      g.a.out[int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d] =
-          __bfloat16_as_ushort(__float2bfloat16_rn(lsum > 0.0f ? tot / lsum : 0.0f));
+    if (h < heads && (few || deal == 0)) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+      *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + 128 * quarter +
+                                 4 * lane) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
-    __syncthreads();
+    __syncwarp();  // wts is read
   }
 }
 
@@ -996,6 +1076,7 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
   e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
   if (e != cudaSuccess) return e;
+  if (ctas == 1) return cudaSuccess;  // nothing is split
   return launch_pdl(paged_combine_kernel, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
                     static_cast<const Parts *>(parts), ctas);
 }
