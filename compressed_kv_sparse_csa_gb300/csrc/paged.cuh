@@ -63,7 +63,8 @@ __device__ __forceinline__ int32_t paged_seq_of(const PagedCache &c, int64_t t, 
     lo += k * step;
     n = step < left ? step : left;
   }
-  return int64_t(__ldcg(c.cu + lo)) <= t && t < int64_t(__ldcg(c.cu + lo + 1)) ? lo : -1;
+  const int32_t from = __ldcg(c.cu + lo), to = __ldcg(c.cu + lo + 1);
+  return from <= t && t < to ? lo : -1;
 }
 
 cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const void *in, bool in_bf16,

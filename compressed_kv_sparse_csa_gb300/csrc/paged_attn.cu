@@ -71,7 +71,7 @@ constexpr int kWWarp0 = 4, kWWarps = 16, kXWarp0 = 20, kXWarps = 8;
 constexpr int kXThreads = 32 * kXWarps;
 constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 896
 // registers a thread: at launch, then by role
-constexpr int kRegs = 72, kRegsLM = 56, kRegsW = 64, kRegsX = 96;
+constexpr int kRegs = 72, kRegsLM = 40, kRegsW = 64, kRegsX = 104;
 static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
@@ -110,7 +110,7 @@ static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 struct Parts {
   int32_t unit[2 * kMaxCtas];            // the part's unit, or -1
   float lse2[2 * kMaxCtas][kHeads];      // log2 of the denominator
-  float o[2 * kMaxCtas][kHeads][kDim];   // normalised
+  float o[2 * kMaxCtas][kHeads][kDim];   // normalised, dims as V' has them (v_chunk)
 };
 
 struct Args {
@@ -280,16 +280,13 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   // valid ones is on its way with their rows)
   const int per = (a.n_tokens + kThreads - 1) / kThreads;
   const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
+  const Rows first_rows = t0 < t1 ? token_rows(a, t0) : Rows{0, 0};
   const int valid = __ldcg(a.c.cu + a.c.n_seqs);  // tokens behind are padding
   auto tiles_of = [&](int t) { return t < valid ? rows_tiles(token_rows(a, t).n) : 0; };
-  const int first = t0 < t1 ? tiles_of(t0) : 0;
+  const int first = t0 < min(t1, valid) ? rows_tiles(first_rows.n) : 0;
   long long mine = first;
   for (int t = t0 + 1; t < t1; ++t) mine += tiles_of(t);
   mine *= g.groups;
-  if (blockIdx.x == 0 && a.idx == nullptr)
-    for (int t = t0; t < min(t1, valid); ++t)
-      if (__ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
-        atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -345,7 +342,7 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
           sm.unit0 = t * g.groups + k;
           sm.off0 = int(off);
           if (at < total) {
-            const Rows r = token_rows(a, t);
+            const Rows r = t == t0 ? first_rows : token_rows(a, t);
             sm.row0 = int(r.r0);
             sm.rows = r.n;
           }
@@ -363,6 +360,11 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
     if (run > INT32_MAX - 8) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));  // (months of work)
     sm.total = int(min(run, (long long)(INT32_MAX - 8)));
   }
+  // a range past what the table can place
+  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr)
+    for (int t = t0; t < min(t1, valid); ++t)
+      if (__ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
+        atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   __syncthreads();
 }
 
@@ -377,7 +379,7 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
   for (;;) {
     const int t = w.unit / g.groups;
     int seq = -1;
-    int64_t n_rows = 0;
+    int n_rows = 0;
     bool fresh = true;
     for (int i = w.i0; i < w.i1; ++i) {
       const int pos = (w.off + (i - w.i0)) * kTile + lane;
@@ -390,25 +392,23 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
       }
       if (fresh) {  // (looked up while the first entries are on their way)
         seq = paged_seq_of(a.c, t, lane);
-        n_rows = a.idx != nullptr && seq >= 0 ? int64_t(__ldcg(a.n_rows + seq)) : 0;
+        n_rows = a.idx != nullptr && seq >= 0 ? int(min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + seq)))) : INT32_MAX;
         fresh = false;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (seq < 0) row[k] = -1;
-        if (a.idx != nullptr && row[k] >= n_rows) row[k] = -2;
       }
       int2 at[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        if (seq < 0) row[k] = -1;
         const int j = row[k] >> a.c.page_log2;
         const bool in = row[k] >= 0 && j < a.c.seq_pages;
         const int32_t page = in ? __ldcg(a.c.table + int64_t(seq) * a.c.table_stride + j) : -1;
         at[k] = make_int2(page < a.c.n_pages ? max(page, -1) : -1, row[k] & ((1 << a.c.page_log2) - 1));
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        if (row[k] >= n_rows) at[k].x = -1;
         if (row[k] != -1 && at[k].x < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      }
       // toward L2: a row's code lines (224 bytes lie in two or three) and RoPE line
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -555,11 +555,13 @@ __device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader 
       wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
       fence_proxy_async_smem();
       tc_fence_after();
-      // K step ks: 16 dims, 32 bytes into panel ks / 4 (descriptor addresses count 16 bytes)
+      // K step 4 p + ks: 16 dims, 32 ks bytes into panel p (descriptor addresses count 16 bytes)
+#pragma unroll 1
+      for (uint32_t p = 0; p < kDim / 64; ++p)
 #pragma unroll
-      for (int ks = 0; ks < kDim / 16; ++ks)
-        mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)),
-                   dS_b + uint64_t(512 * (ks >> 2) + 2 * (ks & 3)), idS, ks > 0 ? 1u : 0u);
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_f16_ss(tmem + kSCol + 64u * b, dS_a + uint64_t(512 * p + 2 * ks), dS_b + uint64_t(512 * p + 2 * ks), idS,
+                     p + ks);
       tc_commit(smem_u32(&sm.sfull[b]));
     }
     if (w.i1 >= total) break;
@@ -620,9 +622,9 @@ __device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, in
   for (int i = 0; i < 16; ++i) {
     const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) m = max(m, max(w4[u] & 0x7fffu, (w4[u] >> 16) & 0x7fffu));
+    for (int u = 0; u < 4; ++u) m = __vmaxu2(m, w4[u] & 0x7fff7fffu);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
   const int slot = seg % 3;
   if (lane == 0) atomicMax(&sm.qmax[slot], m);
   // the next unit's slot: its last readers (three units ago) passed the previous unit's barrier
@@ -827,7 +829,7 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
         for (int j = 0; j < 2; ++j) {
           const int hc = 32 * half + 16 * j;  // heads hc .. hc + 15
           if (!whole) {
-            float *po = &parts->o[part][hc][d];
+            float *po = &parts->o[part][hc][128 * k + 32 * qd + lane];
 #pragma unroll
             for (int u = 0; u < 16; ++u)
               if (hc + u < heads) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
@@ -1043,8 +1045,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
     }
     if (h < heads && (few || deal == 0)) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-      *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + 128 * quarter +
-                                 4 * lane) =
+      const int d = 8 * v_chunk_back(16 * quarter + (lane >> 1)) + 4 * (lane & 1);
+      *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
     __syncwarp();  // wts is read
