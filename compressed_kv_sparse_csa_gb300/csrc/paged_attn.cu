@@ -67,11 +67,11 @@ constexpr int kDim = DS4X_KV_DIM;  // 512
 constexpr int kTile = 64;          // rows a tile
 constexpr int kHeads = 64;         // heads a unit, at most
 constexpr int kMWarp0 = 1;                           // S of even tiles, S of odd tiles, O
-constexpr int kWWarp0 = 4, kWWarps = 16, kXWarp0 = 20, kXWarps = 8;
+constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 12, kXWarps = 8;
 constexpr int kXThreads = 32 * kXWarps;
-constexpr int kThreads = 32 * (kXWarp0 + kXWarps);   // 896
+constexpr int kThreads = 32 * (kXWarp0 + kXWarps);  // 640
 // registers a thread: at launch, then by role
-constexpr int kRegs = 72, kRegsLM = 40, kRegsW = 64, kRegsX = 104;
+constexpr int kRegs = 96, kRegsLM = 64, kRegsW = 96, kRegsX = 104;
 static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
@@ -80,21 +80,21 @@ constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
 constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
-constexpr int kNoRow = INT32_MIN;  // rowe of a row that is not there
+constexpr int kTame = 20;
 enum { kBarX = 1 };               // named barrier
 
 struct __align__(1024) Smem {
   uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
   uint8_t v[2][kTile * kDim * 2];   // V': 8 panels of 8 KB, two tiles
   uint8_t p[2][kTile * kHeads * 2]; // P^T: one panel, two tiles
-  int rowe[2][kTile];               // E_j, or kNoRow
+  float4 rowe[2][kTile];            // 2^E_j, E_j, 2^-E_j, E_j; a row that is not there: 0, -inf, 0, 0
   int2 found[kAhead][kTile];        // a row's page (-1: no row) and its number there
   float red[4][kHeads];
   float alpha[kHeads];
   float mh[kHeads], hinv[kHeads];
   float qbase[2];                   // scale log2 e 2^-c, by segment parity
   uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
-  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2], lfull[kAhead], lfree[kAhead], qfull, drain;
+  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2][2], lfull[kAhead], lfree[kAhead], qfull, drain;
   long long scan[kThreads / 32];
   long long cut0, cut1;             // the CTA's run of tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
@@ -102,6 +102,7 @@ struct __align__(1024) Smem {
   int total;                        // its tiles
   uint32_t tmem_base;
   int abort_flag;
+  int wide;                         // a row so far has an exponent beyond +-kTame
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
@@ -481,23 +482,27 @@ __device__ __forceinline__ void widen8(uint32_t addr, uint32_t w, uint32_t f) {
       : "r"(w));
   sts16(addr, hmul2_bits(h0, f), hmul2_bits(h1, f), hmul2_bits(h2, f), hmul2_bits(h3, f));
 }
-// A row (at `row`) of V': x = 16 (row % 8).
-__device__ __forceinline__ void widen(uint32_t row, uint32_t x, int l, const uint32_t (&off_b)[4], const Raw &w) {
+// A row (at `row`) of V', x = 16 (row % 8): panels 0 to 3, then 4 to 7.
+__device__ __forceinline__ void widen_low(uint32_t row, uint32_t x, int l, const Raw &w) {
   const int E = int((w.sc.w >> 16) & 0xffu);
-  const uint32_t sh = 8 * (l & 3);
-  const uint32_t fa = pow2_half_bits(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> sh) & 0xffu) - E)) * 0x10001u;
+  const uint32_t f =
+      pow2_half_bits(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> (8 * (l & 3))) & 0xffu) - E)) * 0x10001u;
   const uint32_t pa = row + (uint32_t(l << 4) ^ x);
-  widen8(pa, w.a.x, fa);
-  widen8(pa + 8192, w.a.y, fa);
-  widen8(pa + 2 * 8192, w.a.z, fa);
-  widen8(pa + 3 * 8192, w.a.w, fa);
-  sts16(pa + 7 * 8192, w.t.x, w.t.y, w.t.z, w.t.w);
+  widen8(pa, w.a.x, f);
+  widen8(pa + 8192, w.a.y, f);
+  widen8(pa + 2 * 8192, w.a.z, f);
+  widen8(pa + 3 * 8192, w.a.w, f);
+}
+__device__ __forceinline__ void widen_high(uint32_t row, uint32_t x, int l, const uint32_t (&off_b)[4], const Raw &w) {
+  const int E = int((w.sc.w >> 16) & 0xffu);
+  sts16(row + 7 * 8192 + (uint32_t(l << 4) ^ x), w.t.x, w.t.y, w.t.z, w.t.w);
   if (l < 6) {
-    const uint32_t fb = pow2_half_bits(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> sh) & 0xffu) - E)) * 0x10001u;
-    widen8(row + (off_b[0] ^ x), w.b.x, fb);
-    widen8(row + (off_b[1] ^ x), w.b.y, fb);
-    widen8(row + (off_b[2] ^ x), w.b.z, fb);
-    widen8(row + (off_b[3] ^ x), w.b.w, fb);
+    const uint32_t f =
+        pow2_half_bits(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> (8 * (l & 3))) & 0xffu) - E)) * 0x10001u;
+    widen8(row + (off_b[0] ^ x), w.b.x, f);
+    widen8(row + (off_b[1] ^ x), w.b.y, f);
+    widen8(row + (off_b[2] ^ x), w.b.z, f);
+    widen8(row + (off_b[3] ^ x), w.b.w, f);
   }
 }
 
@@ -505,29 +510,43 @@ __device__ __forceinline__ void role_w(const Args &g, Smem &sm, WsHeader *hdr) {
   const int total = sm.total;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
   const int l = lane & 7, q = lane >> 3;
-  const int r = 4 * warp + q;            // the tile's row that this lane helps to widen
+  const int r = 8 * warp + q;            // the tile's rows that this lane helps to widen: r and r + 4
   uint32_t off_b[4];                     // block 8 + l's words, within a row
 #pragma unroll
   for (int u = 0; u < 4; ++u) off_b[u] = uint32_t(4 + ((l + 6 * u) >> 3)) * 8192u + (uint32_t((l + 6 * u) & 7) << 4);
-  const uint32_t row0 = smem_u32(sm.v[0]) + r * 128;
-  auto load = [&](int i, Raw &raw) {
+  const uint32_t row0 = smem_u32(sm.v[0]) + r * 128, x = uint32_t(q) << 4;
+  auto load = [&](int i, Raw (&raw)[2]) {
     if (i >= total) return;
     const int slot = i % kAhead;
     wait_bar(sm, &sm.lfull[slot], (i / kAhead) & 1, hdr);
-    const int2 at = sm.found[slot][r];
+    const int2 at0 = sm.found[slot][r], at1 = sm.found[slot][r + 4];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.lfree[slot]));
-    load_raw(g.a.c, at, l, raw);
+    load_raw(g.a.c, at0, l, raw[0]);
+    load_raw(g.a.c, at1, l, raw[1]);
   };
-  auto tile = [&](int i, int buf, Raw &raw) {
-    if (i >= 2) wait_bar(sm, &sm.pvdone[buf], ((i >> 1) - 1) & 1, hdr);
-    widen(row0 + 65536u * buf, uint32_t(r & 7) << 4, l, off_b, raw);
-    if (l == 0) sm.rowe[buf][r] = raw.sc.w >> 24 ? kNoRow : int((raw.sc.w >> 16) & 0xffu) - 127;
+  auto tile = [&](int i, int buf, Raw (&raw)[2]) {
+    const uint32_t row = row0 + 65536u * buf;
+    // the buffer's lower and upper panels come free one after the other
+    if (i >= 2) wait_bar(sm, &sm.pvdone[buf][0], ((i >> 1) - 1) & 1, hdr);
+    widen_low(row, x, l, raw[0]);
+    widen_low(row + 4 * 128, x ^ 64u, l, raw[1]);
+    if (i >= 2) wait_bar(sm, &sm.pvdone[buf][1], ((i >> 1) - 1) & 1, hdr);
+    widen_high(row, x, l, off_b, raw[0]);
+    widen_high(row + 4 * 128, x ^ 64u, l, off_b, raw[1]);
+    if (l < 2) {
+      const uint32_t scw = l ? raw[1].sc.w : raw[0].sc.w;
+      const int E = int((scw >> 16) & 0xffu) - 127;
+      const bool none = scw >> 24;
+      sm.rowe[buf][r + 4 * l] = none ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                                     : make_float4(pow2f(E), float(E), pow2f(-E), float(E));
+      if (!none && (E > kTame || E < -kTame)) sm.wide = 1;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
     load(i + 2, raw);
   };
-  Raw even, odd;
+  Raw even[2], odd[2];
   load(0, even);
   load(1, odd);
   for (int i = 0; i < total; i += 2) {
@@ -556,7 +575,7 @@ __device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader 
       fence_proxy_async_smem();
       tc_fence_after();
       // K step 4 p + ks: 16 dims, 32 ks bytes into panel p (descriptor addresses count 16 bytes)
-#pragma unroll 1
+#pragma unroll 2
       for (uint32_t p = 0; p < kDim / 64; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
@@ -589,12 +608,13 @@ __device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
       const uint32_t acc = i > w.i0 ? 1u : 0u;
       // M tile mi: panels 2 mi, 2 mi + 1; K step ks: 16 rows (2 KB)
 #pragma unroll
-      for (int mi = 0; mi < kDim / 128; ++mi)
+      for (int mi = 0; mi < kDim / 128; ++mi) {
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
           mma_f16_ss(tmem + kOCol + 64u * mi, dO_a + uint64_t(1024 * mi + 128 * ks), dO_b + uint64_t(128 * ks), idO,
                      ks > 0 ? 1u : acc);
-      tc_commit(smem_u32(&sm.pvdone[b]));
+        if (mi & 1) tc_commit(smem_u32(&sm.pvdone[b][mi >> 1]));  // the lower panels are read, all are
+      }
     }
     if (w.i1 >= total) break;
     w.next(g, total);
@@ -671,18 +691,18 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       const int b = i & 1;
       wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
       tc_fence_after();
-      float d[16], er[2];  // x - m of row r0 + 8 r: d[4 j + 2 r + c]; the rows' E_j
-      float over = -INFINITY, under = 0.0f;
+      float d[16];  // x - m of row r0 + 8 r: d[4 j + 2 r + c]
+      float inv[2] = {0.0f, 0.0f}, er[2] = {0.0f, 0.0f};  // the rows' 2^-E_j, E_j
+      float over = -INFINITY;
+      const bool wide = *reinterpret_cast<volatile int *>(&sm.wide) != 0;
       if (i == w.i0) base = sm.qbase[seg & 1];
       if (busy) {
         uint32_t s[16];
         tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
-        const int e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
-        // a row that is not there: x = -inf, weight 0
-        const float f[2] = {e0 == kNoRow ? 0.0f : base * pow2f(e0), e1 == kNoRow ? 0.0f : base * pow2f(e1)};
-        const float ef[2] = {e0 == kNoRow ? -INFINITY : float(e0), e1 == kNoRow ? -INFINITY : float(e1)};
-        er[0] = e0 == kNoRow ? 0.0f : float(e0);
-        er[1] = e1 == kNoRow ? 0.0f : float(e1);
+        const float4 e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
+        const float f[2] = {base * e0.x, base * e1.x}, ef[2] = {e0.y, e1.y};  // (not there: x = -inf, weight 0)
+        inv[0] = e0.z, inv[1] = e1.z;
+        er[0] = e0.w, er[1] = e1.w;
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -693,7 +713,6 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
           d[k] = x.x;
           d[k + 1] = x.y;
           over = fmaxf(fmaxf(over, d[k]), d[k + 1]);
-          under = fminf(fminf(under, d[k]), d[k + 1]);
         }
       }
       if (named_bar_or(kBarX, kXThreads, over > kLazy || fresh)) {
@@ -724,12 +743,11 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
             if (qd == 0 && lane < 4) sm.alpha[h] = ex2(-up);
           }
           fresh = fresh && none;
-          under = -INFINITY;
         }
         named_bar_sync(kBarX, kXThreads);
         if (i > w.i0 && busy) {
           // O^T of the unit so far, once the previous tile's product is done
-          wait_bar(sm, &sm.pvdone[b ^ 1], ((i - 1) >> 1) & 1, hdr);
+          wait_bar(sm, &sm.pvdone[b ^ 1][1], ((i - 1) >> 1) & 1, hdr);
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < 2 * kDim / 128; ++k) {
@@ -746,17 +764,16 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
         }
       }
       if (busy) {
-        // a weight far below 1 may underflow although its part of the denominator,
-        // 2^-E_j as large, does not: then that is formed by itself
-        const bool apart = __any_sync(0xffffffffu, under < -100.0f);
-        if (apart) {
+        // Rows of very different size: a weight 2^(l_j + E_j - m) may underflow although
+        // its part of the denominator, 2^-E_j as large, does not; then that is formed by
+        // itself.  (While all |E_j| <= kTame a lost part is below 2^-86 of the whole.)
+        if (wide) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) sum[2 * (k >> 2) + (k & 1)] += ex2(d[k] - er[(k >> 1) & 1]);
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) d[k] = ex2(d[k]);
-        if (!apart) {
-          const float inv[2] = {pow2f(-int(er[0])), pow2f(-int(er[1]))};
+        if (!wide) {
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             const int row = (k >> 1) & 1, h = 2 * (k >> 2);
@@ -812,7 +829,7 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
     }
     if (xt == 0 && !whole) parts->unit[part] = w.unit;
     named_bar_sync(kBarX, kXThreads);
-    wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1], ((w.i1 - 1) >> 1) & 1, hdr);
+    wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1][1], ((w.i1 - 1) >> 1) & 1, hdr);
     tc_fence_after();
     // O^T, 32 heads by 128 dims a step.  (The loads of a step are waited for before
     // the loop goes round: a register that a load is still to write must not be moved.)
@@ -866,7 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
       mbar_init(smem_u32(&sm.vfull[b]), kWWarps);
       mbar_init(smem_u32(&sm.sfull[b]), 1);
       mbar_init(smem_u32(&sm.pfull[b]), kXWarps);
-      mbar_init(smem_u32(&sm.pvdone[b]), 1);
+      mbar_init(smem_u32(&sm.pvdone[b][0]), 1);
+      mbar_init(smem_u32(&sm.pvdone[b][1]), 1);
     }
     for (int k = 0; k < kAhead; ++k) {
       mbar_init(smem_u32(&sm.lfull[k]), 1);
@@ -874,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
     }
     mbar_init(smem_u32(&sm.qfull), kXWarps);
     mbar_init(smem_u32(&sm.drain), 3);
-    sm.abort_flag = 0;
+    sm.abort_flag = sm.wide = 0;
     sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
     fence_mbar_init();
   }
