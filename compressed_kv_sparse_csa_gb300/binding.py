@@ -441,58 +441,61 @@ _ELEMENT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 def _paged(pages, page_rows, table, cu_tokens, ws):
-    """The cache's arguments, common to the paged calls: (pages, n_pages,
-    page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens)."""
-    _check(pages, torch.uint8, "pages")
-    _check(cu_tokens, torch.int32, "cu_tokens")
-    _check(ws, torch.uint8, "ws")
-    dev = pages.device
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
-        raise ValueError("table must be a CUDA int32 [n_seqs, seq_pages] tensor with contiguous rows")
-    if dev != table.device or dev != cu_tokens.device or dev != ws.device:
-        raise ValueError("pages, table, cu_tokens and ws must be on one device")
+    """The device index and the cache's arguments, common to the paged calls:
+    (pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride,
+    cu_tokens).  The library launches on the current device, so everything
+    has to be there."""
+    dev = pages.get_device()
+    if dev < 0:
+        raise ValueError("pages must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"pages is on device {dev}, the current device is {torch.cuda.current_device()}")
+    if table.get_device() != dev or table.dtype != torch.int32 or table.dim() != 2:
+        raise ValueError("table must be an int32 [n_seqs, seq_pages] tensor on the pages' device")
     n_seqs, seq_pages = table.shape
-    if cu_tokens.numel() != n_seqs + 1:
-        raise ValueError(f"cu_tokens holds {cu_tokens.numel()} entries, needs {n_seqs + 1}")
+    if table.stride(1) != 1 and seq_pages > 1:
+        raise ValueError("table's rows must be contiguous")
     if not 0 < page_rows <= 256:
         raise ValueError("page_rows must be 16, 32, 64, 128 or 256")
     n_pages, rest = divmod(pages.numel(), page_rows * 368)
     if rest:
         raise ValueError(f"pages must hold whole pages of {page_rows} * 368 bytes")
-    return (pages.data_ptr(), n_pages, page_rows, table.data_ptr(), n_seqs, seq_pages,
-            table.stride(0) if n_seqs > 1 else seq_pages, cu_tokens.data_ptr())
+    _per(ws, torch.uint8, "ws", None, dev)
+    return dev, (_per(pages, torch.uint8, "pages", None, dev), n_pages, page_rows, table.data_ptr(), n_seqs, seq_pages,
+                 table.stride(0) if n_seqs > 1 else seq_pages, _per(cu_tokens, torch.int32, "cu_tokens", n_seqs + 1, dev))
 
 
 def _per(t, dtype, name, count, dev):
-    """A contiguous tensor of one value a token or a sequence; its address."""
-    _check(t, dtype, name)
-    if t.numel() != count:
-        raise ValueError(f"{name} holds {t.numel()} elements, needs {count}")
-    if t.device != dev:
+    """A contiguous tensor of `count` elements (None: any number) on device
+    dev; its address."""
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the pages' device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} holds {t.numel()} elements, needs {count}")
     return t.data_ptr()
 
 
 def _strided(t, name, dims, dtypes, dev):
     """A tensor of vectors whose dimensions behind the first are contiguous:
-    its stride from token to token, in elements."""
-    if not t.is_cuda or t.device != dev:
+    its shape and its stride from token to token, in elements."""
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the pages' device")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != dims or t.shape[-1] != 512:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims or shape[-1] != 512:
         raise ValueError(f"{name} must be {dims}-dimensional with 512 values a vector")
-    if t.stride(-1) != 1 or (dims == 3 and t.shape[1] > 1 and t.stride(1) != 512):
+    if stride[-1] != 1 or (dims == 3 and shape[1] > 1 and stride[1] != 512):
         raise ValueError(f"{name} must be contiguous behind its first dimension")
-    return t.stride(0) if t.shape[0] > 1 else 512 * (t.shape[1] if dims == 3 else 1)
+    return shape, stride[0] if shape[0] > 1 else 512 * (shape[1] if dims == 3 else 1)
 
 
-def _on(dev, stream):
-    """The stream handle of a paged call: `stream`, or the pages' device's
-    current one.  The library launches on the current device."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
-    return _stream(stream)
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def ds4x_paged_append(pages, page_rows, table, cu_tokens, row0, kv_in, ws, pos=None, inv_freq=None, rope_style=0,
@@ -502,24 +505,21 @@ def ds4x_paged_append(pages, page_rows, table, cu_tokens, row0, kv_in, ws, pos=N
     [n_pages, page_rows * 368], table int32 [n_seqs, seq_pages], cu_tokens
     int32 [n_seqs + 1], row0 int64 [n_seqs], pos int64 [n] or None (the row's
     number), inv_freq f32 [32] or None (no rotation), ws u8 >= 256 bytes."""
-    cache = _paged(pages, page_rows, table, cu_tokens, ws)
-    dev = pages.device
-    stride = _strided(kv_in, "kv_in", 2, (torch.float32, torch.bfloat16), dev)
-    n = kv_in.shape[0]
+    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    (n, _), stride = _strided(kv_in, "kv_in", 2, (torch.float32, torch.bfloat16), dev)
     _call("ds4x_paged_append", *cache, _per(row0, torch.int64, "row0", cache[4], dev), kv_in.data_ptr(),
           _ELEMENT_TYPES[kv_in.dtype], stride, n, None if pos is None else _per(pos, torch.int64, "pos", n, dev),
           None if inv_freq is None else _per(inv_freq, torch.float32, "inv_freq", 32, dev), int(rope_style),
-          ws.data_ptr(), ws.numel(), _on(dev, stream))
+          ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_gather(pages, page_rows, table, cu_tokens, row0, out, ws, stream=None):
     """Read rows back into out f32 or bf16 [n, 512] (rows may be strided):
     token j of sequence s gets the sequence's row row0[s] + j."""
-    cache = _paged(pages, page_rows, table, cu_tokens, ws)
-    dev = pages.device
-    stride = _strided(out, "out", 2, (torch.float32, torch.bfloat16), dev)
+    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    (n, _), stride = _strided(out, "out", 2, (torch.float32, torch.bfloat16), dev)
     _call("ds4x_paged_gather", *cache, _per(row0, torch.int64, "row0", cache[4], dev), out.data_ptr(),
-          _ELEMENT_TYPES[out.dtype], stride, out.shape[0], ws.data_ptr(), ws.numel(), _on(dev, stream))
+          _ELEMENT_TYPES[out.dtype], stride, n, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_attn_workspace() -> int:
@@ -528,11 +528,10 @@ def ds4x_paged_attn_workspace() -> int:
 
 def _paged_qo(q, out, lse, dev):
     """(n_tokens, n_heads, q stride, out stride, lse address)"""
-    qs = _strided(q, "q", 3, (torch.bfloat16,), dev)
-    os = _strided(out, "out", 3, (torch.bfloat16,), dev)
-    n, heads = q.shape[:2]
-    if out.shape != q.shape:
-        raise ValueError(f"out is {tuple(out.shape)}, q is {tuple(q.shape)}")
+    (n, heads, _), qs = _strided(q, "q", 3, (torch.bfloat16,), dev)
+    shape, os = _strided(out, "out", 3, (torch.bfloat16,), dev)
+    if shape != q.shape:
+        raise ValueError(f"out is {tuple(shape)}, q is {tuple(q.shape)}")
     return n, heads, qs, os, None if lse is None else _per(lse, torch.float32, "lse", n * heads, dev)
 
 
@@ -542,23 +541,21 @@ def ds4x_paged_attn(pages, page_rows, table, cu_tokens, row_end, q, softmax_scal
     [row_begin, row_end) (int64 [n] each; row_begin None: 0) of its sequence;
     out bf16 [n, heads, 512], lse f32 [n, heads] or None, ws u8 of
     ds4x_paged_attn_workspace() bytes.  q and out may be strided by token."""
-    cache = _paged(pages, page_rows, table, cu_tokens, ws)
-    dev = pages.device
+    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     n, heads, qs, os, lp = _paged_qo(q, out, lse, dev)
     _call("ds4x_paged_attn", *cache, None if row_begin is None else _per(row_begin, torch.int64, "row_begin", n, dev),
           _per(row_end, torch.int64, "row_end", n, dev), n, heads, q.data_ptr(), qs, float(softmax_scale),
-          out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _on(dev, stream))
+          out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_sparse_attn(pages, page_rows, table, cu_tokens, n_rows, idx, q, softmax_scale, out, lse, ws,
                            stream=None):
     """Attention of each token q bf16 [n, heads, 512] over its own rows idx
     int32 [n, k] of its sequence (n_rows int64 [n_seqs] rows; -1 skipped)."""
-    cache = _paged(pages, page_rows, table, cu_tokens, ws)
-    dev = pages.device
+    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     n, heads, qs, os, lp = _paged_qo(q, out, lse, dev)
     if idx.dim() != 2 or idx.shape[0] != n:
         raise ValueError("idx must be int32 [n_tokens, k]")
     _call("ds4x_paged_sparse_attn", *cache, _per(n_rows, torch.int64, "n_rows", cache[4], dev),
           _per(idx, torch.int32, "idx", idx.numel(), dev), idx.shape[1], n, heads, q.data_ptr(), qs,
-          float(softmax_scale), out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _on(dev, stream))
+          float(softmax_scale), out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))

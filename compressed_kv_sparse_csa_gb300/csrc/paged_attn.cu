@@ -119,6 +119,7 @@ struct Args {
   int32_t groups;     // head groups a token
   int32_t group;      // heads a group (the last may have fewer)
   int32_t n_cols;     // `group` rounded up to 16: the products' N
+  uint64_t per_grid;  // 2^64 / gridDim.x, rounded up
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -306,12 +307,15 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   }
   const long long total = __shfl_sync(0xffffffffu, wi, 31);
   const long long before = __shfl_sync(0xffffffffu, wi - ws, warp) + incl - mine;
-  // every CTA of the first G has a tile
-  const unsigned G = unsigned(max(1ll, min((long long)gridDim.x, total)));
-  auto part = [&](unsigned c) {  // c total / G, in 32 bits where they do (total < 2^43, G <= 160)
-    return total < (1 << 24) ? (long long)(c * unsigned(total) / G) : (long long)(c * (unsigned long long)total / G);
+  // Cut c is at c total / gridDim.x, so that every CTA has a tile, or, with fewer
+  // tiles than CTAs, at c.  (total < 2^43 and c <= 160: the high word of the product
+  // with the rounded-up reciprocal is the quotient.)
+  const bool plenty = total >= (long long)(gridDim.x);
+  auto part = [&](unsigned c) {
+    if (c >= gridDim.x) return total;
+    return plenty ? (long long)(__umul64hi(c * (unsigned long long)total, g.per_grid)) : min((long long)c, total);
   };
-  const long long tol = total < (1 << 24) ? (long long)(unsigned(total) / (16 * G)) : total / (16 * G);
+  const long long tol = plenty ? (long long)(__umul64hi((unsigned long long)total, g.per_grid) >> 4) : 0;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const long long x = part(blockIdx.x + e);
@@ -938,10 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
 }
 
 // Joins the parts of the units that several CTAs share.  A warp takes 128 dims (a
-// float4 a lane) of a head; a block of 16 warps takes four heads where the unit
-// has at most 16 parts, else one head with its parts dealt over four warps (one
-// unit split over every CTA has only 64 heads to go round).  Sums go in a fixed
-// order.
+// float4 a lane) of a head, eight parts on their way at once.  Where the unit has at
+// most 16 parts, a block's 16 warps take four heads; else 128 dims of one head, its
+// parts dealt over them (a unit split over every CTA has 64 heads to go round: 256
+// blocks then read 9 or 10 parts a warp).  Sums go in a fixed order.
 constexpr int kJoinWarps = 16, kJoinThreads = 32 * kJoinWarps, kJoinFew = 16;
 
 __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, const Parts *__restrict__ parts,
@@ -989,7 +993,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
           }
         count[e] = c - first[e];
         const int h0 = (unit[2 * first[e] + 1] % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
-        mine = count[e] <= kJoinFew ? (heads + 3) / 4 : heads;
+        mine = count[e] <= kJoinFew ? (heads + 3) / 4 : 4 * heads;
       }
       int incl = mine;
 #pragma unroll
@@ -1012,9 +1016,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
     const int c0 = first[e], n = count[e], u = unit[2 * c0 + 1];
     const int t = u / g.groups, h0 = (u % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
     const bool few = n <= kJoinFew;
-    const int quarter = warp & 3, deal = warp >> 2;
-    const int h = few ? 4 * (item - item0[e]) + deal : item - item0[e];
-    const int k0 = few ? 0 : deal, step = few ? 1 : 4;
+    const int it = item - item0[e], quarter = few ? warp & 3 : it & 3;
+    const int h = few ? 4 * it + (warp >> 2) : it >> 2;
+    const int k0 = few ? 0 : warp, step = few ? 1 : kJoinWarps;
+    const bool writes = few || warp == 0;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (h < heads) {  // (a block's warps differ in it only where few)
       auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
@@ -1048,20 +1053,20 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
           }
       }
       if (!few) part_sum[warp][lane] = o;
-      if (lane == 0 && quarter == 0 && (few || deal == 0) && g.a.lse != nullptr)
+      if (lane == 0 && quarter == 0 && writes && g.a.lse != nullptr)
         g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
     }
     if (!few) {
       __syncthreads();
-      if (deal == 0)
+      if (warp == 0)
 #pragma unroll
-        for (int k = 1; k < 4; ++k) {
-          const float4 v = part_sum[4 * k + quarter][lane];
+        for (int k = 1; k < kJoinWarps; ++k) {
+          const float4 v = part_sum[k][lane];
           o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
         }
       __syncthreads();
     }
-    if (h < heads && (few || deal == 0)) {
+    if (h < heads && writes) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
       const int d = 8 * v_chunk_back(16 * quarter + (lane >> 1)) + 4 * (lane & 1);
       *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
@@ -1085,13 +1090,14 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0};
+  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0};
   g.group = (a.n_heads + g.groups - 1) / g.groups;
   g.n_cols = (g.group + 15) / 16 * 16;
   // no more CTAs than there can be tiles
   const int64_t rows = a.idx != nullptr ? a.k : int64_t(a.c.seq_pages) << a.c.page_log2;
   const int64_t most = int64_t(a.n_tokens) * g.groups * ((rows + kTile - 1) / kTile);
   const int ctas = int(most < sms ? most : sms) < kMaxCtas ? int(most < sms ? most : sms) : kMaxCtas;
+  g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
   WsHeader *hdr = static_cast<WsHeader *>(ws);
   Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
   e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
