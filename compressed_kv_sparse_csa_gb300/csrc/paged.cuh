@@ -50,8 +50,12 @@ __device__ __forceinline__ int64_t paged_scale_off(const PagedCache &c, const Pa
 }
 
 // The sequence of token t: the s with cu[s] <= t < cu[s + 1], or -1 (padding,
-// or a cu that is not what it should be).  One warp searches, 32 ways a step.
-__device__ __forceinline__ int32_t paged_seq_of(const PagedCache &c, int64_t t, int lane) {
+// or a cu that is not what it should be); its first token and the one behind its
+// last.  One warp searches, 32 ways a step.
+struct PagedSeq {
+  int32_t s, from, to;
+};
+__device__ __forceinline__ PagedSeq paged_seq_of(const PagedCache &c, int64_t t, int lane) {
   int32_t lo = 0, n = c.n_seqs;  // the answer, if any, is in [lo, lo + n)
   while (n > 1) {
     const int32_t step = (n + 31) / 32;
@@ -64,7 +68,7 @@ __device__ __forceinline__ int32_t paged_seq_of(const PagedCache &c, int64_t t, 
     n = step < left ? step : left;
   }
   const int32_t from = __ldcg(c.cu + lo), to = __ldcg(c.cu + lo + 1);
-  return from <= t && t < to ? lo : -1;
+  return PagedSeq{from <= t && t < to ? lo : -1, from, to};
 }
 
 cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const void *in, bool in_bf16,

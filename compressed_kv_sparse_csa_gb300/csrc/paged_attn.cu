@@ -81,7 +81,7 @@ constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 constexpr int kTame = 20;
-enum { kBarX = 1 };               // named barrier
+enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 
 struct __align__(1024) Smem {
   uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
@@ -103,6 +103,7 @@ struct __align__(1024) Smem {
   uint32_t tmem_base;
   int abort_flag;
   int wide;                         // a row so far has an exponent beyond +-kTame
+  int end_unit, end_part;           // the CTA's last unit, and its part (-1: the whole unit)
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
@@ -396,7 +397,7 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
           row[k] = a.idx != nullptr ? __ldcg(a.idx + int64_t(t) * a.k + pos + 32 * k) : w.r0 + pos + 32 * k;
       }
       if (fresh) {  // (looked up while the first entries are on their way)
-        seq = paged_seq_of(a.c, t, lane);
+        seq = paged_seq_of(a.c, t, lane).s;
         n_rows = a.idx != nullptr && seq >= 0 ? int(min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + seq)))) : INT32_MAX;
         fresh = false;
       }
@@ -510,7 +511,48 @@ __device__ __forceinline__ void widen_high(uint32_t row, uint32_t x, int l, cons
   }
 }
 
-__device__ __forceinline__ void role_w(const Args &g, Smem &sm, WsHeader *hdr) {
+// A unit's output (part -1), or its part: O^T over the denominator, M tiles k0 .. k1
+// - 1, 128 dims each, by 32 heads (`half`); the warp's dims are 32 qd .. of each M
+// tile.  (A step's loads are waited for before the loop goes round: a register that a
+// load is still to write must not be moved.)
+__device__ __forceinline__ void store_output(const Args &g, Smem &sm, uint32_t tmem, Parts *parts, int unit, int part,
+                                             int qd, int half, int k0, int k1) {
+  const int lane = threadIdx.x & 31;
+  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
+  const int heads = min(g.group, g.a.n_heads - h0);
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) {
+    uint32_t o[2][16];
+    const uint32_t ta = tmem + (uint32_t(32 * qd) << 16) + kOCol + 64u * k + 32u * half;
+    tc_ld_x16(ta, o[0]);
+    tc_ld_x16(ta + 16u, o[1]);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int hc = 32 * half + 16 * j;  // heads hc .. hc + 15
+      if (part >= 0) {
+        float *po = &parts->o[part][hc][128 * k + 32 * qd + lane];
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          if (hc + u < heads) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
+      } else {
+        // neighbouring lanes swap one of two heads, so each stores two dims of one head
+        const int odd = lane & 1, d = 8 * v_chunk_back(16 * k + 4 * qd + (lane >> 3)) + (lane & 6);
+        uint16_t *out = g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + hc + odd) * kDim + d;
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) {
+          const float v0 = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
+          const float v1 = __uint_as_float(o[j][u + 1]) * sm.hinv[hc + u + 1];
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+          const __nv_bfloat162 pr = odd ? __floats2bfloat162_rn(got, v1) : __floats2bfloat162_rn(v0, got);
+          if (hc + u + odd < heads) *reinterpret_cast<__nv_bfloat162 *>(out + u * kDim) = pr;
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void role_w(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const int total = sm.total;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
   const int l = lane & 7, q = lane >> 3;
@@ -557,6 +599,14 @@ __device__ __forceinline__ void role_w(const Args &g, Smem &sm, WsHeader *hdr) {
     tile(i, 0, even);
     if (i + 1 < total) tile(i + 1, 1, odd);
   }
+  // half of the last unit's output (a lone small call waits for little else)
+  named_bar_sync(kBarEnd, kXThreads + 32 * kWWarps);
+  const int half = warp >> 2, end = total - 1;
+  wait_bar(sm, &sm.pvdone[end & 1][1], (end >> 1) & 1, hdr);
+  tc_fence_after();
+  if (32 * half < g.n_cols)
+    store_output(g, sm, sm.tmem_base, parts, sm.end_unit, sm.end_part, warp & 3, half, kDim / 256, kDim / 128);
+  tc_fence_before();
 }
 
 // ---- M: the products --------------------------------------------------------------
@@ -814,7 +864,8 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       }
     }
     // the next unit's Q' (this one's last first product is done: its softmax is)
-    if (w.i1 < total) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
+    const bool last = w.i1 >= total;
+    if (!last) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
     named_bar_sync(kBarX, kXThreads);
     const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
     const int heads = min(g.group, a.n_heads - h0);
@@ -835,41 +886,14 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
     named_bar_sync(kBarX, kXThreads);
     wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1][1], ((w.i1 - 1) >> 1) & 1, hdr);
     tc_fence_after();
-    // O^T, 32 heads by 128 dims a step.  (The loads of a step are waited for before
-    // the loop goes round: a register that a load is still to write must not be moved.)
-    if (busy) {
-#pragma unroll 1
-      for (int k = 0; k < kDim / 128; ++k) {
-        uint32_t o[2][16];
-        const uint32_t ta = tmem + lane_base + kOCol + 64u * k + 32u * half;
-        tc_ld_x16(ta, o[0]);
-        tc_ld_x16(ta + 16u, o[1]);
-        const int d = 8 * v_chunk_back(16 * k + 4 * qd + (lane >> 3)) + (lane & 7);
-        tc_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int hc = 32 * half + 16 * j;  // heads hc .. hc + 15
-          if (!whole) {
-            float *po = &parts->o[part][hc][128 * k + 32 * qd + lane];
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-              if (hc + u < heads) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
-          } else {
-            // neighbouring lanes swap one of two heads, so each stores two dims of one head
-            uint16_t *out = a.out + int64_t(t) * a.out_stride + int64_t(h0 + hc) * kDim;
-            const int odd = lane & 1;
-#pragma unroll
-            for (int u = 0; u < 16; u += 2) {
-              const float v0 = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
-              const float v1 = __uint_as_float(o[j][u + 1]) * sm.hinv[hc + u + 1];
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-              const __nv_bfloat162 pr = odd ? __floats2bfloat162_rn(got, v1) : __floats2bfloat162_rn(v0, got);
-              if (hc + u + odd < heads) *reinterpret_cast<__nv_bfloat162 *>(out + (u + odd) * kDim + (d & ~1)) = pr;
-            }
-          }
-        }
+    if (last) {
+      if (xt == 0) {
+        sm.end_unit = w.unit;
+        sm.end_part = whole ? -1 : part;
       }
+      named_bar_sync(kBarEnd, kXThreads + 32 * kWWarps);  // W, done with its tiles, takes half of the output
     }
+    if (busy) store_output(g, sm, tmem, parts, w.unit, whole ? -1 : part, qd, half, 0, last ? kDim / 256 : kDim / 128);
     tc_fence_before();
     if (w.i1 >= total) break;
     w.next(g, total);
@@ -917,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
       role_x(g, sm, parts, hdr);
     } else if (warp >= kWWarp0) {
       set_regs_down<kRegsW>();
-      role_w(g, sm, hdr);
+      role_w(g, sm, parts, hdr);
     } else {
       set_regs_down<kRegsLM>();
       if (warp < kMWarp0) {

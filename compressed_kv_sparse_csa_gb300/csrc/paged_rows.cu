@@ -72,104 +72,131 @@ __device__ __forceinline__ void load8(const void *in, int64_t at, float (&v)[8])
   }
 }
 
+// The tokens of a warp: `per` in a row, so that a sequence found serves the next.
+struct Tokens {
+  int64_t t, end;
+  __device__ __forceinline__ Tokens(int64_t n, int64_t per) {
+    t = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * per;
+    end = min(n, t + per);
+  }
+};
+
 template <bool BF16>
 __global__ void __launch_bounds__(kWarps * 32)
 paged_append_kernel(PagedCache c, const int64_t *__restrict__ row0, const void *__restrict__ in, int64_t in_stride,
-                    int64_t n, const int64_t *__restrict__ pos, const float *__restrict__ inv_freq, int halves,
-                    WsHeader *__restrict__ hdr) {
+                    int64_t n, int64_t per, const int64_t *__restrict__ pos, const float *__restrict__ inv_freq,
+                    int halves, WsHeader *__restrict__ hdr) {
+  __shared__ unsigned long long turn[32];  // pair i's turn a position, 2^-64 turns
   // launched as a programmatic dependent: past this wait the previous kernel
   // (say the one that formed kv_in) is complete and visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= n) return;
-  float a[8], b[8];
-  load8<BF16>(in, t * in_stride + 8 * lane, a);
-  load8<BF16>(in, t * in_stride + 256 + 8 * lane, b);
-  const int32_t s = paged_seq_of(c, t, lane);
-  if (s < 0) return;
-  const int64_t r = __ldcg(row0 + s) + (t - __ldcg(c.cu + s));
-  const PagedRow p = paged_row(c, s, r);
-  if (p.page == nullptr) {
-    if (lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-    return;
-  }
-  if (inv_freq != nullptr) {
-    // lane i: pair i's angle
+  Tokens tk(n, per);
+  // (the block's one warp that does it: 64-bit floating point is slow here, and a
+  // warp a token spent more time on it than on everything else)
+  if (inv_freq != nullptr && threadIdx.x < 32) {
     // inv_freq / 2 pi as t + e, 1 / 2 pi in two doubles; the whole turns of t
     // dropped exactly, then 64 fraction bits of both
     const double w = double(__ldcg(inv_freq + lane));
     const double t0 = w * kInv2PiHi, e0 = fma(w, kInv2PiHi, -t0) + w * kInv2PiLo;
     const double fr = t0 - floor(t0);
-    const uint64_t f =
-        (fr < 1.0 ? uint64_t(fr * 18446744073709551616.0) : 0ull) + uint64_t(int64_t(e0 * 18446744073709551616.0));
-    const uint64_t at = f * uint64_t(pos != nullptr ? __ldcg(pos + t) : r);
-    float sn, cs;
-    sincospif(float(int32_t(uint32_t(at >> 32))) * 4.656612873077393e-10f, &sn, &cs);  // half turns: * 2^-31
-    const bool tail = lane >= kTailLane;
-    if (halves) {  // elements i and 32 + i: lanes 24-27 hold the first of each pair, 28-31 the second
+    turn[lane] = (fr < 1.0 ? (unsigned long long)(fr * 18446744073709551616.0) : 0ull) +
+                 (unsigned long long)((long long)(e0 * 18446744073709551616.0));
+  }
+  PagedSeq sq{-1, 0, 0};
+  int64_t first_row = 0;
+  bool ready = inv_freq == nullptr;
+  if (tk.t >= tk.end && !ready) __syncthreads();  // (the block's other warps wait for the turns)
+  for (; tk.t < tk.end; ++tk.t) {
+    const int64_t t = tk.t;
+    float a[8], b[8];
+    load8<BF16>(in, t * in_stride + 8 * lane, a);
+    load8<BF16>(in, t * in_stride + 256 + 8 * lane, b);
+    const int64_t place = pos != nullptr ? __ldcg(pos + t) : 0;
+    if (sq.s < 0 || t >= sq.to) {
+      sq = paged_seq_of(c, t, lane);
+      if (sq.s >= 0) first_row = __ldcg(row0 + sq.s);
+    }
+    const int64_t r = first_row + (t - sq.from);
+    const PagedRow p = sq.s >= 0 ? paged_row(c, sq.s, r) : PagedRow{nullptr, 0};
+    if (!ready) {
+      __syncthreads();
+      ready = true;
+    }
+    if (p.page == nullptr) {
+      if (sq.s >= 0 && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      continue;
+    }
+    if (inv_freq != nullptr) {
+      // lane i: pair i's angle
+      const uint64_t at = turn[lane] * uint64_t(pos != nullptr ? place : r);
+      float sn, cs;
+      sincospif(float(int32_t(uint32_t(at >> 32))) * 4.656612873077393e-10f, &sn, &cs);  // half turns: * 2^-31
+      const bool tail = lane >= kTailLane;
+      if (halves) {  // elements i and 32 + i: lanes 24-27 hold the first of each pair, 28-31 the second
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pair = 8 * (lane & 3) + i;
-        const float ci = __shfl_sync(0xffffffffu, cs, pair), si = __shfl_sync(0xffffffffu, sn, pair);
-        const float o = __shfl_xor_sync(0xffffffffu, b[i], 4);
-        if (tail) b[i] = (lane & 4) ? b[i] * ci + o * si : b[i] * ci - o * si;
-      }
-    } else {  // elements 2 i and 2 i + 1
+        for (int i = 0; i < 8; ++i) {
+          const int pair = 8 * (lane & 3) + i;
+          const float ci = __shfl_sync(0xffffffffu, cs, pair), si = __shfl_sync(0xffffffffu, sn, pair);
+          const float o = __shfl_xor_sync(0xffffffffu, b[i], 4);
+          if (tail) b[i] = (lane & 4) ? b[i] * ci + o * si : b[i] * ci - o * si;
+        }
+      } else {  // elements 2 i and 2 i + 1
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pair = (4 * (lane - kTailLane) + i) & 31;
-        const float ci = __shfl_sync(0xffffffffu, cs, pair), si = __shfl_sync(0xffffffffu, sn, pair);
-        const float x = b[2 * i], y = b[2 * i + 1];
-        if (tail) {
-          b[2 * i] = x * ci - y * si;
-          b[2 * i + 1] = x * si + y * ci;
+        for (int i = 0; i < 4; ++i) {
+          const int pair = (4 * (lane - kTailLane) + i) & 31;
+          const float ci = __shfl_sync(0xffffffffu, cs, pair), si = __shfl_sync(0xffffffffu, sn, pair);
+          const float x = b[2 * i], y = b[2 * i + 1];
+          if (tail) {
+            b[2 * i] = x * ci - y * si;
+            b[2 * i + 1] = x * si + y * ci;
+          }
         }
       }
     }
-  }
-  // block maxima over four lanes, the RoPE part's over lanes 24-31
-  float ma = amax8(a), mb = amax8(b);
+    // block maxima over four lanes, the RoPE part's over lanes 24-31
+    float ma = amax8(a), mb = amax8(b);
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-    mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-  }
-  const float m4 = __shfl_xor_sync(0xffffffffu, mb, 4);
-  const int ea = paged_exponent(ma, 0.75f, 3);  // 6 = 0.75 * 2^3
-  const int eb = lane < kTailLane ? paged_exponent(mb, 0.75f, 3)
-                                  : paged_exponent(fmaxf(mb, m4), 0.5f, 4);  // 8 = 0.5 * 2^4
-  const int E = __reduce_max_sync(0xffffffffu, max(ea, eb));  // the RoPE part's: the row's largest
-
-  uint8_t *page = const_cast<uint8_t *>(p.page);
-  uint8_t *codes = page + paged_code_off(p);
-  *reinterpret_cast<uint32_t *>(codes + 4 * lane) = codes8(a, pow2_neg(ea));
-  if (lane < kTailLane) {
-    *reinterpret_cast<uint32_t *>(codes + 128 + 4 * lane) = codes8(b, pow2_neg(eb));
-  } else {
-    const float f = pow2_neg(E);
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = fminf(fmaxf(b[2 * i] * f, -65504.0f), 65504.0f);
-      const float hi = fminf(fmaxf(b[2 * i + 1] * f, -65504.0f), 65504.0f);
-      const __half2 v = __floats2half2_rn(lo, hi);
-      h[i] = *reinterpret_cast<const uint32_t *>(&v);
+    for (int o = 1; o < 4; o <<= 1) {
+      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     }
-    *reinterpret_cast<uint4 *>(page + paged_tail_off(c, p) + 16 * (lane - kTailLane)) =
-        make_uint4(h[0], h[1], h[2], h[3]);
+    const float m4 = __shfl_xor_sync(0xffffffffu, mb, 4);
+    const int ea = paged_exponent(ma, 0.75f, 3);  // 6 = 0.75 * 2^3
+    const int eb = lane < kTailLane ? paged_exponent(mb, 0.75f, 3)
+                                    : paged_exponent(fmaxf(mb, m4), 0.5f, 4);  // 8 = 0.5 * 2^4
+    const int E = __reduce_max_sync(0xffffffffu, max(ea, eb));  // the RoPE part's: the row's largest
+
+    uint8_t *page = const_cast<uint8_t *>(p.page);
+    uint8_t *codes = page + paged_code_off(p);
+    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = codes8(a, pow2_neg(ea));
+    if (lane < kTailLane) {
+      *reinterpret_cast<uint32_t *>(codes + 128 + 4 * lane) = codes8(b, pow2_neg(eb));
+    } else {
+      const float f = pow2_neg(E);
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = fminf(fmaxf(b[2 * i] * f, -65504.0f), 65504.0f);
+        const float hi = fminf(fmaxf(b[2 * i + 1] * f, -65504.0f), 65504.0f);
+        const __half2 v = __floats2half2_rn(lo, hi);
+        h[i] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+      *reinterpret_cast<uint4 *>(page + paged_tail_off(c, p) + 16 * (lane - kTailLane)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    // the scale record: byte i < 8 from lane 4 i's first chunk, 8 .. 13 from lane
+    // 4 (i - 8)'s second, 14 the RoPE part's
+    const uint32_t ba = uint32_t(ea + 127), bb = uint32_t(eb + 127);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= __shfl_sync(0xffffffffu, ba, 4 * i) << (8 * (i & 3));
+#pragma unroll
+    for (int i = 8; i < kPgBlocks; ++i) w[i >> 2] |= __shfl_sync(0xffffffffu, bb, 4 * (i - 8)) << (8 * (i & 3));
+    w[3] |= uint32_t(E + 127) << 16;
+    if (lane == 0) *reinterpret_cast<uint4 *>(page + paged_scale_off(c, p)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // the scale record: byte i < 8 from lane 4 i's first chunk, 8 .. 13 from lane
-  // 4 (i - 8)'s second, 14 the RoPE part's
-  const uint32_t ba = uint32_t(ea + 127), bb = uint32_t(eb + 127);
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= __shfl_sync(0xffffffffu, ba, 4 * i) << (8 * (i & 3));
-#pragma unroll
-  for (int i = 8; i < kPgBlocks; ++i) w[i >> 2] |= __shfl_sync(0xffffffffu, bb, 4 * (i - 8)) << (8 * (i & 3));
-  w[3] |= uint32_t(E + 127) << 16;
-  if (lane == 0) *reinterpret_cast<uint4 *>(page + paged_scale_off(c, p)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Eight values as bf16 or f32.
@@ -206,61 +233,89 @@ __device__ __forceinline__ void decode8(uint32_t w, float s, float (&v)[8]) {
 template <bool BF16>
 __global__ void __launch_bounds__(kWarps * 32)
 paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__restrict__ out, int64_t out_stride,
-                    int64_t n, WsHeader *__restrict__ hdr) {
+                    int64_t n, int64_t per, WsHeader *__restrict__ hdr) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= n) return;
-  const int32_t s = paged_seq_of(c, t, lane);
-  if (s < 0) return;
-  const PagedRow p = paged_row(c, s, __ldcg(row0 + s) + (t - __ldcg(c.cu + s)));
-  float a[8], b[8];
-  if (p.page == nullptr) {
-    if (lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
-  } else {
-    const uint8_t *codes = p.page + paged_code_off(p);
-    const uint32_t wa = __ldcg(reinterpret_cast<const uint32_t *>(codes + 4 * lane));
-    const uint8_t *sc = p.page + paged_scale_off(c, p);
-    const float sa = pow2_byte(__ldcg(sc + (lane >> 2)));
-    if (lane < kTailLane) {
-      decode8(__ldcg(reinterpret_cast<const uint32_t *>(codes + 128 + 4 * lane)), pow2_byte(__ldcg(sc + 8 + (lane >> 2))), b);
-    } else {
-      const uint4 h = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p) + 16 * (lane - kTailLane)));
-      const uint32_t u[4] = {h.x, h.y, h.z, h.w};
-      const float f = pow2_byte(__ldcg(sc + kPgTailScale));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
-        b[2 * i] = v.x * f;
-        b[2 * i + 1] = v.y * f;
-      }
+  PagedSeq sq{-1, 0, 0};
+  int64_t first_row = 0;
+  for (Tokens tk(n, per); tk.t < tk.end; ++tk.t) {
+    const int64_t t = tk.t;
+    if (sq.s < 0 || t >= sq.to) {
+      sq = paged_seq_of(c, t, lane);
+      if (sq.s >= 0) first_row = __ldcg(row0 + sq.s);
     }
-    decode8(wa, sa, a);
+    if (sq.s < 0) continue;
+    const PagedRow p = paged_row(c, sq.s, first_row + (t - sq.from));
+    float a[8], b[8];
+    if (p.page == nullptr) {
+      if (lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
+    } else {
+      const uint8_t *codes = p.page + paged_code_off(p);
+      const uint32_t wa = __ldcg(reinterpret_cast<const uint32_t *>(codes + 4 * lane));
+      const uint8_t *sc = p.page + paged_scale_off(c, p);
+      const float sa = pow2_byte(__ldcg(sc + (lane >> 2)));
+      if (lane < kTailLane) {
+        decode8(__ldcg(reinterpret_cast<const uint32_t *>(codes + 128 + 4 * lane)), pow2_byte(__ldcg(sc + 8 + (lane >> 2))), b);
+      } else {
+        const uint4 h = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p) + 16 * (lane - kTailLane)));
+        const uint32_t u[4] = {h.x, h.y, h.z, h.w};
+        const float f = pow2_byte(__ldcg(sc + kPgTailScale));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+          b[2 * i] = v.x * f;
+          b[2 * i + 1] = v.y * f;
+        }
+      }
+      decode8(wa, sa, a);
+    }
+    store8<BF16>(out, t * out_stride + 8 * lane, a);
+    store8<BF16>(out, t * out_stride + 256 + 8 * lane, b);
   }
-  store8<BF16>(out, t * out_stride + 8 * lane, a);
-  store8<BF16>(out, t * out_stride + 256 + 8 * lane, b);
 }
 
+}  // namespace
+
+namespace {
+// Tokens a warp, so that the grid is at most what the GPU holds at once (8 blocks an
+// SM: 64 warps).
+cudaError_t tokens_per_warp(int64_t n, int64_t *per, unsigned *blocks) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = int64_t(sms) * 8 * kWarps;
+  *per = (n + warps - 1) / warps;
+  *blocks = unsigned((n + *per * kWarps - 1) / (*per * kWarps));
+  return cudaSuccess;
+}
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const void *in, bool in_bf16,
                                 int64_t in_stride, int64_t n, const int64_t *pos, const float *inv_freq, bool halves,
                                 void *ws, cudaStream_t stream) {
-  const unsigned blocks = unsigned((n + kWarps - 1) / kWarps);
+  int64_t per;
+  unsigned blocks;
+  const cudaError_t e = tokens_per_warp(n, &per, &blocks);
+  if (e != cudaSuccess) return e;
   WsHeader *hdr = static_cast<WsHeader *>(ws);
   return launch_pdl(in_bf16 ? paged_append_kernel<true> : paged_append_kernel<false>, blocks, kWarps * 32, 0, stream,
-                    c, row0, in, in_stride, n, pos, inv_freq, int(halves), hdr);
+                    c, row0, in, in_stride, n, per, pos, inv_freq, int(halves), hdr);
 }
 
 cudaError_t launch_paged_gather(const PagedCache &c, const int64_t *row0, void *out, bool out_bf16,
                                 int64_t out_stride, int64_t n, void *ws, cudaStream_t stream) {
-  const unsigned blocks = unsigned((n + kWarps - 1) / kWarps);
+  int64_t per;
+  unsigned blocks;
+  const cudaError_t e = tokens_per_warp(n, &per, &blocks);
+  if (e != cudaSuccess) return e;
   WsHeader *hdr = static_cast<WsHeader *>(ws);
   return launch_pdl(out_bf16 ? paged_gather_kernel<true> : paged_gather_kernel<false>, blocks, kWarps * 32, 0, stream,
-                    c, row0, out, out_stride, n, hdr);
+                    c, row0, out, out_stride, n, per, hdr);
 }
 
 }  // namespace ds4x
