@@ -75,6 +75,7 @@ constexpr int kRegs = 96, kRegsLM = 64, kRegsW = 96, kRegsX = 104;
 static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
+constexpr int kFewUnits = 16;      // up to so many units are joined by a block a head's half each
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
 constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
 constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
@@ -83,12 +84,19 @@ constexpr float kLazy = 8.0f;
 constexpr int kTame = 20;
 enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 
+// Where a row lies: its codes (null: no row), and from there to its RoPE part and
+// its scale record.
+struct __align__(16) Found {
+  const uint8_t *codes;
+  int32_t tail, scales;
+};
+
 struct __align__(1024) Smem {
   uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
   uint8_t v[2][kTile * kDim * 2];   // V': 8 panels of 8 KB, two tiles
   uint8_t p[2][kTile * kHeads * 2]; // P^T: one panel, two tiles
   float4 rowe[2][kTile];            // 2^E_j, E_j, 2^-E_j, E_j; a row that is not there: 0, -inf, 0, 0
-  int2 found[kAhead][kTile];        // a row's page (-1: no row) and its number there
+  Found found[kAhead][kTile];
   float red[4][kHeads];
   float alpha[kHeads];
   float mh[kHeads], hinv[kHeads];
@@ -96,7 +104,7 @@ struct __align__(1024) Smem {
   uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
   unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2][2], lfull[kAhead], lfree[kAhead], qfull, drain;
   long long scan[kThreads / 32];
-  long long cut0, cut1;             // the CTA's run of tiles
+  long long cut0, cut1, all;        // the CTA's run of tiles, and all tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
   int row0, rows;                   // that unit's rows
   int total;                        // its tiles
@@ -111,6 +119,7 @@ static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 // earlier CTA began; part 2 c + 1: of one that it begins and a later one ends.
 struct Parts {
   int32_t unit[2 * kMaxCtas];            // the part's unit, or -1
+  int2 span[kFewUnits];                  // with few units: a unit's first CTA, and how many have a part of it
   float lse2[2 * kMaxCtas][kHeads];      // log2 of the denominator
   float o[2 * kMaxCtas][kHeads][kDim];   // normalised, dims as V' has them (v_chunk)
 };
@@ -120,7 +129,8 @@ struct Args {
   int32_t groups;     // head groups a token
   int32_t group;      // heads a group (the last may have fewer)
   int32_t n_cols;     // `group` rounded up to 16: the products' N
-  uint64_t per_grid;  // 2^64 / gridDim.x, rounded up
+  uint64_t per_grid;  // 2^64 / CTAs, rounded up
+  int32_t few;        // at most kFewUnits units
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -210,10 +220,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
-// 2^e as fp16 bits for e <= 0 (0 below the smallest subnormal 2^-24).
-__device__ __forceinline__ uint32_t pow2_half_bits(int e) {
-  if (e >= -14) return uint32_t(e + 15) << 10;
-  return e >= -24 ? 1u << (e + 24) : 0u;
+// 2^d twice, as fp16, for d <= 0 (0 below the smallest subnormal 2^-24: the
+// conversion's rounding does it).
+__device__ __forceinline__ uint32_t pow2_half2(int d) {
+  const float f = pow2f(max(d, -32));
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(f));
+  return r;
 }
 __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -274,8 +287,29 @@ struct Walk {
 
 // ---- the cuts ------------------------------------------------------------------
 
+// Cut c of `total` tiles: at c total / CTAs, so that every CTA has a tile, or, with
+// fewer tiles than CTAs, at c.  (total < 2^43 and c <= 160: the high word of the
+// product with the rounded-up reciprocal is the quotient.)
+__device__ __forceinline__ long long cut_at(const Args &g, unsigned c, long long total) {
+  if (c >= gridDim.x) return total;
+  if (total < (long long)(gridDim.x)) return min((long long)c, total);
+  return (long long)(__umul64hi(c * (unsigned long long)total, g.per_grid));
+}
+// A cut at most so far from a unit's end moves there.
+__device__ __forceinline__ long long cut_tolerance(const Args &g, long long total) {
+  return total < (long long)(gridDim.x) ? 0 : (long long)(__umul64hi((unsigned long long)total, g.per_grid) >> 4);
+}
+// How many CTAs from this one on have a part of a unit that ends with tile end - 1,
+// that this one begins and does not end: the cuts inside it that do not move to its
+// end, and one.  (c total / CTAs < e for the c below e CTAs / total.)
+__device__ __forceinline__ int unit_parts(const Args &g, long long end, long long total) {
+  const long long e = end - cut_tolerance(g, total), n = gridDim.x;
+  const long long last = total < n ? e - 1 : (long long)(((unsigned long long)(e) * n + total - 1) / (unsigned long long)total) - 1;
+  return 1 + int(min(last, n - 1) - (long long)(blockIdx.x));
+}
+
 // The run of CTA c of g: unit0, off0, total; the first unit's rows.  All threads.
-__device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
+__device__ void find_cuts(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const PagedAttn &a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
@@ -308,18 +342,11 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
   }
   const long long total = __shfl_sync(0xffffffffu, wi, 31);
   const long long before = __shfl_sync(0xffffffffu, wi - ws, warp) + incl - mine;
-  // Cut c is at c total / gridDim.x, so that every CTA has a tile, or, with fewer
-  // tiles than CTAs, at c.  (total < 2^43 and c <= 160: the high word of the product
-  // with the rounded-up reciprocal is the quotient.)
-  const bool plenty = total >= (long long)(gridDim.x);
-  auto part = [&](unsigned c) {
-    if (c >= gridDim.x) return total;
-    return plenty ? (long long)(__umul64hi(c * (unsigned long long)total, g.per_grid)) : min((long long)c, total);
-  };
-  const long long tol = plenty ? (long long)(__umul64hi((unsigned long long)total, g.per_grid) >> 4) : 0;
+  if (tid == 0) sm.all = total;
+  const long long tol = cut_tolerance(g, total);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const long long x = part(blockIdx.x + e);
+    const long long x = cut_at(g, blockIdx.x + e, total);
     if (x >= total) {
       if (tid == 0) (e ? sm.cut1 : sm.cut0) = total;
       continue;
@@ -366,6 +393,8 @@ __device__ void find_cuts(const Args &g, Smem &sm, WsHeader *hdr) {
     if (run > INT32_MAX - 8) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));  // (months of work)
     sm.total = int(min(run, (long long)(INT32_MAX - 8)));
   }
+  // (padding has no parts)
+  if (blockIdx.x == 0 && g.few && tid < kFewUnits && tid / g.groups >= valid) parts->span[tid] = make_int2(0, 0);
   // a range past what the table can place
   if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr)
     for (int t = t0; t < min(t1, valid); ++t)
@@ -415,21 +444,25 @@ __device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
         if (row[k] >= n_rows) at[k].x = -1;
         if (row[k] != -1 && at[k].x < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
       }
-      // toward L2: a row's code lines (224 bytes lie in two or three) and RoPE line
+      Found f[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        f[k] = Found{nullptr, 0, 0};
         if (at[k].x >= 0) {
           const PagedRow p{a.c.pages + (int64_t(at[k].x) << a.c.page_log2) * DS4X_PAGED_ROW_BYTES, at[k].y};
-          const uint8_t *co = p.page + paged_code_off(p);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(co));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(co + 112));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(co + 223));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.page + paged_tail_off(a.c, p)));
+          const int32_t co = int32_t(paged_code_off(p));
+          f[k] = Found{p.page + co, int32_t(paged_tail_off(a.c, p)) - co, int32_t(paged_scale_off(a.c, p)) - co};
+          // toward L2: the code lines (224 bytes lie in two or three) and the RoPE part's
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(f[k].codes));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(f[k].codes + 112));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(f[k].codes + 223));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(f[k].codes + f[k].tail));
         }
+      }
       const int slot = i % kAhead;
       if (i >= kAhead) wait_bar(sm, &sm.lfree[slot], (i / kAhead - 1) & 1, hdr);
-      sm.found[slot][lane] = at[0];
-      sm.found[slot][32 + lane] = at[1];
+      sm.found[slot][lane] = f[0];
+      sm.found[slot][32 + lane] = f[1];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.lfull[slot]));
     }
@@ -462,15 +495,14 @@ __device__ __forceinline__ int v_chunk_back(int P) {  // the C of place P
 struct Raw {
   uint4 a, b, t, sc;  // (the scale record's zero byte: 255 marks a row that is not there)
 };
-__device__ __forceinline__ void load_raw(const PagedCache &c, int2 at, int l, Raw &w) {
+__device__ __forceinline__ void load_raw(const Found &at, int l, Raw &w) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  if (at.x >= 0) {
-    const PagedRow p{c.pages + (int64_t(at.x) << c.page_log2) * DS4X_PAGED_ROW_BYTES, at.y};
-    const uint4 *co = reinterpret_cast<const uint4 *>(p.page + paged_code_off(p)) + l;
-    w.sc = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_scale_off(c, p)));
-    w.a = __ldcg(co);
-    w.b = l < 6 ? __ldcg(co + 8) : z;
-    w.t = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p)) + l);
+  if (at.codes != nullptr) {
+    const uint8_t *lane = at.codes + 16 * l;
+    w.sc = __ldcg(reinterpret_cast<const uint4 *>(at.codes + at.scales));
+    w.a = __ldcg(reinterpret_cast<const uint4 *>(lane));
+    w.b = l < 6 ? __ldcg(reinterpret_cast<const uint4 *>(lane + 128)) : z;
+    w.t = __ldcg(reinterpret_cast<const uint4 *>(lane + at.tail));
   } else {
     w.a = w.b = w.t = z;
     w.sc = make_uint4(0, 0, 0, 0xff000000u);
@@ -490,8 +522,7 @@ __device__ __forceinline__ void widen8(uint32_t addr, uint32_t w, uint32_t f) {
 // A row (at `row`) of V', x = 16 (row % 8): panels 0 to 3, then 4 to 7.
 __device__ __forceinline__ void widen_low(uint32_t row, uint32_t x, int l, const Raw &w) {
   const int E = int((w.sc.w >> 16) & 0xffu);
-  const uint32_t f =
-      pow2_half_bits(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> (8 * (l & 3))) & 0xffu) - E)) * 0x10001u;
+  const uint32_t f = pow2_half2(min(0, int(((l & 4 ? w.sc.y : w.sc.x) >> (8 * (l & 3))) & 0xffu) - E));
   const uint32_t pa = row + (uint32_t(l << 4) ^ x);
   widen8(pa, w.a.x, f);
   widen8(pa + 8192, w.a.y, f);
@@ -502,8 +533,7 @@ __device__ __forceinline__ void widen_high(uint32_t row, uint32_t x, int l, cons
   const int E = int((w.sc.w >> 16) & 0xffu);
   sts16(row + 7 * 8192 + (uint32_t(l << 4) ^ x), w.t.x, w.t.y, w.t.z, w.t.w);
   if (l < 6) {
-    const uint32_t f =
-        pow2_half_bits(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> (8 * (l & 3))) & 0xffu) - E)) * 0x10001u;
+    const uint32_t f = pow2_half2(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> (8 * (l & 3))) & 0xffu) - E));
     widen8(row + (off_b[0] ^ x), w.b.x, f);
     widen8(row + (off_b[1] ^ x), w.b.y, f);
     widen8(row + (off_b[2] ^ x), w.b.z, f);
@@ -565,11 +595,11 @@ __device__ __forceinline__ void role_w(const Args &g, Smem &sm, Parts *parts, Ws
     if (i >= total) return;
     const int slot = i % kAhead;
     wait_bar(sm, &sm.lfull[slot], (i / kAhead) & 1, hdr);
-    const int2 at0 = sm.found[slot][r], at1 = sm.found[slot][r + 4];
+    const Found at0 = sm.found[slot][r], at1 = sm.found[slot][r + 4];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.lfree[slot]));
-    load_raw(g.a.c, at0, l, raw[0]);
-    load_raw(g.a.c, at1, l, raw[1]);
+    load_raw(at0, l, raw[0]);
+    load_raw(at1, l, raw[1]);
   };
   auto tile = [&](int i, int buf, Raw (&raw)[2]) {
     const uint32_t row = row0 + 65536u * buf;
@@ -732,6 +762,8 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
   const int r0 = 16 * qd + (lane >> 2);         // this lane's rows r0 and r0 + 8
   const int hb = 32 * half + 2 * (lane & 3);    // this lane's heads hb + 8 j + c
   const uint32_t lane_base = uint32_t(32 * qd) << 16;
+  // P^T: row r0, heads hb, hb + 1; heads 8 j on at the 16-byte chunk's number ^ j
+  const uint32_t p0 = smem_u32(sm.p[0]) + r0 * 128 + (((4 * half) ^ (r0 & 7)) << 4) + 4 * (lane & 3);
   make_query(g, sm, sm.unit0, 0, xw, lane);
   Walk w;
   w.begin(sm, total);
@@ -838,11 +870,10 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
           }
         }
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const int rr = r0 + 8 * ((k >> 1) & 1);
-          *reinterpret_cast<uint32_t *>(sm.p[b] + rr * 128 + (((4 * half + (k >> 2)) ^ (rr & 7)) << 4) +
-                                        4 * (lane & 3)) = half2_bits(d[k], d[k + 1]);
-        }
+        for (int k = 0; k < 16; k += 2)  // (rows r0 and r0 + 8 have the same place in their 8 rows)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"((p0 ^ uint32_t((k >> 2) << 4)) + 8192u * b +
+                                                       1024u * ((k >> 1) & 1)),
+                       "r"(half2_bits(d[k], d[k + 1])));
       }
       tc_fence_before();
       __syncwarp();
@@ -883,6 +914,9 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       }
     }
     if (xt == 0 && !whole) parts->unit[part] = w.unit;
+    if (xt == 0 && g.few && w.off == 0) {
+      parts->span[w.unit] = make_int2(int(blockIdx.x), whole ? 1 : unit_parts(g, sm.cut0 + w.i0 + w.tiles, sm.all));
+    }
     named_bar_sync(kBarX, kXThreads);
     wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1][1], ((w.i1 - 1) >> 1) & 1, hdr);
     tc_fence_after();
@@ -933,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < 2) parts->unit[2 * blockIdx.x + tid] = -1;
   tc_fence_before();
-  find_cuts(g, sm, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
+  find_cuts(g, sm, parts, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
   tc_fence_after();
   if (sm.total > 0) {
     if (warp >= kXWarp0) {
@@ -1100,6 +1134,85 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
   }
 }
 
+// The same for at most kFewUnits units, where a call's latency counts: a block takes
+// 256 dims of a head, its parts dealt over four pairs of warps; no list to make first.
+constexpr int kFewThreads = 256;
+__global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, const Parts *__restrict__ parts) {
+  __shared__ float wts[kMaxCtas], lsum, lmax;
+  __shared__ float4 part_sum[kFewThreads / 32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = blockIdx.x >> 7, h = (blockIdx.x >> 1) & 63;
+  const int t = u / g.groups, h0 = (u % g.groups) * g.group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (h >= min(g.group, g.a.n_heads - h0)) return;
+  const int2 span = __ldcg(&parts->span[u]);
+  const int c0 = span.x, n = span.y;
+  if (n <= 1) return;  // one CTA wrote it all
+  auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+  const int d0 = 256 * (blockIdx.x & 1) + 128 * (warp & 1) + 4 * lane, deal = warp >> 1;
+  // the first parts on their way, then the weights
+  float4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (deal + 4 * i < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(&parts->o[slot(deal + 4 * i)][h][d0]));
+  if (warp == 0) {
+    float x[kMaxCtas / 32], m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxCtas / 32; ++i) {
+      x[i] = lane + 32 * i < n ? __ldcg(&parts->lse2[slot(lane + 32 * i)][h]) : -INFINITY;
+      m = fmaxf(m, x[i]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+    for (int i = 0; i < kMaxCtas / 32; ++i) {
+      const float w = x[i] == -INFINITY ? 0.0f : exp2f(x[i] - m);
+      wts[lane + 32 * i] = w;
+      s += w;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0) {
+      lsum = s;
+      lmax = m;
+    }
+  }
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = deal;;) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + 4 * i < n) {
+        const float w = wts[k + 4 * i];
+        o.x = fmaf(w, v[i].x, o.x);
+        o.y = fmaf(w, v[i].y, o.y);
+        o.z = fmaf(w, v[i].z, o.z);
+        o.w = fmaf(w, v[i].w, o.w);
+      }
+    k += 32;
+    if (k >= n) break;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + 4 * i < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(&parts->o[slot(k + 4 * i)][h][d0]));
+  }
+  part_sum[warp][lane] = o;
+  __syncthreads();
+  if (deal != 0) return;
+  const float s = lsum, inv = s > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) {
+    const float4 p = part_sum[warp + 2 * k][lane];
+    o = make_float4(o.x + p.x, o.y + p.y, o.z + p.z, o.w + p.w);
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  const int d = 8 * v_chunk_back(d0 >> 3) + (d0 & 4);
+  *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+  if (threadIdx.x == 0 && (blockIdx.x & 1) == 0 && g.a.lse != nullptr)
+    g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (lmax + log2f(s)) * 0.6931471805599453f : -INFINITY;
+}
+
 }  // namespace
 
 size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts); }
@@ -1114,7 +1227,8 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0};
+  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0, 0};
+  g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;
   g.group = (a.n_heads + g.groups - 1) / g.groups;
   g.n_cols = (g.group + 15) / 16 * 16;
   // no more CTAs than there can be tiles
@@ -1127,6 +1241,9 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
   if (e != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;  // nothing is split
+  if (g.few)
+    return launch_pdl(paged_combine_few_kernel, unsigned(a.n_tokens * g.groups * 2 * kHeads), unsigned(kFewThreads),
+                      size_t(0), stream, g, static_cast<const Parts *>(parts));
   return launch_pdl(paged_combine_kernel, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
                     static_cast<const Parts *>(parts), ctas);
 }
