@@ -1213,6 +1213,53 @@ __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, 
     g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (lmax + log2f(s)) * 0.6931471805599453f : -INFINITY;
 }
 
+// The same where a unit has at most kShortParts tiles (short lists): a warp takes 128
+// dims of a head with all its parts on their way at once, and nothing is shared.
+constexpr int kShortParts = 16, kShortThreads = 256;
+__global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args g, const Parts *__restrict__ parts) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = blockIdx.x >> 5, h = 2 * (blockIdx.x & 31) + (warp >> 2);
+  const int t = u / g.groups, h0 = (u % g.groups) * g.group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (h >= min(g.group, g.a.n_heads - h0)) return;
+  const int2 span = __ldcg(&parts->span[u]);
+  const int c0 = span.x, n = span.y;
+  if (n <= 1) return;  // one CTA wrote it all
+  auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+  const int d0 = 128 * (warp & 3) + 4 * lane;
+  const float x = lane < n ? __ldcg(&parts->lse2[slot(lane)][h]) : -INFINITY;
+  float4 v[kShortParts];
+#pragma unroll
+  for (int k = 0; k < kShortParts; ++k)
+    if (k < n) v[k] = __ldcg(reinterpret_cast<const float4 *>(&parts->o[slot(k)][h][d0]));
+  float m = x;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float w = x == -INFINITY ? 0.0f : exp2f(x - m);
+  float s = w;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kShortParts; ++k) {
+    const float wk = __shfl_sync(0xffffffffu, w, k) * inv;
+    if (k < n) {
+      o.x = fmaf(wk, v[k].x, o.x);
+      o.y = fmaf(wk, v[k].y, o.y);
+      o.z = fmaf(wk, v[k].z, o.z);
+      o.w = fmaf(wk, v[k].w, o.w);
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+  const int d = 8 * v_chunk_back(d0 >> 3) + (d0 & 4);
+  *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+  if (lane == 0 && (warp & 3) == 0 && g.a.lse != nullptr)
+    g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+}
+
 }  // namespace
 
 size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts); }
@@ -1241,6 +1288,9 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
   if (e != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;  // nothing is split
+  if (g.few && (rows + kTile - 1) / kTile <= kShortParts)
+    return launch_pdl(paged_combine_short_kernel, unsigned(a.n_tokens * g.groups * kHeads / 2),
+                      unsigned(kShortThreads), size_t(0), stream, g, static_cast<const Parts *>(parts));
   if (g.few)
     return launch_pdl(paged_combine_few_kernel, unsigned(a.n_tokens * g.groups * 2 * kHeads), unsigned(kFewThreads),
                       size_t(0), stream, g, static_cast<const Parts *>(parts));
