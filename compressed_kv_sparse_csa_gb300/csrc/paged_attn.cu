@@ -75,6 +75,7 @@ constexpr int kRegs = 96, kRegsLM = 64, kRegsW = 96, kRegsX = 104;
 static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
+constexpr int kPackTokens = 8;     // tokens a unit, at most
 constexpr int kFewUnits = 16;      // up to so many units are joined by a block a head's half each
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
 constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
@@ -100,9 +101,9 @@ struct __align__(1024) Smem {
   float red[4][kHeads];
   float alpha[kHeads];
   float mh[kHeads], hinv[kHeads];
-  float qbase[2];                   // scale log2 e 2^-c, by segment parity
-  uint32_t qmax[3];                 // the unit's largest |q| (bf16 bits), by segment modulo 3
-  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2][2], lfull[kAhead], lfree[kAhead], qfull, drain;
+  float qscale[kHeads];             // the unit's columns' scale log2 e 2^-c
+  float qodd[kHeads];               // NaN for a column with NaN or infinity, else 0
+  unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2][2], lfull[kAhead], lfree[kAhead], qfull, qtaken, drain;
   long long scan[kThreads / 32];
   long long cut0, cut1, all;        // the CTA's run of tiles, and all tiles
   int unit0, off0;                  // where it begins: tile off0 of unit unit0
@@ -111,6 +112,8 @@ struct __align__(1024) Smem {
   uint32_t tmem_base;
   int abort_flag;
   int wide;                         // a row so far has an exponent beyond +-kTame
+  int2 seen[kPackTokens];           // packed: the rows that each token sees, from the unit's first
+  long long out_at[kHeads];         // packed: a column's output (-1: no column)
   int end_unit, end_part;           // the CTA's last unit, and its part (-1: the whole unit)
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
@@ -124,13 +127,32 @@ struct Parts {
   float o[2 * kMaxCtas][kHeads][kDim];   // normalised, dims as V' has them (v_chunk)
 };
 
+// With several tokens a unit: its tokens t0 .. t0 + count - 1, of one sequence, and
+// the rows that any of them sees.
+struct __align__(16) Pack {
+  int32_t t0, count, r0, n;
+};
+struct Plan {
+  int32_t n_units, pad[3];
+  Pack unit[DS4X_PAGED_MAX_TOKENS];
+};
+
 struct Args {
   PagedAttn a;
+  const Plan *plan;   // several tokens a unit (n_heads columns each), or null
   int32_t groups;     // head groups a token
-  int32_t group;      // heads a group (the last may have fewer)
+  int32_t group;      // a unit's columns at most: heads a group (the last may have fewer), or tokens x heads
+  int32_t per_head;   // 2^16 / n_heads, rounded up
   int32_t n_cols;     // `group` rounded up to 16: the products' N
   uint64_t per_grid;  // 2^64 / CTAs, rounded up
   int32_t few;        // at most kFewUnits units
+  __device__ __forceinline__ bool packed() const { return plan != nullptr; }
+};
+// The same where the kernel is compiled for either: unpacked units cost nothing for the others.
+template <bool P>
+struct ArgsFor : Args {
+  ArgsFor(const Args &g) : Args(g) {}
+  static __device__ __forceinline__ constexpr bool packed() { return P; }
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -211,6 +233,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
@@ -242,6 +271,31 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
+// A unit's query vectors ("columns"): heads h0 .. of token t0, or, packed, all heads
+// of count tokens from t0, head by head.
+struct Columns {
+  int32_t t0, h0, n;
+  template <class A>
+  __device__ __forceinline__ Columns(const A &g, int unit) {
+    if (g.packed()) {
+      const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[unit]));
+      t0 = p.x;
+      h0 = 0;
+      n = p.y * g.a.n_heads;
+    } else {
+      t0 = unit / g.groups;
+      h0 = (unit % g.groups) * g.group;
+      n = min(g.group, g.a.n_heads - h0);
+    }
+  }
+  // column c's token and head (c < 64 and n_heads <= 64: the product is the quotient)
+  template <class A>
+  __device__ __forceinline__ int64_t at(const A &g, int c, int64_t token_stride, int head_stride) const {
+    const int j = g.packed() ? (c * g.per_head) >> 16 : 0;
+    return int64_t(t0 + j) * token_stride + (h0 + c - j * g.a.n_heads) * head_stride;
+  }
+};
+
 // A token's rows: n of them, from row r0 of its sequence (or of its list).
 struct Rows {
   int64_t r0;
@@ -254,6 +308,12 @@ __device__ __forceinline__ Rows token_rows(const PagedAttn &a, int t) {
   const int64_t b = a.row_begin != nullptr ? max(int64_t(0), int64_t(__ldcg(a.row_begin + t))) : 0;
   const int64_t e = min(room, int64_t(__ldcg(a.row_end + t)));
   return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
+}
+template <class A>
+__device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
+  if (!g.packed()) return token_rows(g.a, unit / g.groups);
+  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[unit]) + 1);
+  return Rows{p.x, p.y};
 }
 // A token without a row still has a tile (of rows that are not there): it writes the zeros.
 __device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
@@ -276,11 +336,12 @@ struct Walk {
     i0 = 0;
     set(sm.row0, sm.rows, total);
   }
-  __device__ __forceinline__ void next(const Args &g, int total) {
+  template <class A>
+  __device__ __forceinline__ void next(const A &g, int total) {
     ++unit;
     off = 0;
     i0 = i1;
-    const Rows r = token_rows(g.a, unit / g.groups);
+    const Rows r = unit_rows(g, unit);
     set(int(r.r0), r.n, total);
   }
 };
@@ -290,36 +351,42 @@ struct Walk {
 // Cut c of `total` tiles: at c total / CTAs, so that every CTA has a tile, or, with
 // fewer tiles than CTAs, at c.  (total < 2^43 and c <= 160: the high word of the
 // product with the rounded-up reciprocal is the quotient.)
-__device__ __forceinline__ long long cut_at(const Args &g, unsigned c, long long total) {
+template <class A>
+__device__ __forceinline__ long long cut_at(const A &g, unsigned c, long long total) {
   if (c >= gridDim.x) return total;
   if (total < (long long)(gridDim.x)) return min((long long)c, total);
   return (long long)(__umul64hi(c * (unsigned long long)total, g.per_grid));
 }
 // A cut at most so far from a unit's end moves there.
-__device__ __forceinline__ long long cut_tolerance(const Args &g, long long total) {
+template <class A>
+__device__ __forceinline__ long long cut_tolerance(const A &g, long long total) {
   return total < (long long)(gridDim.x) ? 0 : (long long)(__umul64hi((unsigned long long)total, g.per_grid) >> 4);
 }
 // How many CTAs from this one on have a part of a unit that ends with tile end - 1,
 // that this one begins and does not end: the cuts inside it that do not move to its
 // end, and one.  (c total / CTAs < e for the c below e CTAs / total.)
-__device__ __forceinline__ int unit_parts(const Args &g, long long end, long long total) {
+template <class A>
+__device__ __forceinline__ int unit_parts(const A &g, long long end, long long total) {
   const long long e = end - cut_tolerance(g, total), n = gridDim.x;
   const long long last = total < n ? e - 1 : (long long)(((unsigned long long)(e) * n + total - 1) / (unsigned long long)total) - 1;
   return 1 + int(min(last, n - 1) - (long long)(blockIdx.x));
 }
 
 // The run of CTA c of g: unit0, off0, total; the first unit's rows.  All threads.
-__device__ void find_cuts(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
+template <class A>
+__device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const PagedAttn &a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
-  // a thread takes `per` tokens in a row (of all that there may be: the count of
-  // valid ones is on its way with their rows)
+  // a thread takes `per` tokens in a row (or packed units; of all that there may be:
+  // the count of valid ones is on its way with their rows)
   const int per = (a.n_tokens + kThreads - 1) / kThreads;
   const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
-  const Rows first_rows = t0 < t1 ? token_rows(a, t0) : Rows{0, 0};
-  const int valid = __ldcg(a.c.cu + a.c.n_seqs);  // tokens behind are padding
-  auto tiles_of = [&](int t) { return t < valid ? rows_tiles(token_rows(a, t).n) : 0; };
+  auto rows_of = [&](int t) { return g.packed() ? unit_rows(g, t) : token_rows(a, t); };
+  const Rows first_rows = t0 < t1 ? rows_of(t0) : Rows{0, 0};
+  // tokens behind are padding
+  const int valid = g.packed() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
+  auto tiles_of = [&](int t) { return t < valid ? rows_tiles(rows_of(t).n) : 0; };
   const int first = t0 < min(t1, valid) ? rows_tiles(first_rows.n) : 0;
   long long mine = first;
   for (int t = t0 + 1; t < t1; ++t) mine += tiles_of(t);
@@ -375,7 +442,7 @@ __device__ void find_cuts(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) 
           sm.unit0 = t * g.groups + k;
           sm.off0 = int(off);
           if (at < total) {
-            const Rows r = t == t0 ? first_rows : token_rows(a, t);
+            const Rows r = t == t0 ? first_rows : rows_of(t);
             sm.row0 = int(r.r0);
             sm.rows = r.n;
           }
@@ -396,7 +463,7 @@ __device__ void find_cuts(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) 
   // (padding has no parts)
   if (blockIdx.x == 0 && g.few && tid < kFewUnits && tid / g.groups >= valid) parts->span[tid] = make_int2(0, 0);
   // a range past what the table can place
-  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr)
+  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.packed())
     for (int t = t0; t < min(t1, valid); ++t)
       if (__ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
         atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
@@ -405,14 +472,15 @@ __device__ void find_cuts(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) 
 
 // ---- L: finding rows ------------------------------------------------------------
 
-__device__ __forceinline__ void role_l(const Args &g, Smem &sm, WsHeader *hdr) {
+template <class A>
+__device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
   const PagedAttn &a = g.a;
   const int total = sm.total;
   const int lane = threadIdx.x & 31;  // finds the tile's rows lane and 32 + lane
   Walk w;
   w.begin(sm, total);
   for (;;) {
-    const int t = w.unit / g.groups;
+    const int t = g.packed() ? __ldcg(&g.plan->unit[w.unit].t0) : w.unit / g.groups;
     int seq = -1;
     int n_rows = 0;
     bool fresh = true;
@@ -545,11 +613,11 @@ __device__ __forceinline__ void widen_high(uint32_t row, uint32_t x, int l, cons
 // - 1, 128 dims each, by 32 heads (`half`); the warp's dims are 32 qd .. of each M
 // tile.  (A step's loads are waited for before the loop goes round: a register that a
 // load is still to write must not be moved.)
-__device__ __forceinline__ void store_output(const Args &g, Smem &sm, uint32_t tmem, Parts *parts, int unit, int part,
+template <class A>
+__device__ __forceinline__ void store_output(const A &g, Smem &sm, uint32_t tmem, Parts *parts, int unit, int part,
                                              int qd, int half, int k0, int k1) {
   const int lane = threadIdx.x & 31;
-  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
-  const int heads = min(g.group, g.a.n_heads - h0);
+  const Columns col(g, unit);
 #pragma unroll 1
   for (int k = k0; k < k1; ++k) {
     uint32_t o[2][16];
@@ -564,25 +632,32 @@ __device__ __forceinline__ void store_output(const Args &g, Smem &sm, uint32_t t
         float *po = &parts->o[part][hc][128 * k + 32 * qd + lane];
 #pragma unroll
         for (int u = 0; u < 16; ++u)
-          if (hc + u < heads) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
+          if (hc + u < col.n) po[u * kDim] = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
       } else {
         // neighbouring lanes swap one of two heads, so each stores two dims of one head
         const int odd = lane & 1, d = 8 * v_chunk_back(16 * k + 4 * qd + (lane >> 3)) + (lane & 6);
-        uint16_t *out = g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + hc + odd) * kDim + d;
+        uint16_t *out = g.a.out + d + (A::packed() ? 0 : col.at(g, hc + odd, g.a.out_stride, kDim));
 #pragma unroll
         for (int u = 0; u < 16; u += 2) {
           const float v0 = __uint_as_float(o[j][u]) * sm.hinv[hc + u];
           const float v1 = __uint_as_float(o[j][u + 1]) * sm.hinv[hc + u + 1];
           const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
           const __nv_bfloat162 pr = odd ? __floats2bfloat162_rn(got, v1) : __floats2bfloat162_rn(v0, got);
-          if (hc + u + odd < heads) *reinterpret_cast<__nv_bfloat162 *>(out + u * kDim) = pr;
+          const int c = hc + u + odd;
+          if (A::packed()) {
+            const long long at = sm.out_at[c];
+            if (at >= 0) *reinterpret_cast<__nv_bfloat162 *>(out + at) = pr;
+          } else if (c < col.n) {
+            *reinterpret_cast<__nv_bfloat162 *>(out + u * kDim) = pr;
+          }
         }
       }
     }
   }
 }
 
-__device__ __forceinline__ void role_w(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
+template <class A>
+__device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const int total = sm.total;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWWarp0;
   const int l = lane & 7, q = lane >> 3;
@@ -645,7 +720,8 @@ __device__ __forceinline__ void role_w(const Args &g, Smem &sm, Parts *parts, Ws
 // loads in flight.
 
 // S of the tiles of one parity.
-__device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader *hdr) {
+template <class A>
+__device__ __forceinline__ void role_s(const A &g, Smem &sm, int b, WsHeader *hdr) {
   const int total = sm.total;
   const uint32_t tmem = sm.tmem_base;
   const uint32_t idS = idesc_f16(kTile, uint32_t(g.n_cols), 0, 0);  // V' K-major, Q' K-major
@@ -654,6 +730,7 @@ __device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader 
   w.begin(sm, total);
   for (int seg = 0;; ++seg) {
     wait_bar(sm, &sm.qfull, seg & 1, hdr);
+    mbar_arrive(smem_u32(&sm.qtaken));
     for (int i = w.i0 + ((w.i0 ^ b) & 1); i < w.i1; i += 2) {
       wait_bar(sm, &sm.vfull[b], (i >> 1) & 1, hdr);
       fence_proxy_async_smem();
@@ -675,7 +752,8 @@ __device__ __forceinline__ void role_s(const Args &g, Smem &sm, int b, WsHeader 
 }
 
 // O of every tile, in order.
-__device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
+template <class A>
+__device__ __forceinline__ void role_o(const A &g, Smem &sm, WsHeader *hdr) {
   const int total = sm.total;
   const uint32_t tmem = sm.tmem_base;
   const uint32_t idO = idesc_f16(128, uint32_t(g.n_cols), 1, 1);  // V'^T MN-major, P^T MN-major
@@ -709,50 +787,67 @@ __device__ __forceinline__ void role_o(const Args &g, Smem &sm, WsHeader *hdr) {
 
 // ---- X: softmax and output ------------------------------------------------------------
 
-// Q' of a unit: warp w of X converts heads 8 w .. 8 w + 7, lane L the 16-byte
-// chunks L and 32 + L of each; heads that the unit does not have are zeros.  All of
+// Q' of a unit: warp w of X converts columns 8 w .. 8 w + 7, lane L the 16-byte
+// chunks L and 32 + L of each; columns that the unit does not have are zeros.  All of
 // a warp's loads are in flight at once (64 registers: the unit's maxima and sums
 // must be in shared memory by then).
-__device__ __forceinline__ void make_query(const Args &g, Smem &sm, int unit, int seg, int xw, int lane) {
-  const int t = unit / g.groups, h0 = (unit % g.groups) * g.group;
-  const int heads = min(g.group, g.a.n_heads - h0) - 8 * xw;  // of this warp's
-  const uint4 *q =
-      reinterpret_cast<const uint4 *>(g.a.q + int64_t(t) * g.a.q_stride + int64_t(h0 + 8 * xw) * kDim) + lane;
-  uint4 qv[16];
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) qv[i] = (i >> 1) < heads ? __ldcg(q + 32 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) m = __vmaxu2(m, w4[u] & 0x7fff7fffu);
+template <class A>
+__device__ __forceinline__ void make_query(const A &g, Smem &sm, int unit, int xw, int lane) {
+  const Columns col(g, unit);
+  if (g.packed() && xw == 0 && lane < kPackTokens) {  // (warp 0)
+    const Rows u = unit_rows(g, unit);
+    const Rows r = lane * g.a.n_heads < col.n ? token_rows(g.a, col.t0 + lane) : Rows{0, 0};
+    const int lo = r.n > 0 ? int(r.r0 - u.r0) : 0;
+    sm.seen[lane] = make_int2(lo, lo + r.n);
   }
-  m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-  const int slot = seg % 3;
-  if (lane == 0) atomicMax(&sm.qmax[slot], m);
-  // the next unit's slot: its last readers (three units ago) passed the previous unit's barrier
-  if (xw == 0 && lane == 0) sm.qmax[(seg + 1) % 3] = 0;
-  named_bar_sync(kBarX, kXThreads);
-  const int e = int(*reinterpret_cast<volatile uint32_t *>(&sm.qmax[slot]) >> 7);  // the largest exponent field
-  const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
-  const float f = pow2f(c);
-  if (xw == 0 && lane == 0) sm.qbase[seg & 1] = g.a.scale * kLog2e * pow2f(-c);
+  const long long mine = col.at(g, 8 * xw + (A::packed() ? lane & 7 : 0), g.a.q_stride, kDim);
+  const uint4 *q = reinterpret_cast<const uint4 *>(g.a.q + (A::packed() ? 0 : mine)) + lane;
+  uint4 qv[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int h = 8 * xw + (i >> 1), P = v_chunk(32 * (i & 1) + lane);
-    const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-    uint32_t o[4];
+    const int c = 8 * xw + (i >> 1);
+    const long long at = A::packed() ? __shfl_sync(0xffffffffu, mine, i >> 1) / 8 + 32 * (i & 1) : 32 * i;
+    qv[i] = c < col.n ? __ldcg(q + at) : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      o[u] = half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
-    sts16(smem_u32(sm.q) + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
+  for (int k = 0; k < 8; ++k) {
+    // the column's largest exponent field e, and the scale that brings it to 14
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 2 * k; i < 2 * k + 2; ++i) {
+      const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) m = __vmaxu2(m, w4[u] & 0x7fff7fffu);
+    }
+    const int e = int(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) >> 7);
+    const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
+    const float f = pow2f(c);
+    const int h = 8 * xw + k;
+    // A column with NaN or infinity (all its logits are, so all its results) is computed
+    // as zeros, so that rows that are not there stay out, and marked: out and lse are NaN.
+    const bool odd = e == 255;
+    if (lane == 0) {
+      sm.qscale[h] = g.a.scale * kLog2e * pow2f(-c);
+      sm.qodd[h] = odd ? __int_as_float(0x7fffffff) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int P = v_chunk(32 * i + lane);
+      const uint4 v = qv[2 * k + i];
+      const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        o[u] = odd ? 0u : half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
+      sts16(smem_u32(sm.q) + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
+    }
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
 }
 
-__device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, WsHeader *hdr) {
+template <class A>
+__device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const int total = sm.total;
   const uint32_t tmem = sm.tmem_base;
   const PagedAttn &a = g.a;
@@ -764,15 +859,25 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
   const uint32_t lane_base = uint32_t(32 * qd) << 16;
   // P^T: row r0, heads hb, hb + 1; heads 8 j on at the 16-byte chunk's number ^ j
   const uint32_t p0 = smem_u32(sm.p[0]) + r0 * 128 + (((4 * half) ^ (r0 & 7)) << 4) + 4 * (lane & 3);
-  make_query(g, sm, sm.unit0, 0, xw, lane);
+  make_query(g, sm, sm.unit0, xw, lane);
+  if (A::packed()) named_bar_sync(kBarX, kXThreads);  // `seen`
   Walk w;
   w.begin(sm, total);
   for (int seg = 0;; ++seg) {
     float m[8], sum[8];  // head hb + 8 j + c: 2 j + c
 #pragma unroll
     for (int k = 0; k < 8; ++k) m[k] = 0.0f, sum[k] = 0.0f;
-    float base = 0.0f;
-    bool fresh = busy;  // no row so far (a row is there for all heads or for none): m is 0 and not a maximum yet
+    // bit k: no row so far for that head (for all heads or none, unless packed); m is 0
+    // and not a maximum yet
+    uint32_t fresh = busy ? 0xffu : 0u;
+    int lo = 0, hi = INT32_MAX;          // packed: the rows that all of the unit's tokens see
+    if (A::packed()) {
+      const int count = __ldcg(&g.plan->unit[w.unit].count);
+      for (int j = 0; j < count; ++j) {
+        lo = max(lo, sm.seen[j].x);
+        hi = min(hi, sm.seen[j].y);
+      }
+    }
     for (int i = w.i0; i < w.i1; ++i) {
       const int b = i & 1;
       wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
@@ -781,27 +886,46 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       float inv[2] = {0.0f, 0.0f}, er[2] = {0.0f, 0.0f};  // the rows' 2^-E_j, E_j
       float over = -INFINITY;
       const bool wide = *reinterpret_cast<volatile int *>(&sm.wide) != 0;
-      if (i == w.i0) base = sm.qbase[seg & 1];
       if (busy) {
         uint32_t s[16];
         tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
         const float4 e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
-        const float f[2] = {base * e0.x, base * e1.x}, ef[2] = {e0.y, e1.y};  // (not there: x = -inf, weight 0)
+        const float ef[2] = {e0.y, e1.y};
         inv[0] = e0.z, inv[1] = e1.z;
         er[0] = e0.w, er[1] = e1.w;
+        float2 qs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qs[k] = *reinterpret_cast<const float2 *>(&sm.qscale[hb + 8 * k]);
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
           const int row = (k >> 1) & 1, h = 2 * (k >> 2);
-          float2 x = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f[row], f[row]),
-                          make_float2(ef[row], ef[row]));
+          const float er2 = row ? e1.x : e0.x;
+          float2 x = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                          mul2(qs[k >> 2], make_float2(er2, er2)), make_float2(ef[row], ef[row]));
           x = add2(x, make_float2(-m[h], -m[h + 1]));
           d[k] = x.x;
           d[k + 1] = x.y;
           over = fmaxf(fmaxf(over, d[k]), d[k + 1]);
         }
       }
-      if (named_bar_or(kBarX, kXThreads, over > kLazy || fresh)) {
+      bool moves = over > kLazy || fresh != 0;
+      if (A::packed()) {
+        const int first = (w.off + (i - w.i0)) * kTile;
+        if (busy && (first < lo || first > hi - kTile)) {  // rows that some token does not see
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int row = first + r0 + 8 * ((k >> 1) & 1), j = ((hb + 8 * (k >> 2) + (k & 1)) * g.per_head) >> 16;
+            if (j < kPackTokens && (row < sm.seen[j].x || row >= sm.seen[j].y)) d[k] = -INFINITY;
+          }
+        }
+        moves = false;  // a maximum is passed, or a first row sets one, however small
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          moves = moves || d[k] > ((fresh >> (2 * (k >> 2) + (k & 1)) & 1) ? -INFINITY : kLazy);
+        moves = moves && busy;
+      }
+      if (named_bar_or(kBarX, kXThreads, moves)) {
         // some head's maximum moves: each head's maximum over the tile
         if (busy) {
 #pragma unroll
@@ -814,21 +938,24 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
         }
         named_bar_sync(kBarX, kXThreads);
         if (busy) {
-          bool none = false;
+          const uint32_t was_fresh = fresh;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int h = hb + 8 * (k >> 1) + (k & 1);
             float up = fmaxf(fmaxf(sm.red[0][h], sm.red[1][h]), fmaxf(sm.red[2][h], sm.red[3][h]));
-            none = up == -INFINITY;
-            if (none || !(fresh || up > kLazy)) up = 0.0f;
+            const bool none = up == -INFINITY;
+            if (none || !((was_fresh >> k & 1) || up > kLazy)) up = 0.0f;
+            if (!none) fresh &= A::packed() ? ~(1u << k) : 0u;
             m[k] += up;
             d[4 * (k >> 1) + (k & 1)] -= up;
             d[4 * (k >> 1) + 2 + (k & 1)] -= up;
-            const float half_al = ex2(-0.5f * up);  // (rows far apart in size: 2^-up itself may underflow)
+            // what there is so far times 2^-up (zeros, before a first row, whose `up` may be far
+            // below zero); in halves for the sum (rows far apart in size: 2^-up itself may underflow)
+            up = fmaxf(up, 0.0f);
+            const float half_al = ex2(-0.5f * up);
             sum[k] = sum[k] * half_al * half_al;
             if (qd == 0 && lane < 4) sm.alpha[h] = ex2(-up);
           }
-          fresh = fresh && none;
         }
         named_bar_sync(kBarX, kXThreads);
         if (i > w.i0 && busy) {
@@ -891,26 +1018,29 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
       for (int k = 0; k < 8; ++k) {
         const int h = hb + 8 * (k >> 1) + (k & 1);
         sm.red[qd][h] = sum[k];
-        if (qd == 0) sm.mh[h] = m[k];
+        if (qd == 0) sm.mh[h] = m[k] + sm.qodd[h];
       }
     }
     // the next unit's Q' (this one's last first product is done: its softmax is)
     const bool last = w.i1 >= total;
-    if (!last) make_query(g, sm, w.unit + 1, seg + 1, xw, lane);
+    if (!last) {
+      wait_bar(sm, &sm.qtaken, seg & 1, hdr);  // (an S thread without a tile in this unit may not have seen its Q' yet)
+      make_query(g, sm, w.unit + 1, xw, lane);
+    }
     named_bar_sync(kBarX, kXThreads);
-    const int t = w.unit / g.groups, h0 = (w.unit % g.groups) * g.group;
-    const int heads = min(g.group, a.n_heads - h0);
     const bool whole = w.off == 0 && w.i1 - w.i0 == w.tiles;
     const int part = 2 * int(blockIdx.x) + (w.off == 0 ? 1 : 0);
     if (xt < g.n_cols) {
       const float tot = (sm.red[0][xt] + sm.red[1][xt]) + (sm.red[2][xt] + sm.red[3][xt]);
-      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) : 0.0f;
+      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) + 0.0f * sm.mh[xt] : 0.0f;  // (m is finite or NaN)
       const float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
-      if (xt < heads) {
+      const Columns col(g, w.unit);
+      if (A::packed()) sm.out_at[xt] = xt < col.n ? col.at(g, xt, a.out_stride, kDim) : -1;
+      if (xt < col.n) {
         if (!whole)
           parts->lse2[part][xt] = l2;
         else if (a.lse != nullptr)
-          a.lse[int64_t(t) * a.n_heads + h0 + xt] = l2 * 0.6931471805599453f;
+          a.lse[col.at(g, xt, a.n_heads, 1)] = l2 * 0.6931471805599453f;
       }
     }
     if (xt == 0 && !whole) parts->unit[part] = w.unit;
@@ -934,7 +1064,70 @@ __device__ __forceinline__ void role_x(const Args &g, Smem &sm, Parts *parts, Ws
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *__restrict__ parts,
+// Packs tokens into units: the tokens of a sequence by threes, or however many times
+// n_heads fits 64 columns, in order.  One block.
+constexpr int kPlanThreads = 1024, kPlanSeqs = 4096;
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, int pack, Plan *__restrict__ plan,
+                                                                  WsHeader *__restrict__ hdr) {
+  __shared__ int32_t cus[kPlanSeqs + 1], warps[kPlanThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_seqs = a.c.n_seqs;
+  const bool held = n_seqs <= kPlanSeqs;
+  if (held)
+    for (int i = tid; i <= n_seqs; i += kPlanThreads) cus[i] = __ldcg(a.c.cu + i);
+  const int valid = max(0, min(a.n_tokens, __ldcg(a.c.cu + n_seqs)));
+  __syncthreads();
+  auto cu = [&](int s) { return held ? cus[s] : __ldcg(a.c.cu + s); };
+  const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
+  int base = 0;
+  for (int c0 = 0; c0 < valid; c0 += kPlanThreads) {
+    const int t = c0 + tid;
+    Pack u{t, 0, 0, 0};
+    if (t < valid) {
+      int s = 0, n = n_seqs;  // the last sequence that begins at or before t
+      while (n > 1) {
+        const int half = n / 2;
+        if (cu(s + half) <= t) s += half, n -= half;
+        else n = half;
+      }
+      const int from = cu(s), to = min(valid, cu(s + 1));
+      const bool in = from <= t && t < to;  // (else cu is not what it should be: a unit without a row)
+      if (!in || (t - from) % pack == 0) {
+        u.count = in ? min(pack, to - t) : 1;
+        int64_t lo = INT64_MAX, hi = 0;
+        for (int j = 0; j < u.count; ++j) {
+          const Rows r = in ? token_rows(a, t + j) : Rows{0, 0};
+          if (r.n > 0) {
+            lo = min(lo, r.r0);
+            hi = max(hi, r.r0 + r.n);
+          }
+          if (__ldcg(a.row_end + t + j) > room) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+        }
+        if (hi > 0) {
+          u.r0 = int(lo);
+          u.n = int(hi - lo);
+        }
+      }
+    }
+    const uint32_t b = __ballot_sync(0xffffffffu, u.count > 0);
+    if (lane == 0) warps[warp] = __popc(b);
+    __syncthreads();
+    int before = __popc(b & ((1u << lane) - 1)), all = 0;
+    for (int k = 0; k < kPlanThreads / 32; ++k) {
+      if (k < warp) before += warps[k];
+      all += warps[k];
+    }
+    if (u.count > 0) plan->unit[base + before] = u;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) plan->n_units = base;
+}
+
+template <bool P>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P> g, Parts *__restrict__ parts,
                                                                  WsHeader *__restrict__ hdr) {
   // (no static shared memory: the dynamic begins at the window's start, as aligned as Smem asks)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -953,9 +1146,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args g, Parts *
       mbar_init(smem_u32(&sm.lfree[k]), kWWarps);
     }
     mbar_init(smem_u32(&sm.qfull), kXWarps);
+    mbar_init(smem_u32(&sm.qtaken), 2);
     mbar_init(smem_u32(&sm.drain), 3);
     sm.abort_flag = sm.wide = 0;
-    sm.qmax[0] = sm.qmax[1] = sm.qmax[2] = 0;
     fence_mbar_init();
   }
   if (warp == kMWarp0) {
@@ -1050,7 +1243,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
             c = clear != 0 ? c + __ffs(int(clear)) - 1 : 32 * k + 32;
           }
         count[e] = c - first[e];
-        const int h0 = (unit[2 * first[e] + 1] % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
+        const int heads = Columns(g, unit[2 * first[e] + 1]).n;
         mine = count[e] <= kJoinFew ? (heads + 3) / 4 : 4 * heads;
       }
       int incl = mine;
@@ -1072,7 +1265,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
   for (int item = blockIdx.x, e = 0; item < items; item += gridDim.x) {
     while (item >= item0[e + 1]) ++e;
     const int c0 = first[e], n = count[e], u = unit[2 * c0 + 1];
-    const int t = u / g.groups, h0 = (u % g.groups) * g.group, heads = min(g.group, g.a.n_heads - h0);
+    const Columns col(g, u);
+    const int heads = col.n;
     const bool few = n <= kJoinFew;
     const int it = item - item0[e], quarter = few ? warp & 3 : it & 3;
     const int h = few ? 4 * it + (warp >> 2) : it >> 2;
@@ -1112,7 +1306,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
       }
       if (!few) part_sum[warp][lane] = o;
       if (lane == 0 && quarter == 0 && writes && g.a.lse != nullptr)
-        g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+        g.a.lse[col.at(g, h, g.a.n_heads, 1)] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
     }
     if (!few) {
       __syncthreads();
@@ -1127,7 +1321,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
     if (h < heads && writes) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
       const int d = 8 * v_chunk_back(16 * quarter + (lane >> 1)) + 4 * (lane & 1);
-      *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
+      *reinterpret_cast<uint2 *>(g.a.out + col.at(g, h, g.a.out_stride, kDim) + d) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
     __syncwarp();  // wts is read
@@ -1142,13 +1336,14 @@ __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, 
   __shared__ float4 part_sum[kFewThreads / 32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = blockIdx.x >> 7, h = (blockIdx.x >> 1) & 63;
-  const int t = u / g.groups, h0 = (u % g.groups) * g.group;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (h >= min(g.group, g.a.n_heads - h0)) return;
+  if (h >= g.n_cols) return;
   const int2 span = __ldcg(&parts->span[u]);
   const int c0 = span.x, n = span.y;
   if (n <= 1) return;  // one CTA wrote it all
+  const Columns col(g, u);
+  if (h >= col.n) return;
   auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
   const int d0 = 256 * (blockIdx.x & 1) + 128 * (warp & 1) + 4 * lane, deal = warp >> 1;
   // the first parts on their way, then the weights
@@ -1207,10 +1402,10 @@ __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, 
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   const int d = 8 * v_chunk_back(d0 >> 3) + (d0 & 4);
-  *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
+  *reinterpret_cast<uint2 *>(g.a.out + col.at(g, h, g.a.out_stride, kDim) + d) =
       make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
   if (threadIdx.x == 0 && (blockIdx.x & 1) == 0 && g.a.lse != nullptr)
-    g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (lmax + log2f(s)) * 0.6931471805599453f : -INFINITY;
+    g.a.lse[col.at(g, h, g.a.n_heads, 1)] = s == 0.0f ? -INFINITY : (lmax + log2f(s)) * 0.6931471805599453f;
 }
 
 // The same where a unit has at most kShortParts tiles (short lists): a warp takes 128
@@ -1219,13 +1414,14 @@ constexpr int kShortParts = 16, kShortThreads = 256;
 __global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args g, const Parts *__restrict__ parts) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = blockIdx.x >> 5, h = 2 * (blockIdx.x & 31) + (warp >> 2);
-  const int t = u / g.groups, h0 = (u % g.groups) * g.group;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (h >= min(g.group, g.a.n_heads - h0)) return;
+  if (h >= g.n_cols) return;
   const int2 span = __ldcg(&parts->span[u]);
   const int c0 = span.x, n = span.y;
   if (n <= 1) return;  // one CTA wrote it all
+  const Columns col(g, u);
+  if (h >= col.n) return;
   auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
   const int d0 = 128 * (warp & 3) + 4 * lane;
   const float x = lane < n ? __ldcg(&parts->lse2[slot(lane)][h]) : -INFINITY;
@@ -1254,38 +1450,52 @@ __global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
   const int d = 8 * v_chunk_back(d0 >> 3) + (d0 & 4);
-  *reinterpret_cast<uint2 *>(g.a.out + int64_t(t) * g.a.out_stride + int64_t(h0 + h) * kDim + d) =
+  *reinterpret_cast<uint2 *>(g.a.out + col.at(g, h, g.a.out_stride, kDim) + d) =
       make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
   if (lane == 0 && (warp & 3) == 0 && g.a.lse != nullptr)
-    g.a.lse[int64_t(t) * g.a.n_heads + h0 + h] = s > 0.0f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+    g.a.lse[col.at(g, h, g.a.n_heads, 1)] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts); }
+size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts) + sizeof(Plan); }
 
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream) {
-  static std::atomic<uint64_t> smem_set{0};
+  static std::atomic<uint64_t> smem_set[2];
   const int smem = int(sizeof(Smem));
-  cudaError_t e = set_max_smem_once(paged_attn_kernel, smem, smem_set);
+  cudaError_t e = set_max_smem_once(paged_attn_kernel<false>, smem, smem_set[0]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<true>, smem, smem_set[1]);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  Args g{a, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0, 0};
+  WsHeader *hdr = static_cast<WsHeader *>(ws);
+  Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
+  Plan *plan = reinterpret_cast<Plan *>(parts + 1);
+  // Several tokens a unit where two or more fit its columns and some sequence must
+  // have two (24 sequences of 5 tokens, 20 heads, 4500 rows: 96 us by single tokens)
+  const int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
+  const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs;
+  Args g{a, packed ? plan : nullptr, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0, 0, 0};
   g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;
-  g.group = (a.n_heads + g.groups - 1) / g.groups;
+  g.group = packed ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
+  g.per_head = 65536 / a.n_heads + 1;
   g.n_cols = (g.group + 15) / 16 * 16;
   // no more CTAs than there can be tiles
   const int64_t rows = a.idx != nullptr ? a.k : int64_t(a.c.seq_pages) << a.c.page_log2;
   const int64_t most = int64_t(a.n_tokens) * g.groups * ((rows + kTile - 1) / kTile);
   const int ctas = int(most < sms ? most : sms) < kMaxCtas ? int(most < sms ? most : sms) : kMaxCtas;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
-  WsHeader *hdr = static_cast<WsHeader *>(ws);
-  Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
-  e = launch_pdl(paged_attn_kernel, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, g, parts, hdr);
+  if (packed) {
+    e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
+    if (e != cudaSuccess) return e;
+  }
+  e = packed ? launch_pdl(paged_attn_kernel<true>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
+                          ArgsFor<true>(g), parts, hdr)
+             : launch_pdl(paged_attn_kernel<false>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
+                          ArgsFor<false>(g), parts, hdr);
   if (e != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;  // nothing is split
   if (g.few && (rows + kTile - 1) / kTile <= kShortParts)

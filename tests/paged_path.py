@@ -69,7 +69,7 @@ def check_token(out, lse, v, q, scale):
     small = 8 * (8 * 2.0 ** -25 * len(v) * (p * big).max(axis=1) + 2.0 ** -25 * (p @ big))
     size = p @ np.abs(v)
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * dl[:, None] + 2.0 ** -18) * size + small[:, None]
-    bad = np.abs(out - ref) > tol
+    bad = ~(np.abs(out - ref) <= tol)
     assert not bad.any(), (f"{bad.sum()} of {bad.size} outside, worst {np.abs(out - ref).max()} at tolerance "
                            f"{tol.flat[np.abs(out - ref).argmax()]}")
     if lse is not None:

@@ -123,6 +123,112 @@ def test_logits_that_move_the_maximum(order):
     check(pool, [1], qv, lambda t, s: np.arange(n), got, lse)
 
 
+@pytest.mark.parametrize("shift", [-900.0, -200.0, 200.0, 900.0])
+def test_logits_far_from_zero(shift):
+    """Every logit far below or above zero, in a list whose first tiles hold no row
+    and in a whole range."""
+    rng = np.random.default_rng(70)
+    n = 500
+    d = rng.standard_normal(512)
+    d /= np.linalg.norm(d)
+    x = (4.0 * d + 0.2 * rng.standard_normal((n, 512))).astype(np.float32)
+    pool = Pool([n], 32, 71, x=[x])
+    qb, qv = bf16((d * shift / 4.0 / SCALE + rng.standard_normal((1, 64, 512)) * 0.1))
+    got, lse = run(pool, [1], qb, end=[n])
+    check(pool, [1], qv, lambda t, s: np.arange(n), got, lse)
+    idx = np.full((1, 700), -1, dtype=np.int32)
+    idx[0, 200:] = rng.integers(0, n, 500)
+    got, lse = run(pool, [1], qb, idx=idx, n_rows=[n])
+    check(pool, [1], qv, lambda t, s: idx[0, 200:], got, lse)
+    # one worker for all tiles: the same among many tokens
+    T = 200
+    many = np.tile(idx, (T, 1))
+    q2 = np.tile(qb, (T, 1, 1))
+    got, lse = run(pool, [T], q2, idx=many, n_rows=[n])
+    for t in (0, 7, 77, T - 1):
+        check_token(C.bf16_decode(got).astype(np.float64)[t], lse[t].astype(np.float64), pool.values(0, idx[0, 200:]), qv[0], SCALE)
+
+
+@pytest.mark.parametrize("heads", [1, 4, 8, 16, 20, 21, 31, 32, 33])
+@pytest.mark.parametrize("window", [0, 70, 400])
+def test_few_heads_many_tokens(heads, window):
+    """Several tokens share a pass over their sequence's rows: chunks, drafts and
+    lone tokens side by side, causal, windowed, with empty and far-apart ranges."""
+    rng = np.random.default_rng(72)
+    rows, tokens = [900, 0, 333, 64, 1500, 10], [37, 3, 1, 8, 0, 5]
+    pool = Pool(rows, 16, 73)
+    n = sum(tokens)
+    seq = np.repeat(np.arange(6), tokens)
+    end = np.concatenate([np.maximum(0, r - (c - 1 - np.arange(c))) for r, c in zip(rows, tokens)]).astype(np.int64)
+    begin = np.maximum(0, end - window) if window else np.zeros(n, dtype=np.int64)
+    end[[2, 9]] = 0                       # a token that sees nothing among ones that do
+    begin[5], end[5] = 870, 871           # neighbours whose ranges do not meet
+    begin[6], end[6] = 0, 3
+    q, qv = queries(n + 2, heads, 74)
+    got, lse = run(pool, tokens, q, begin=np.append(begin, [0, 0]), end=np.append(end, [9, 9]), pad=8)
+    check(pool, tokens, qv, lambda t, s: np.arange(begin[t], max(end[t], begin[t])), got, lse)
+
+
+@pytest.mark.parametrize("heads", [5, 16])
+def test_few_heads_over_long_rows_and_many_units(heads):
+    pool = Pool([6000, 200], 64, 75)
+    tokens = [130, 70]
+    n = sum(tokens)
+    end = np.concatenate([6000 - 129 + np.arange(130), 200 - 69 + np.arange(70)])
+    q, qv = queries(n, heads, 76)
+    got, lse = run(pool, tokens, q, end=end)
+    check(pool, tokens, qv, lambda t, s: np.arange(end[t]), got, lse)
+    again, lse2 = run(pool, tokens, q, end=end)
+    assert np.array_equal(got, again) and np.array_equal(lse.view(np.uint32), lse2.view(np.uint32))
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+def test_a_head_does_not_touch_its_neighbours(heads):
+    """Heads and tokens of very different size side by side; then NaN and infinity in
+    some: the others' results stay bit for bit."""
+    pool = Pool([500], 32, 80)
+    rng = np.random.default_rng(81)
+    size = rng.integers(-60, 5, (9, heads, 1))
+    q, qv = bf16(rng.standard_normal((9, heads, 512)) * 2.0**size)
+    end = 500 - 8 + np.arange(9)
+    got, lse = run(pool, [9], q, end=end)
+    check(pool, [9], qv, lambda t, s: np.arange(end[t]), got, lse)
+    bad = q.copy()
+    bad[2, 3, 17], bad[5, :, 100], bad[7, 0, 511], bad[7, 1, 0] = 0x7FC0, 0x7F80, 0xFF80, 0xFFC1
+    hit = np.zeros((9, heads), dtype=bool)
+    hit[2, 3] = hit[5] = hit[7, :2] = True
+    got2, lse2 = run(pool, [9], bad, end=end)
+    assert np.array_equal(got2[~hit], got[~hit])
+    assert np.array_equal(lse2[~hit].view(np.uint32), lse[~hit].view(np.uint32))
+    # (an infinite query has no finite logit: its softmax is NaN as well)
+    assert np.isnan(C.bf16_decode(got2[hit])).all() and np.isnan(lse2[hit]).all()
+    # the same where a unit's parts are joined, by each of the joins
+    idx = np.tile(np.arange(500, dtype=np.int32), (9, 1))
+    for n in (1, 9, 40):
+        i = np.resize(idx, (n, 500))
+        out, l = run(pool, [n], np.resize(bad, (n, heads, 512)), idx=i, n_rows=[500])
+        h = np.resize(hit, (n, heads))
+        assert np.array_equal(np.isnan(C.bf16_decode(out)).all(axis=2), h) and np.array_equal(np.isnan(l), h)
+        assert np.array_equal(np.isnan(C.bf16_decode(out)).any(axis=2), h)
+    long = Pool([9000], 64, 84)
+    out, l = run(long, [1], bad[2:3], end=[9000])
+    assert np.array_equal(np.isnan(C.bf16_decode(out)).all(axis=2), hit[2:3]) and np.array_equal(np.isnan(l), hit[2:3])
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+def test_a_token_that_sees_nothing_is_zeros_whatever_its_query(heads):
+    pool = Pool([90, 0], 16, 82)
+    q, qv = queries(4, heads, 83)
+    q[1] = 0x7FC0
+    q[3] = 0xFF80
+    got, lse = run(pool, [3, 1], q, end=[70, 0, 90, 0])
+    check(pool, [3, 1], qv, lambda t, s: np.arange([70, 0, 90, 0][t]), got, lse)
+    idx = np.full((4, 80), -1, dtype=np.int32)
+    idx[0, :70], idx[2, :70] = np.arange(70), np.arange(20, 90)
+    got, lse = run(pool, [3, 1], q, idx=idx, n_rows=[90, 0])
+    check(pool, [3, 1], qv, lambda t, s: idx[t][idx[t] >= 0], got, lse)
+
+
 @pytest.mark.parametrize("spread", [0, 6, 12, 20, 60])
 def test_row_and_block_scale_spread(spread):
     """Each block and each row at its own power of two, the RoPE part too: rows
