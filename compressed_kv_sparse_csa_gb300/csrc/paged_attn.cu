@@ -1474,19 +1474,23 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   WsHeader *hdr = static_cast<WsHeader *>(ws);
   Parts *parts = reinterpret_cast<Parts *>(hdr + 1);
   Plan *plan = reinterpret_cast<Plan *>(parts + 1);
-  // Several tokens a unit where two or more fit its columns and some sequence must
-  // have two (24 sequences of 5 tokens, 20 heads, 4500 rows: 96 us by single tokens)
+  // no more CTAs than there can be tiles
+  const int64_t rows = a.idx != nullptr ? a.k : int64_t(a.c.seq_pages) << a.c.page_log2;
+  const int groups = (a.n_heads + kHeads - 1) / kHeads;
+  const int64_t most = int64_t(a.n_tokens) * groups * ((rows + kTile - 1) / kTile);
+  const int ctas = int(most < sms ? most : sms) < kMaxCtas ? int(most < sms ? most : sms) : kMaxCtas;
+  // Several tokens a unit where two or more fit its columns, some sequence must have
+  // two, and single tokens could fill more than two tiles a CTA: below that the plan's
+  // launch costs more than the passes that it saves.  Packed / single, us a call:
+  // 1 sequence x 2 tokens x 20 heads x 700 rows 17.1 / 12.2, 8 x 2 x 16 x 2000
+  // 22.4 / 23.0, 24 x 5 x 20 x 4500 66 / 130, 1 x 512 x 16 x 4096 124 / 420.
   const int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
-  const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs;
-  Args g{a, packed ? plan : nullptr, (a.n_heads + kHeads - 1) / kHeads, 0, 0, 0, 0, 0};
+  const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas;
+  Args g{a, packed ? plan : nullptr, groups, 0, 0, 0, 0, 0};
   g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;
   g.group = packed ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
   g.per_head = 65536 / a.n_heads + 1;
   g.n_cols = (g.group + 15) / 16 * 16;
-  // no more CTAs than there can be tiles
-  const int64_t rows = a.idx != nullptr ? a.k : int64_t(a.c.seq_pages) << a.c.page_log2;
-  const int64_t most = int64_t(a.n_tokens) * g.groups * ((rows + kTile - 1) / kTile);
-  const int ctas = int(most < sms ? most : sms) < kMaxCtas ? int(most < sms ? most : sms) : kMaxCtas;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
   if (packed) {
     e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);

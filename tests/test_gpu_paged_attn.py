@@ -186,18 +186,18 @@ def test_few_heads_over_long_rows_and_many_units(heads):
 def test_a_head_does_not_touch_its_neighbours(heads):
     """Heads and tokens of very different size side by side; then NaN and infinity in
     some: the others' results stay bit for bit."""
-    pool = Pool([500], 32, 80)
+    pool = Pool([500, 4000], 32, 80)  # (room enough that few heads' tokens share passes)
     rng = np.random.default_rng(81)
     size = rng.integers(-60, 5, (9, heads, 1))
     q, qv = bf16(rng.standard_normal((9, heads, 512)) * 2.0**size)
     end = 500 - 8 + np.arange(9)
-    got, lse = run(pool, [9], q, end=end)
-    check(pool, [9], qv, lambda t, s: np.arange(end[t]), got, lse)
+    got, lse = run(pool, [9, 0], q, end=end)
+    check(pool, [9, 0], qv, lambda t, s: np.arange(end[t]), got, lse)
     bad = q.copy()
     bad[2, 3, 17], bad[5, :, 100], bad[7, 0, 511], bad[7, 1, 0] = 0x7FC0, 0x7F80, 0xFF80, 0xFFC1
     hit = np.zeros((9, heads), dtype=bool)
     hit[2, 3] = hit[5] = hit[7, :2] = True
-    got2, lse2 = run(pool, [9], bad, end=end)
+    got2, lse2 = run(pool, [9, 0], bad, end=end)
     assert np.array_equal(got2[~hit], got[~hit])
     assert np.array_equal(lse2[~hit].view(np.uint32), lse[~hit].view(np.uint32))
     # (an infinite query has no finite logit: its softmax is NaN as well)
@@ -206,7 +206,7 @@ def test_a_head_does_not_touch_its_neighbours(heads):
     idx = np.tile(np.arange(500, dtype=np.int32), (9, 1))
     for n in (1, 9, 40):
         i = np.resize(idx, (n, 500))
-        out, l = run(pool, [n], np.resize(bad, (n, heads, 512)), idx=i, n_rows=[500])
+        out, l = run(pool, [n, 0], np.resize(bad, (n, heads, 512)), idx=i, n_rows=[500, 0])
         h = np.resize(hit, (n, heads))
         assert np.array_equal(np.isnan(C.bf16_decode(out)).all(axis=2), h) and np.array_equal(np.isnan(l), h)
         assert np.array_equal(np.isnan(C.bf16_decode(out)).any(axis=2), h)
@@ -217,16 +217,16 @@ def test_a_head_does_not_touch_its_neighbours(heads):
 
 @pytest.mark.parametrize("heads", [8, 64])
 def test_a_token_that_sees_nothing_is_zeros_whatever_its_query(heads):
-    pool = Pool([90, 0], 16, 82)
+    pool = Pool([90, 0, 9000], 16, 82)
     q, qv = queries(4, heads, 83)
     q[1] = 0x7FC0
     q[3] = 0xFF80
-    got, lse = run(pool, [3, 1], q, end=[70, 0, 90, 0])
-    check(pool, [3, 1], qv, lambda t, s: np.arange([70, 0, 90, 0][t]), got, lse)
+    got, lse = run(pool, [3, 1, 0], q, end=[70, 0, 90, 0])
+    check(pool, [3, 1, 0], qv, lambda t, s: np.arange([70, 0, 90, 0][t]), got, lse)
     idx = np.full((4, 80), -1, dtype=np.int32)
     idx[0, :70], idx[2, :70] = np.arange(70), np.arange(20, 90)
-    got, lse = run(pool, [3, 1], q, idx=idx, n_rows=[90, 0])
-    check(pool, [3, 1], qv, lambda t, s: idx[t][idx[t] >= 0], got, lse)
+    got, lse = run(pool, [3, 1, 0], q, idx=idx, n_rows=[90, 0, 0])
+    check(pool, [3, 1, 0], qv, lambda t, s: idx[t][idx[t] >= 0], got, lse)
 
 
 @pytest.mark.parametrize("spread", [0, 6, 12, 20, 60])
@@ -401,6 +401,81 @@ def test_captured_call_follows_its_inputs_on_another_stream():
         check(pool, [1, 1], qv, lambda t, s: np.arange(ends[s]), bf16_host_bits(outs[0]), lses[0].cpu().numpy())
         check(pool, [1, 1], qv, lambda t, s: ix[t][ix[t] >= 0], bf16_host_bits(outs[1]), lses[1].cpu().numpy())
     assert B.ds4x_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("heads", [12, 64])
+def test_captured_ragged_tokens(heads):
+    """One graph, replayed with the tokens dealt otherwise over the sequences (few
+    heads: other plans) and other lengths; tokens behind the last sequence stay."""
+    B = require_gpu()
+    rows, n = [700, 3000, 40], 40
+    pool = Pool(rows, 64, 90)
+    pages, table = dev(pool.pages), dev(pool.table)
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    end = torch.zeros(n, dtype=torch.int64, device="cuda")
+    q, qv = queries(n, heads, 91)
+    qd = bf16_dev(q)
+    out, lse = torch.zeros_like(qd), torch.zeros((n, heads), device="cuda")
+    B.ds4x_paged_attn(pages, 64, table, cu, end, qd, SCALE, out, lse, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.ds4x_paged_attn(pages, 64, table, cu, end, qd, SCALE, out, lse, ws)
+    rng = np.random.default_rng(92)
+    for tokens in ([40, 0, 0], [0, 0, 0], [1, 30, 4], [13, 13, 14], [0, 40, 0]):
+        ends = np.array([rng.integers(0, rows[s] + 1) for s in np.repeat(np.arange(3), tokens)] + [5] * (n - sum(tokens)))
+        cu.copy_(dev(np.concatenate([[0], np.cumsum(tokens)]).astype(np.int32)))
+        end.copy_(dev(ends.astype(np.int64)))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check(pool, tokens, qv, lambda t, s: np.arange(ends[t]), bf16_host_bits(out), lse.cpu().numpy())
+    assert B.ds4x_workspace_status(ws) == 0
+
+
+def test_thousands_of_sequences():
+    """More sequences than a plan holds at once; the last ones' tokens and rows."""
+    S, heads = 4200, 16
+    rng = np.random.default_rng(93)
+    rows = rng.integers(0, 12, S)
+    tokens = np.ones(S, dtype=int)
+    tokens[[0, 9, 4095, 4096, S - 1]] = 5, 0, 4, 6, 7
+    pool = Pool(list(rows), 16, 94)
+    n = tokens.sum()
+    seq = np.repeat(np.arange(S), tokens)
+    end = np.array([rng.integers(0, rows[s] + 1) for s in seq])
+    q, qv = queries(n, heads, 95)
+    got, lse = run(pool, list(tokens), q, end=end)
+    out = C.bf16_decode(got).astype(np.float64)
+    for t in [*range(0, 12), *range(12, n, 401), *range(int(np.argmax(seq == 4094)), int(np.argmax(seq == 4098))), *range(n - 9, n)]:
+        check_token(out[t], lse[t].astype(np.float64), pool.values(seq[t], np.arange(end[t])), qv[t], SCALE)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its workspace, its own cache and other shapes."""
+    B = require_gpu()
+    pools = [Pool([3000, 100], 64, 96), Pool([500, 2500], 16, 97)]
+    shapes = [([1, 1], 64), ([30, 9], 10)]
+    jobs = []
+    for pool, (tokens, heads) in zip(pools, shapes):
+        n = sum(tokens)
+        end = np.repeat([pool.rows[0], pool.rows[1]], tokens) - np.arange(n) % 7
+        q, qv = queries(n, heads, 98 + n)
+        a = dict(pages=dev(pool.pages), table=dev(pool.table), cu=dev(np.concatenate([[0], np.cumsum(tokens)]).astype(np.int32)),
+                 end=dev(end.astype(np.int64)), q=bf16_dev(q), ws=new_ws(B.ds4x_paged_attn_workspace()),
+                 out=torch.zeros((n, heads, 512), dtype=torch.bfloat16, device="cuda"), lse=torch.zeros((n, heads), device="cuda"))
+        jobs.append((pool, tokens, qv, end, a, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for pool, _, _, _, a, stream in jobs:
+            with torch.cuda.stream(stream):
+                B.ds4x_paged_attn(a["pages"], pool.R, a["table"], a["cu"], a["end"], a["q"], SCALE, a["out"], a["lse"], a["ws"])
+    torch.cuda.synchronize()
+    for pool, tokens, qv, end, a, _ in jobs:
+        assert B.ds4x_workspace_status(a["ws"]) == 0
+        check(pool, tokens, qv, lambda t, s: np.arange(end[t]), bf16_host_bits(a["out"]), a["lse"].cpu().numpy())
 
 
 def test_append_select_attend_together():
