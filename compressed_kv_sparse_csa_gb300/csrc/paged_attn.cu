@@ -4,12 +4,14 @@
 //   lse_h = log sum_j e^(l_hj)
 //
 // over a token's rows: the range [row_begin, row_end) of its sequence, or its
-// own list of rows.  A unit is a token and up to 64 of its heads; its rows come
-// in tiles of 64.  Two tcgen05.mma (kind::f16, fp16 operands, fp32 sums in
-// tensor memory) a tile:
+// own list of rows.  A unit is a token and up to 64 of its heads, or, where heads
+// are few, several neighbouring tokens of one sequence with all their heads
+// (paged_plan_kernel): up to 64 query vectors, its columns.  Its rows come in tiles
+// of 64.  Two tcgen05.mma (kind::f16, fp16 operands, fp32 sums in tensor memory) a
+// tile:
 //
-//   S^T[64 rows][heads] = V'[64 rows][512] . Q'[heads][512]^T
-//   O^T[512 dims][heads] += V'^T[512][64 rows] . P^T[64 rows][heads]
+//   S^T[64 rows][columns] = V'[64 rows][512] . Q'[columns][512]^T
+//   O^T[512 dims][columns] += V'^T[512][64 rows] . P^T[64 rows][columns]
 //
 // V' is the tile's rows widened once to fp16, in shared memory, as eight
 // 128-byte-swizzled panels of 64 dims (16-byte chunk c of row r at c ^ (r % 8); which
@@ -19,12 +21,13 @@
 // Exact operands.  Row j's exponent E_j is its RoPE part's, the row's largest:
 // V'_j = v_j 2^-E_j, at most 8, is exact in fp16 while a block's scale lies
 // within 2^14 of 2^E_j (smaller blocks round at 2^-25 of 2^E_j); the RoPE part's
-// fp16 values are V' as they are.  Q' = q 2^c in fp16, c taking the unit's
-// largest |q| into [2^14, 2^15): a bf16 value is exact down to 2^-32 of it.
+// fp16 values are V' as they are.  Q' = q 2^c in fp16, c taking the vector's
+// largest |q| into [2^14, 2^15): a bf16 value is exact down to 2^-32 of it.  (One c
+// a unit was 1.5 % faster and let a large head round away a small one beside it.)
 //
 // Softmax in the log2 domain, online, with the row's exponent kept apart:
 // x_j = l_j log2 e + E_j, w_j = 2^(x_j - m) is what multiplies V'_j, and the
-// denominator is sum_j w_j 2^-E_j.  m is a head's running maximum of x, lazily: it
+// denominator is sum_j w_j 2^-E_j.  m is a column's running maximum of x, lazily: it
 // moves (and O^T and the sums are rescaled) only when a tile's x exceeds it by
 // more than 8, so w stays below 2^8.  w enters the second product as fp16 (half
 // a step is 2^-12 to 2^-11 of it, an eighth of the bf16 output's own step; hi +
@@ -35,20 +38,30 @@
 // an SM), so any mix of lengths fills the GPU; a cut that falls near a unit's
 // end moves there.  A unit that one CTA covers goes straight to the output; the
 // parts of the others go to the workspace in fp32, normalised, with their
-// log-sum-exp, and paged_combine_kernel joins them in a fixed order.  The cuts
+// log-sum-exp, and a second kernel joins them in a fixed order.  The cuts
 // depend on the lengths alone, so results do not depend on timing.
 //
-// Roles (28 warps).  L (warp 0): finds the rows of the tiles to come (list entry,
-// page table), four tiles ahead, and asks for them into L2.  W (4-19): widens the
-// tiles into two V' buffers in turn, with the 16-byte words of the next two tiles on
-// their way into registers meanwhile.
-// X (20-27): the softmax, four 16-row quarters of S^T by two halves of the heads;
+// Roles (20 warps).  L (warp 0): finds the rows of the tiles to come (list entry,
+// page table), four tiles ahead, and asks for them into L2.  W (4-11): widens the
+// tiles into two V' buffers in turn, two rows a lane, with the 16-byte words of the
+// next two tiles on their way into registers meanwhile.
+// X (12-19): the softmax, four 16-row quarters of S^T by two halves of the columns;
 // when a unit ends, the next one's Q' first, then the output.  M (1-3): issue the
 // products, a thread each for S of the even tiles, S of the odd ones and O: a
 // thread that has committed MMAs is held at its next barrier until they are done,
 // so one thread for all of them left the tensor core idle between tiles.
 // Registers go from L, M and W to X (setmaxnreg): the softmax must not spill,
 // because local loads queue behind W's.
+//
+// What bounds it.  Long histories and chunks: the chain of a tile, widen -> S ->
+// softmax -> O, about 3300 cycles a tile with the two V' buffers that shared memory
+// holds (64 KB each beside 64 KB of Q'), of which the products fill 55 % (M = 64
+// rows make S run at half the tensor rate): 64 heads over 1,048,576 rows 190 us
+// (2.0 TB/s of packed rows, 0.72 PFLOP/s), a chunk of 2048 tokens over 8192 rows
+// 2.43 ms (0.79 PFLOP/s).  Two tiles' loads in flight and a third product queue
+// took it there from 307 us.  Short histories: latency, 10 us for the kernel (its
+// launch, the cuts, one round trip to the rows, three tiles' chain) and 1.4 to 3.5
+// us for the join: 777 rows 13.3 us, 8192 rows 20.3 us.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
@@ -577,6 +590,11 @@ __device__ __forceinline__ void load_raw(const Found &at, int l, Raw &w) {
   }
 }
 
+// NaN and infinities to the largest fp16 values.
+__device__ __forceinline__ uint32_t finite_half2(uint32_t v) {
+  asm("{\n\t.reg .b32 t;\n\tmax.f16x2 t, %0, %1;\n\tmin.f16x2 %0, t, %2;\n\t}" : "+r"(v) : "r"(0xfbfffbffu), "r"(0x7bff7bffu));
+  return v;
+}
 // Eight codes times the factor pair f, as fp16, to shared memory.
 __device__ __forceinline__ void widen8(uint32_t addr, uint32_t w, uint32_t f) {
   uint32_t h0, h1, h2, h3;
@@ -597,9 +615,12 @@ __device__ __forceinline__ void widen_low(uint32_t row, uint32_t x, int l, const
   widen8(pa + 2 * 8192, w.a.z, f);
   widen8(pa + 3 * 8192, w.a.w, f);
 }
+template <class A>
 __device__ __forceinline__ void widen_high(uint32_t row, uint32_t x, int l, const uint32_t (&off_b)[4], const Raw &w) {
   const int E = int((w.sc.w >> 16) & 0xffu);
-  sts16(row + 7 * 8192 + (uint32_t(l << 4) ^ x), w.t.x, w.t.y, w.t.z, w.t.w);
+  // (packed: a row that only one token sees must not reach the others by 0 * NaN)
+  auto t = [](uint32_t v) { return A::packed() ? finite_half2(v) : v; };
+  sts16(row + 7 * 8192 + (uint32_t(l << 4) ^ x), t(w.t.x), t(w.t.y), t(w.t.z), t(w.t.w));
   if (l < 6) {
     const uint32_t f = pow2_half2(min(0, int(((l & 4 ? w.sc.w : w.sc.z) >> (8 * (l & 3))) & 0xffu) - E));
     widen8(row + (off_b[0] ^ x), w.b.x, f);
@@ -683,8 +704,8 @@ __device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHea
     widen_low(row, x, l, raw[0]);
     widen_low(row + 4 * 128, x ^ 64u, l, raw[1]);
     if (i >= 2) wait_bar(sm, &sm.pvdone[buf][1], ((i >> 1) - 1) & 1, hdr);
-    widen_high(row, x, l, off_b, raw[0]);
-    widen_high(row + 4 * 128, x ^ 64u, l, off_b, raw[1]);
+    widen_high<A>(row, x, l, off_b, raw[0]);
+    widen_high<A>(row + 4 * 128, x ^ 64u, l, off_b, raw[1]);
     if (l < 2) {
       const uint32_t scw = l ? raw[1].sc.w : raw[0].sc.w;
       const int E = int((scw >> 16) & 0xffu) - 127;
@@ -1064,8 +1085,9 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
   }
 }
 
-// Packs tokens into units: the tokens of a sequence by threes, or however many times
-// n_heads fits 64 columns, in order.  One block.
+// Packs tokens into units: the tokens of a sequence in order, as many as n_heads
+// goes into 64 columns, so that a row is widened once for all of them and the
+// products' 64 columns are full.  One block; bound by latency (about 3 us).
 constexpr int kPlanThreads = 1024, kPlanSeqs = 4096;
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, int pack, Plan *__restrict__ plan,
                                                                   WsHeader *__restrict__ hdr) {
@@ -1084,7 +1106,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
   int base = 0;
   for (int c0 = 0; c0 < valid; c0 += kPlanThreads) {
     const int t = c0 + tid;
-    Pack u{t, 0, 0, 0};
+    int count = 0, units = 0;  // the tokens from t on, and the units they make
+    Pack u{t, 1, 0, 0};
     if (t < valid) {
       int s = 0, n = n_seqs;  // the last sequence that begins at or before t
       while (n > 1) {
@@ -1093,34 +1116,45 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         else n = half;
       }
       const int from = cu(s), to = min(valid, cu(s + 1));
-      const bool in = from <= t && t < to;  // (else cu is not what it should be: a unit without a row)
-      if (!in || (t - from) % pack == 0) {
-        u.count = in ? min(pack, to - t) : 1;
-        int64_t lo = INT64_MAX, hi = 0;
-        for (int j = 0; j < u.count; ++j) {
-          const Rows r = in ? token_rows(a, t + j) : Rows{0, 0};
-          if (r.n > 0) {
-            lo = min(lo, r.r0);
-            hi = max(hi, r.r0 + r.n);
-          }
+      if (!(from <= t && t < to)) {  // (cu is not what it should be: a unit without a row)
+        units = 1;
+      } else if ((t - from) % pack == 0) {
+        count = min(pack, to - t);
+        int rest = 0;  // tokens whose rows do not meet those from lo to hi
+        int64_t lo = 0, hi = 0;
+        for (int j = 0; j < count; ++j) {
           if (__ldcg(a.row_end + t + j) > room) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+          const Rows r = token_rows(a, t + j);
+          if (r.n == 0) continue;
+          if (hi == 0) lo = r.r0, hi = r.r0 + r.n;
+          else if (r.r0 > hi || r.r0 + r.n < lo) ++rest;
+          else lo = min(lo, r.r0), hi = max(hi, r.r0 + r.n);
         }
-        if (hi > 0) {
-          u.r0 = int(lo);
-          u.n = int(hi - lo);
-        }
+        // Rows between the tokens' ranges, which no token sees, must not be read (and
+        // would be work for nothing): then each token is its own unit.
+        units = rest > 0 ? count : 1;
+        u = Pack{t, count, int32_t(lo), int32_t(hi - lo)};
       }
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, u.count > 0);
-    if (lane == 0) warps[warp] = __popc(b);
-    __syncthreads();
-    int before = __popc(b & ((1u << lane) - 1)), all = 0;
-    for (int k = 0; k < kPlanThreads / 32; ++k) {
-      if (k < warp) before += warps[k];
-      all += warps[k];
+    int incl = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-    if (u.count > 0) plan->unit[base + before] = u;
-    base += all;
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+    int at = base + incl - units;
+    for (int k = 0; k < kPlanThreads / 32; ++k) {
+      if (k < warp) at += warps[k];
+      base += warps[k];
+    }
+    if (units == 1) plan->unit[at] = u;
+    if (units > 1)
+      for (int j = 0; j < count; ++j) {
+        const Rows r = token_rows(a, t + j);
+        plan->unit[at + j] = Pack{t + j, 1, int32_t(r.r0), r.n};
+      }
     __syncthreads();
   }
   if (tid == 0) plan->n_units = base;
@@ -1329,7 +1363,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
 }
 
 // The same for at most kFewUnits units, where a call's latency counts: a block takes
-// 256 dims of a head, its parts dealt over four pairs of warps; no list to make first.
+// 256 dims of a head, its parts dealt over four pairs of warps; no list to make first
+// (the units' spans are written by the CTAs that begin them).  A call over 777 rows
+// takes 13.4 us so, 15.6 by the list; 16 sessions of 8192 to 65536 rows 97.9 us, and
+// 105.5 where kFewUnits is 4.
 constexpr int kFewThreads = 256;
 __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, const Parts *__restrict__ parts) {
   __shared__ float wts[kMaxCtas], lsum, lmax;
@@ -1409,7 +1446,8 @@ __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, 
 }
 
 // The same where a unit has at most kShortParts tiles (short lists): a warp takes 128
-// dims of a head with all its parts on their way at once, and nothing is shared.
+// dims of a head with all its parts on their way at once, and nothing is shared (16
+// sessions' lists of 512 rows: 17.5 us a call, 20.8 by the kernel above).
 constexpr int kShortParts = 16, kShortThreads = 256;
 __global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args g, const Parts *__restrict__ parts) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

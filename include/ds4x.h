@@ -565,8 +565,8 @@ size_t ds4x_paged_attn_workspace(void);
  *   l_hj = softmax_scale * (q_h . v_j);  o_h = sum_j softmax_j(l_h)_j v_j;
  *   lse_h = log sum_j e^(l_hj)
  *
- *   row_begin  i64 [n_tokens] or NULL (0); row_end i64 [n_tokens].  A token
- *              with row_end <= row_begin sees nothing: zeros, lse -inf
+ *   row_begin  i64 [n_tokens] or NULL (0), below 0: 0; row_end i64 [n_tokens].
+ *              A token with row_end <= row_begin sees nothing: zeros, lse -inf
  *   n_tokens   1 .. DS4X_PAGED_MAX_TOKENS
  *   n_heads    1 .. DS4X_PAGED_MAX_HEADS
  *   q_bf16     bf16 [n_tokens][n_heads][512], q_stride elements from token to
@@ -578,8 +578,12 @@ size_t ds4x_paged_attn_workspace(void);
  *              use; not for two calls that may overlap on the GPU (two
  *              captured graphs that may run at once need one each)
  *
- * Rows outside the range are never read, so what unwritten rows hold does not
- * matter.  Results do not depend on the order in which the GPU works.
+ * A row that no token sees is never read, so what unwritten rows hold does not
+ * matter; a row that only some tokens see has no part in the others' results
+ * (few heads: neighbouring tokens of a sequence may share a pass over its rows).
+ * Nor has a token's or a head's query, whatever it holds: NaN or infinity in
+ * one makes that one's output and lse NaN.  Results do not depend on the order
+ * in which the GPU works.
  */
 int ds4x_paged_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
                     int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row_begin,

@@ -169,6 +169,32 @@ def test_few_heads_many_tokens(heads, window):
     check(pool, tokens, qv, lambda t, s: np.arange(begin[t], max(end[t], begin[t])), got, lse)
 
 
+@pytest.mark.parametrize("heads", [8, 20, 64])
+def test_rows_that_only_some_tokens_see(heads):
+    """A drafted token's range that reaches into rows never written (NaN where their
+    values would be) leaves its neighbours' results alone; pages between the tokens'
+    ranges that no token sees may be anywhere."""
+    R, seen = 16, 1000
+    pool = Pool([seen + 40, 4000], R, 77)
+    codes, tails = R * 224, R * 128
+    for j in range(seen, seen + 40):  # plausible scales, NaN and infinities for values
+        page = pool.pages[pool.table[0, j // R]]
+        page[codes + 128 * (j % R):codes + 128 * (j % R) + 128] = [0x00, 0x7E, 0x00, 0x7C, 0x00, 0xFC, 0x01, 0xFE] * 16
+        page[codes + tails + 16 * (j % R):][:16] = [200] * 15 + [0]
+    end = np.array([seen - 2, seen - 1, seen + 7, seen + 40, seen, seen - 3])
+    begin = np.array([0, 400, 0, 900, 0, -5])
+    q, qv = queries(6, heads, 78)
+    got, lse = run(pool, [6, 0], q, begin=begin, end=end)
+    out = C.bf16_decode(got).astype(np.float64)
+    for t in (0, 1, 4, 5):
+        check_token(out[t], lse[t].astype(np.float64), pool.values(0, np.arange(max(0, begin[t]), end[t])), qv[t], SCALE)
+    # rows 200 .. 599 placed nowhere, and no token's
+    pool.table[0, 200 // R + 1:592 // R] = -3
+    begin, end = np.array([0, 0, 600, 700, 3, 0]), np.array([200, 150, 1000, 800, 3, 0])
+    got, lse = run(pool, [6, 0], q, begin=begin, end=end)
+    check(pool, [6, 0], qv, lambda t, s: np.arange(begin[t], max(begin[t], end[t])), got, lse)
+
+
 @pytest.mark.parametrize("heads", [5, 16])
 def test_few_heads_over_long_rows_and_many_units(heads):
     pool = Pool([6000, 200], 64, 75)
