@@ -441,28 +441,30 @@ _ELEMENT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 def _paged(pages, page_rows, table, cu_tokens, ws):
-    """The device index and the cache's arguments, common to the paged calls:
-    (pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride,
+    """The device index, the workspace's address and the cache's arguments,
+    common to the paged calls: (pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride,
     cu_tokens).  The library launches on the current device, so everything
     has to be there."""
     dev = pages.get_device()
     if dev < 0:
         raise ValueError("pages must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"pages is on device {dev}, the current device is {torch.cuda.current_device()}")
-    if table.get_device() != dev or table.dtype != torch.int32 or table.dim() != 2:
+    shape = table.shape
+    if table.get_device() != dev or table.dtype is not torch.int32 or len(shape) != 2:
         raise ValueError("table must be an int32 [n_seqs, seq_pages] tensor on the pages' device")
-    n_seqs, seq_pages = table.shape
-    if table.stride(1) != 1 and seq_pages > 1:
+    n_seqs, seq_pages = shape
+    stride, inner = table.stride()
+    if inner != 1 and seq_pages > 1:
         raise ValueError("table's rows must be contiguous")
     if not 0 < page_rows <= 256:
         raise ValueError("page_rows must be 16, 32, 64, 128 or 256")
     n_pages, rest = divmod(pages.numel(), page_rows * 368)
     if rest:
         raise ValueError(f"pages must hold whole pages of {page_rows} * 368 bytes")
-    _per(ws, torch.uint8, "ws", None, dev)
-    return dev, (_per(pages, torch.uint8, "pages", None, dev), n_pages, page_rows, table.data_ptr(), n_seqs, seq_pages,
-                 table.stride(0) if n_seqs > 1 else seq_pages, _per(cu_tokens, torch.int32, "cu_tokens", n_seqs + 1, dev))
+    return dev, _per(ws, torch.uint8, "ws", None, dev), (
+        _per(pages, torch.uint8, "pages", None, dev), n_pages, page_rows, table.data_ptr(), n_seqs, seq_pages,
+        stride if n_seqs > 1 else seq_pages, _per(cu_tokens, torch.int32, "cu_tokens", n_seqs + 1, dev))
 
 
 def _per(t, dtype, name, count, dev):
@@ -470,7 +472,7 @@ def _per(t, dtype, name, count, dev):
     dev; its address."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the pages' device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -505,21 +507,21 @@ def ds4x_paged_append(pages, page_rows, table, cu_tokens, row0, kv_in, ws, pos=N
     [n_pages, page_rows * 368], table int32 [n_seqs, seq_pages], cu_tokens
     int32 [n_seqs + 1], row0 int64 [n_seqs], pos int64 [n] or None (the row's
     number), inv_freq f32 [32] or None (no rotation), ws u8 >= 256 bytes."""
-    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     (n, _), stride = _strided(kv_in, "kv_in", 2, (torch.float32, torch.bfloat16), dev)
     _call("ds4x_paged_append", *cache, _per(row0, torch.int64, "row0", cache[4], dev), kv_in.data_ptr(),
           _ELEMENT_TYPES[kv_in.dtype], stride, n, None if pos is None else _per(pos, torch.int64, "pos", n, dev),
           None if inv_freq is None else _per(inv_freq, torch.float32, "inv_freq", 32, dev), int(rope_style),
-          ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+          wp, ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_gather(pages, page_rows, table, cu_tokens, row0, out, ws, stream=None):
     """Read rows back into out f32 or bf16 [n, 512] (rows may be strided):
     token j of sequence s gets the sequence's row row0[s] + j."""
-    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     (n, _), stride = _strided(out, "out", 2, (torch.float32, torch.bfloat16), dev)
     _call("ds4x_paged_gather", *cache, _per(row0, torch.int64, "row0", cache[4], dev), out.data_ptr(),
-          _ELEMENT_TYPES[out.dtype], stride, n, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+          _ELEMENT_TYPES[out.dtype], stride, n, wp, ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_attn_workspace() -> int:
@@ -541,21 +543,21 @@ def ds4x_paged_attn(pages, page_rows, table, cu_tokens, row_end, q, softmax_scal
     [row_begin, row_end) (int64 [n] each; row_begin None: 0) of its sequence;
     out bf16 [n, heads, 512], lse f32 [n, heads] or None, ws u8 of
     ds4x_paged_attn_workspace() bytes.  q and out may be strided by token."""
-    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     n, heads, qs, os, lp = _paged_qo(q, out, lse, dev)
     _call("ds4x_paged_attn", *cache, None if row_begin is None else _per(row_begin, torch.int64, "row_begin", n, dev),
           _per(row_end, torch.int64, "row_end", n, dev), n, heads, q.data_ptr(), qs, float(softmax_scale),
-          out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+          out.data_ptr(), os, lp, wp, ws.numel(), _raw_stream(stream, dev))
 
 
 def ds4x_paged_sparse_attn(pages, page_rows, table, cu_tokens, n_rows, idx, q, softmax_scale, out, lse, ws,
                            stream=None):
     """Attention of each token q bf16 [n, heads, 512] over its own rows idx
     int32 [n, k] of its sequence (n_rows int64 [n_seqs] rows; -1 skipped)."""
-    dev, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
     n, heads, qs, os, lp = _paged_qo(q, out, lse, dev)
     if idx.dim() != 2 or idx.shape[0] != n:
         raise ValueError("idx must be int32 [n_tokens, k]")
     _call("ds4x_paged_sparse_attn", *cache, _per(n_rows, torch.int64, "n_rows", cache[4], dev),
           _per(idx, torch.int32, "idx", idx.numel(), dev), idx.shape[1], n, heads, q.data_ptr(), qs,
-          float(softmax_scale), out.data_ptr(), os, lp, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+          float(softmax_scale), out.data_ptr(), os, lp, wp, ws.numel(), _raw_stream(stream, dev))

@@ -1077,12 +1077,15 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
     named_bar_sync(kBarX, kXThreads);
     const bool whole = w.off == 0 && w.i1 - w.i0 == w.tiles;
     const int part = 2 * int(blockIdx.x) + (w.off == 0 ? 1 : 0);
+    if (A::packed() && xt < kHeads) {  // (all 64: store_output looks at 32 at a time)
+      const Columns col(g, w.unit);
+      sm.out_at[xt] = xt < col.n ? col.at(g, xt, a.out_stride, kDim) : -1;
+    }
     if (xt < g.n_cols) {
       const float tot = (sm.red[0][xt] + sm.red[1][xt]) + (sm.red[2][xt] + sm.red[3][xt]);
       sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) + 0.0f * sm.mh[xt] : 0.0f;  // (m is finite or NaN)
       const float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
       const Columns col(g, w.unit);
-      if (A::packed()) sm.out_at[xt] = xt < col.n ? col.at(g, xt, a.out_stride, kDim) : -1;
       if (xt < col.n) {
         if (!whole)
           parts->lse2[part][xt] = l2;

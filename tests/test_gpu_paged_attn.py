@@ -169,6 +169,22 @@ def test_few_heads_many_tokens(heads, window):
     check(pool, tokens, qv, lambda t, s: np.arange(begin[t], max(end[t], begin[t])), got, lse)
 
 
+@pytest.mark.parametrize("heads", [1, 2, 3, 11, 13, 16, 24])
+def test_units_of_few_columns(heads):
+    """Two, one and two tokens: units whose columns end far below 32, or between 32
+    and 48; every value of the output is the token's own."""
+    rows, tokens = [11, 80, 76], [2, 1, 2]
+    pool = Pool(rows, 128, 79, extra_entries=400)
+    end = np.array([10, 11, 80, 75, 76])
+    for seed in range(4):
+        q, qv = queries(7, heads, 790 + seed)
+        got, lse = run(pool, tokens, q, end=np.append(end, [3, 3]), pad=16)
+        check(pool, tokens, qv, lambda t, s: np.arange(end[t]), got, lse)
+    q, qv = queries(40, heads, 795)
+    got, lse = run(pool, [0, 33, 5], q, end=np.append(np.arange(33) + 40, [70, 71, 72, 73, 74, 9, 9]))
+    check(pool, [0, 33, 5], qv, lambda t, s: np.arange(t + 40 if s == 1 else 70 + t - 33), got, lse)
+
+
 @pytest.mark.parametrize("heads", [8, 20, 64])
 def test_rows_that_only_some_tokens_see(heads):
     """A drafted token's range that reaches into rows never written (NaN where their
