@@ -19,9 +19,10 @@
 // gather: 367 in and 1024 or 2048 out), so loads and stores are 16 bytes a lane but
 // for the codes (4 bytes a lane, 128 consecutive bytes a warp); at the sizes that a
 // step has, the chain cu -> row0 -> table -> page, a round trip to memory each.
-// 16384 tokens in bf16 appended and read back: 25.4 us, 1.8 TB/s; one token: the
-// launches' 17 us (the calls' host side).  Several tokens a warp let one search and
-// one forming of the turns serve them: one token a warp took 33 us.
+// 16384 tokens in bf16 appended and read back: 23.2 us, 2.0 TB/s; one token: 17 us, of
+// which the calls' host side is 15.  Several tokens a warp let one search, one page and
+// one forming of the turns serve them, and the next one's words are on their way while
+// one is worked on.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,23 +59,31 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
   return m;
 }
 
+// Eight values as they lie in memory.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *in, int64_t at, float (&v)[8]) {
-  if (BF16) {
-    const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(in) + at));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Words {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void *in, int64_t at) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(in) + at * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(in) + at);
-    const float4 a = __ldcg(p), b = __ldcg(p + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = __ldcg(p + i);
   }
-}
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (BF16) {
+          v[2 * k] = __uint_as_float(u[k] << 16);
+          v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        } else {
+          v[4 * i + k] = __uint_as_float(u[k]);
+        }
+      }
+    }
+  }
+};
 
 // The tokens of a warp: `per` in a row, so that a sequence found serves the next.
 struct Tokens {
@@ -82,6 +91,30 @@ struct Tokens {
   __device__ __forceinline__ Tokens(int64_t n, int64_t per) {
     t = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * per;
     end = min(n, t + per);
+  }
+};
+
+// Where token after token lies: the sequence and the page found for one serve the
+// next while they hold.
+struct Places {
+  PagedSeq sq{-1, 0, 0};
+  int64_t first_row = 0, r = 0;
+  PagedRow p{nullptr, 0};
+  // false: padding
+  __device__ __forceinline__ bool find(const PagedCache &c, const int64_t *row0, int64_t t, int lane) {
+    const int64_t before = r;
+    const bool known = sq.s >= 0 && t < sq.to;
+    if (!known) {
+      sq = paged_seq_of(c, t, lane);
+      if (sq.s < 0) return false;
+      first_row = __ldcg(row0 + sq.s);
+    }
+    r = first_row + (t - sq.from);
+    if (known && p.page != nullptr && r >> c.page_log2 == before >> c.page_log2)
+      p.at = int32_t(r & ((1 << c.page_log2) - 1));
+    else
+      p = paged_row(c, sq.s, r);
+    return true;
   }
 };
 
@@ -108,30 +141,34 @@ paged_append_kernel(PagedCache c, const int64_t *__restrict__ row0, const void *
     turn[lane] = (fr < 1.0 ? (unsigned long long)(fr * 18446744073709551616.0) : 0ull) +
                  (unsigned long long)((long long)(e0 * 18446744073709551616.0));
   }
-  PagedSeq sq{-1, 0, 0};
-  int64_t first_row = 0;
+  Places at_row;
   bool ready = inv_freq == nullptr;
   // (a named barrier: a warp without a token waits at another place than the rest)
   auto turns_made = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
   if (tk.t >= tk.end && !ready) turns_made();
+  Words<BF16> wa, wb;  // the next token's, on their way while one is worked on
+  int64_t next_pos = 0;
+  auto load = [&](int64_t t) {
+    wa.load(in, t * in_stride + 8 * lane);
+    wb.load(in, t * in_stride + 256 + 8 * lane);
+    next_pos = pos != nullptr ? __ldcg(pos + t) : 0;
+  };
+  if (tk.t < tk.end) load(tk.t);
   for (; tk.t < tk.end; ++tk.t) {
     const int64_t t = tk.t;
+    const bool token = at_row.find(c, row0, t, lane);
+    const PagedRow p = token ? at_row.p : PagedRow{nullptr, 0};
+    const int64_t r = at_row.r, place = next_pos;
     float a[8], b[8];
-    load8<BF16>(in, t * in_stride + 8 * lane, a);
-    load8<BF16>(in, t * in_stride + 256 + 8 * lane, b);
-    const int64_t place = pos != nullptr ? __ldcg(pos + t) : 0;
-    if (sq.s < 0 || t >= sq.to) {
-      sq = paged_seq_of(c, t, lane);
-      if (sq.s >= 0) first_row = __ldcg(row0 + sq.s);
-    }
-    const int64_t r = first_row + (t - sq.from);
-    const PagedRow p = sq.s >= 0 ? paged_row(c, sq.s, r) : PagedRow{nullptr, 0};
+    wa.values(a);
+    wb.values(b);
+    if (t + 1 < tk.end) load(t + 1);
     if (!ready) {
       turns_made();
       ready = true;
     }
     if (p.page == nullptr) {
-      if (sq.s >= 0 && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      if (token && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
       continue;
     }
     if (inv_freq != nullptr) {
@@ -243,32 +280,51 @@ paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__rest
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  PagedSeq sq{-1, 0, 0};
-  int64_t first_row = 0;
-  for (Tokens tk(n, per); tk.t < tk.end; ++tk.t) {
-    const int64_t t = tk.t;
-    if (sq.s < 0 || t >= sq.to) {
-      sq = paged_seq_of(c, t, lane);
-      if (sq.s >= 0) first_row = __ldcg(row0 + sq.s);
+  // a row's words, the next one's on their way while one is worked on
+  struct Row {
+    bool token, placed;
+    uint32_t a, b, sa, sb;
+    uint4 h;
+  };
+  Places at_row;
+  auto load = [&](int64_t t) {
+    Row w;
+    w.token = at_row.find(c, row0, t, lane);
+    const PagedRow p = at_row.p;
+    w.placed = w.token && p.page != nullptr;
+    if (w.placed) {
+      const uint8_t *codes = p.page + paged_code_off(p), *sc = p.page + paged_scale_off(c, p);
+      w.a = __ldcg(reinterpret_cast<const uint32_t *>(codes + 4 * lane));
+      w.sa = __ldcg(sc + (lane >> 2));
+      if (lane < kTailLane) {
+        w.b = __ldcg(reinterpret_cast<const uint32_t *>(codes + 128 + 4 * lane));
+        w.sb = __ldcg(sc + 8 + (lane >> 2));
+      } else {
+        w.h = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p) + 16 * (lane - kTailLane)));
+        w.sb = __ldcg(sc + kPgTailScale);
+      }
     }
-    if (sq.s < 0) continue;
-    const PagedRow p = paged_row(c, sq.s, first_row + (t - sq.from));
+    return w;
+  };
+  Tokens tk(n, per);
+  Row next{};
+  if (tk.t < tk.end) next = load(tk.t);
+  for (; tk.t < tk.end; ++tk.t) {
+    const int64_t t = tk.t;
+    const Row w = next;
+    if (t + 1 < tk.end) next = load(t + 1);
+    if (!w.token) continue;
     float a[8], b[8];
-    if (p.page == nullptr) {
+    if (!w.placed) {
       if (lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
 #pragma unroll
       for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
     } else {
-      const uint8_t *codes = p.page + paged_code_off(p);
-      const uint32_t wa = __ldcg(reinterpret_cast<const uint32_t *>(codes + 4 * lane));
-      const uint8_t *sc = p.page + paged_scale_off(c, p);
-      const float sa = pow2_byte(__ldcg(sc + (lane >> 2)));
+      const float f = pow2_byte(w.sb);
       if (lane < kTailLane) {
-        decode8(__ldcg(reinterpret_cast<const uint32_t *>(codes + 128 + 4 * lane)), pow2_byte(__ldcg(sc + 8 + (lane >> 2))), b);
+        decode8(w.b, f, b);
       } else {
-        const uint4 h = __ldcg(reinterpret_cast<const uint4 *>(p.page + paged_tail_off(c, p) + 16 * (lane - kTailLane)));
-        const uint32_t u[4] = {h.x, h.y, h.z, h.w};
-        const float f = pow2_byte(__ldcg(sc + kPgTailScale));
+        const uint32_t u[4] = {w.h.x, w.h.y, w.h.z, w.h.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
@@ -276,7 +332,7 @@ paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__rest
           b[2 * i + 1] = v.y * f;
         }
       }
-      decode8(wa, sa, a);
+      decode8(w.a, pow2_byte(w.sa), a);
     }
     store8<BF16>(out, t * out_stride + 8 * lane, a);
     store8<BF16>(out, t * out_stride + 256 + 8 * lane, b);
@@ -286,16 +342,16 @@ paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__rest
 }  // namespace
 
 namespace {
-// Tokens a warp, so that the grid is at most 8 blocks an SM, 64 warps (the append's
-// registers let half of them run at once).  16384 tokens appended and read back take
-// 25.4 us so, 28.2 with 4 blocks an SM, 28.5 with half as many of twice the size.
+// Tokens a warp, so that the grid is at most what the GPU holds at once (4 blocks an
+// SM, by the registers).  16384 tokens appended and read back take 23.2 us so, 24.3
+// with 8 blocks an SM, 25.4 with 2, 33 with a token a warp.
 cudaError_t tokens_per_warp(int64_t n, int64_t *per, unsigned *blocks) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t warps = int64_t(sms) * 8 * kWarps;
+  const int64_t warps = int64_t(sms) * 4 * kWarps;
   *per = (n + warps - 1) / warps;
   *blocks = unsigned((n + *per * kWarps - 1) / (*per * kWarps));
   return cudaSuccess;
