@@ -61,7 +61,7 @@
 // 2.43 ms (0.79 PFLOP/s).  Two tiles' loads in flight and a third product queue
 // took it there from 307 us.  Short histories: latency, 10 us for the kernel (its
 // launch, the cuts, one round trip to the rows, three tiles' chain) and 1.4 to 3.5
-// us for the join: 777 rows 13.4 us, 8192 rows 18.0 us.
+// us for the join: 777 rows 13.4 us, 8192 rows 18.4 us.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
