@@ -1009,7 +1009,9 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
           for (int k = 0; k < 8; ++k) {
             const int h = hb + 8 * (k >> 1) + (k & 1);
             float up = fmaxf(fmaxf(sm.red[0][h], sm.red[1][h]), fmaxf(sm.red[2][h], sm.red[3][h]));
-            const bool none = up == -INFINITY;
+            // (columns past the unit's hold what an earlier kernel left in tensor memory: where
+            // that is NaN in every row, it must not end the others' wait for a first row)
+            const bool none = !(up > -INFINITY);
             if (none || !((was_fresh >> k & 1) || up > kLazy)) up = 0.0f;
             if (!none) fresh &= A::packed() ? ~(1u << k) : 0u;
             m[k] += up;
