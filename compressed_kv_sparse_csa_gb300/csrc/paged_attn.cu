@@ -27,12 +27,15 @@
 //
 // Softmax in the log2 domain, online, with the row's exponent kept apart:
 // x_j = l_j log2 e + E_j, w_j = 2^(x_j - m) is what multiplies V'_j, and the
-// denominator is sum_j w_j 2^-E_j.  m is a column's running maximum of x, lazily: it
-// moves (and O^T and the sums are rescaled) only when a tile's x exceeds it by
-// more than 8, so w stays below 2^8.  w enters the second product as fp16 (half
-// a step is 2^-12 to 2^-11 of it, an eighth of the bf16 output's own step; hi +
-// lo parts would double that product); sums are fp32.  E_j is within +-96, so
-// the denominator stays inside fp32 for 2^22 rows.
+// denominator is sum_j w_j 2^-(E_j + 7).  m is 7 below a column's running maximum of x,
+// lazily: it moves (and O^T and the sums are rescaled) only when a tile's x exceeds it
+// by more than 15, so the largest w lies between 2^7 and 2^15.  w enters the second
+// product as fp16: half a step is 2^-12 to 2^-11 of it, an eighth of the bf16 output's
+// own step (hi + lo parts would double that product), while it is above 2^-21 of the
+// largest, and at most 2^-32 of the largest below that, so that 2^20 small weights
+// together lose at most 2^-12 of it.  (With the largest at 1 they lost 2^-5: a sink
+// row above a flat history.)  Sums are fp32.  E_j is within +-96, so the denominator,
+// which leaves the 2^7 out, stays inside fp32 for 2^22 rows.
 //
 // Work split.  All units' tiles, in order, are cut into one run a CTA (one CTA
 // an SM), so any mix of lengths fills the GPU; a cut that falls near a unit's
@@ -94,7 +97,8 @@ constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i
 constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
 constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 8.0f;
+constexpr int kTop = 7;                       // log2 of the largest weight, when a maximum has moved
+constexpr float kLazy = 8.0f + kTop;          // ... and at most
 constexpr int kTame = 20;
 enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 
@@ -109,7 +113,7 @@ struct __align__(1024) Smem {
   uint8_t q[kHeads * kDim * 2];     // Q': 8 panels of 64 dims, 8 KB each
   uint8_t v[2][kTile * kDim * 2];   // V': 8 panels of 8 KB, two tiles
   uint8_t p[2][kTile * kHeads * 2]; // P^T: one panel, two tiles
-  float4 rowe[2][kTile];            // 2^E_j, E_j, 2^-E_j, E_j; a row that is not there: 0, -inf, 0, 0
+  float4 rowe[2][kTile];            // 2^E_j, E_j, 2^-(E_j + 7), E_j + 7; a row that is not there: 0, -inf, 0, 0
   Found found[kAhead][kTile];
   float red[4][kHeads];
   float alpha[kHeads];
@@ -756,7 +760,7 @@ __device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHea
       const int E = int((scw >> 16) & 0xffu) - 127;
       const bool none = scw >> 24;
       sm.rowe[buf][r + 4 * l] = none ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                     : make_float4(pow2f(E), float(E), pow2f(-E), float(E));
+                                     : make_float4(pow2f(E), float(E), pow2f(-E - kTop), float(E + kTop));
       if (!none && (E > kTame || E < -kTame)) sm.wide = 1;
     }
     __syncwarp();
@@ -930,7 +934,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
   Walk w;
   w.begin(sm, total);
   for (int seg = 0;; ++seg) {
-    float m[8], sum[8];  // head hb + 8 j + c: 2 j + c
+    float m[8], sum[8];  // head hb + 8 j + c: 2 j + c (m: kTop below the maximum)
 #pragma unroll
     for (int k = 0; k < 8; ++k) m[k] = 0.0f, sum[k] = 0.0f;
     // bit k: no row so far for that head (for all heads or none, unless packed); m is 0
@@ -949,7 +953,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       wait_bar(sm, &sm.sfull[b], (i >> 1) & 1, hdr);
       tc_fence_after();
       float d[16];  // x - m of row r0 + 8 r: d[4 j + 2 r + c]
-      float inv[2] = {0.0f, 0.0f}, er[2] = {0.0f, 0.0f};  // the rows' 2^-E_j, E_j
+      float inv[2] = {0.0f, 0.0f}, er[2] = {0.0f, 0.0f};  // the rows' 2^-(E_j + 7), E_j + 7
       float over = -INFINITY;
       const bool wide = *reinterpret_cast<volatile int *>(&sm.wide) != 0;
       if (busy) {
@@ -1012,7 +1016,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
             // (columns past the unit's hold what an earlier kernel left in tensor memory: where
             // that is NaN in every row, it must not end the others' wait for a first row)
             const bool none = !(up > -INFINITY);
-            if (none || !((was_fresh >> k & 1) || up > kLazy)) up = 0.0f;
+            up = none || !((was_fresh >> k & 1) || up > kLazy) ? 0.0f : up - kTop;
             if (!none) fresh &= A::packed() ? ~(1u << k) : 0u;
             m[k] += up;
             d[4 * (k >> 1) + (k & 1)] -= up;
@@ -1046,8 +1050,8 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       }
       if (busy) {
         // Rows of very different size: a weight 2^(l_j + E_j - m) may underflow although
-        // its part of the denominator, 2^-E_j as large, does not; then that is formed by
-        // itself.  (While all |E_j| <= kTame a lost part is below 2^-86 of the whole.)
+        // its part of the denominator, 2^-(E_j + 7) as large, does not; then that is formed
+        // by itself.  (While all |E_j| <= kTame a lost part is below 2^-86 of the whole.)
         if (wide) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) sum[2 * (k >> 2) + (k & 1)] += ex2(d[k] - er[(k >> 1) & 1]);
@@ -1086,7 +1090,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       for (int k = 0; k < 8; ++k) {
         const int h = hb + 8 * (k >> 1) + (k & 1);
         sm.red[qd][h] = sum[k];
-        if (qd == 0) sm.mh[h] = m[k] + sm.qodd[h];
+        if (qd == 0) sm.mh[h] = m[k] + kTop + sm.qodd[h];
       }
     }
     // the next unit's Q' (this one's last first product is done: its softmax is)
@@ -1104,7 +1108,8 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
     }
     if (xt < g.n_cols) {
       const float tot = (sm.red[0][xt] + sm.red[1][xt]) + (sm.red[2][xt] + sm.red[3][xt]);
-      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) + 0.0f * sm.mh[xt] : 0.0f;  // (m is finite or NaN)
+      // (m is finite or NaN)
+      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) * pow2f(-kTop) + 0.0f * sm.mh[xt] : 0.0f;
       const float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
       const Columns col(g, w.unit);
       if (xt < col.n) {

@@ -43,6 +43,59 @@ def attend(pages, page_rows, table, cu, end, q, ws, begin=None, scale=SCALE, sta
     return out, lse
 
 
+@pytest.mark.parametrize("heads", [64, 16])
+@pytest.mark.parametrize("n", [1 << 15])
+def test_a_row_above_many_small_ones(n, heads):
+    """One row far above flat ones, each token's rows all one worker's: the many small
+    weights together are a part of the output that must not be lost.
+
+    Bound, beside paged_path's: a small weight enters the second product in fp16
+    whose largest weight is at least 2^7: it is off by 2^-11 of itself where fp16 is
+    normal; below that half a step is 2^-25, so 2^-25 / 2^7 = 2^-32 of the largest (or
+    all of itself, where that is less: it becomes zero).  The products' fp32 sum goes
+    over a run of 2^15 rows, 16 at a time, each of the 17 terms of a step cut off at
+    2^-24 of the largest: 2^11 * 17 * 2^-24 < 2^-8 of the sum of sizes."""
+    B = require_gpu()
+    R, T = 64, torch.cuda.get_device_properties(0).multi_processor_count * (64 // heads)
+    rng = np.random.default_rng(14)
+    x = rng.choice([0.5, 1.0, 1.5, 2.0, 3.0, -0.5], (16 * R, 512)).astype(np.float32)
+    x[:, :32] = 0
+    x[:, 448] = 5.0                # every row's largest exponent: 0
+    x[0] = 0
+    x[0, 0], x[0, 448], x[0, 100], x[0, 480] = 6.0, 5.0, 2.0, 1.0
+    pages, _ = appended(torch.from_numpy(x).cuda()[None], R)
+    table = (torch.arange(n // R, dtype=torch.int32, device="cuda") % 15 + 1)[None].contiguous()
+    table[0, 0] = 0
+    # logits: c for the one row, 0 for the others, in nats
+    qv = np.zeros((heads, 512))
+    qv[:, 0] = np.linspace(16.0, 18.5, heads) / (6 * SCALE)
+    bits, qv = bf16(qv)
+    q = bf16_dev(np.tile(bits, (T, 1, 1)))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    end = torch.full((T,), n, dtype=torch.int64, device="cuda")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    out, lse = attend(pages, R, table, cu, end, q, ws)
+    # the rows that there are, each as often as it stands
+    tb = table[0].cpu().numpy()
+    count = np.zeros(16 * R)
+    for p in range(16):
+        count[p * R:(p + 1) * R] = (tb == p).sum()
+    v, count = x[count > 0].astype(np.float64), count[count > 0]
+    w = np.exp(qv @ v.T * SCALE - (qv @ v[0] * SCALE)[:, None]) * count  # the one row's: 1
+    z = w.sum(axis=1)
+    p = w / z[:, None]
+    ref, ref_lse = p @ v, (qv @ v[0]) * SCALE + np.log(z)
+    size = p @ np.abs(v)
+    few = (np.minimum(2.0 ** -32 * count / z[:, None], p) + 2.0 ** -11 * p) @ np.abs(v)
+    dl = 32 * 2.0 ** -23 * np.abs(qv[:, :1]) * 6 * SCALE + 2.0 ** -21 * 20
+    tol = 2.0 ** -8 * np.abs(ref) + few + (2.0 ** -8 + 2 * dl) * size
+    for t in (0, T // 2, T - 1):
+        o, l = out[t].double().cpu().numpy(), lse[t].double().cpu().numpy()
+        err = np.abs(o - ref)
+        assert np.all(err <= tol), (t, (err / np.maximum(size, 1e-30)).max(), (tol / np.maximum(size, 1e-30)).min())
+        assert np.all(np.abs(l - ref_lse) <= dl[:, 0] + 2.0 ** -18 * 20)
+
+
 def test_what_an_earlier_call_left_does_not_show():
     """A call of 64 heads over bytes that were never rows (NaN in every product), then
     calls of few heads whose lists begin with tiles without a row and whose logits are
