@@ -32,10 +32,16 @@
 // by more than 15, so the largest w lies between 2^7 and 2^15.  w enters the second
 // product as fp16: half a step is 2^-12 to 2^-11 of it, an eighth of the bf16 output's
 // own step (hi + lo parts would double that product), while it is above 2^-21 of the
-// largest, and at most 2^-32 of the largest below that, so that 2^20 small weights
-// together lose at most 2^-12 of it.  (With the largest at 1 they lost 2^-5: a sink
-// row above a flat history.)  Sums are fp32.  E_j is within +-96, so the denominator,
-// which leaves the 2^7 out, stays inside fp32 for 2^22 rows.
+// largest, and at most 2^-32 of the largest below that.  (With the largest at 1 a sink
+// row took a flat history's part of the output with it.)
+//
+// Sums are fp32, over runs of at most 512 tiles of a unit: both the denominator's and
+// the tensor core's drop a term that is 2^-24 of the sum so far.  Over 2^20 rows at once
+// that was 2.5 % of the output and 2^-9 of the denominator; over 2^15 it is below 2^-10
+// and 2^-14.  A longer share of a unit is joined run by run in the CTA's own part of the
+// workspace, by its log-sum-exp (152 units of 2^20 rows: 25.2 ms, 24.7 by 1024 tiles at
+// twice the error, 24.2 in one sum).  E_j is within +-96, so a run's denominator stays
+// inside fp32 (the 2^7 is left out of it).
 //
 // Work split.  All units' tiles, in order, are cut into one run a CTA (one CTA
 // an SM), so any mix of lengths fills the GPU; a cut that falls near a unit's
@@ -100,6 +106,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTop = 7;                       // log2 of the largest weight, when a maximum has moved
 constexpr float kLazy = 8.0f + kTop;          // ... and at most
 constexpr int kTame = 20;
+constexpr int kRunTiles = 512;     // tiles that one sum goes over, at most
 enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 
 // Where a row lies: its codes (null: no row), and from there to its RoPE part and
@@ -120,6 +127,7 @@ struct __align__(1024) Smem {
   float mh[kHeads], hinv[kHeads];
   float qscale[kHeads];             // the unit's columns' scale log2 e 2^-c
   float qodd[kHeads];               // NaN for a column with NaN or infinity, else 0
+  float run2[kHeads], keep[kHeads]; // a share of several runs: log2 of the denominator so far; its part of the joined output
   unsigned long long vfull[2], sfull[2], pfull[2], pvdone[2][2], lfull[kAhead], lfree[kAhead], qfull, qtaken, drain;
   long long scan[kThreads / 32];
   long long cut0, cut1, all;        // the CTA's run of tiles, and all tiles
@@ -131,7 +139,7 @@ struct __align__(1024) Smem {
   int wide;                         // a row so far has an exponent beyond +-kTame
   int2 seen[kPackTokens];           // packed: the rows that each token sees, from the unit's first
   long long out_at[kHeads];         // packed: a column's output (-1: no column)
-  int end_unit, end_part;           // the CTA's last unit, and its part (-1: the whole unit)
+  int end_unit, end_part;           // the CTA's last unit (-1: W has no part in its output), and its part (-1: the whole unit)
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
@@ -335,28 +343,40 @@ __device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
 // A token without a row still has a tile (of rows that are not there): it writes the zeros.
 __device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
 
-// Walks the CTA's run of tiles (numbered from 0 locally), a unit's share at a time.
+// Walks the CTA's tiles (numbered from 0 locally), a run of a unit's share at a time.
 struct Walk {
-  int unit, off;   // the share's unit, and its first tile within it
-  int i0, i1;      // the share's tiles, locally
+  int unit, from;  // the share's unit, and its first tile within it
+  int off;         // the run's first tile within the unit
+  int i0, i1;      // the run's tiles, locally
   int tiles;       // the unit's tiles
   int r0, n;       // the token's rows
+  __device__ __forceinline__ void end_run(int total) {
+    i1 = int(min(int64_t(total), int64_t(i0) + min(tiles - off, kRunTiles)));
+  }
   __device__ __forceinline__ void set(int row0, int rows, int total) {
     r0 = row0;
     n = rows;
     tiles = rows_tiles(n);
-    i1 = int(min(int64_t(total), int64_t(i0) + tiles - off));
+    end_run(total);
   }
   __device__ __forceinline__ void begin(const Smem &sm, int total) {
     unit = sm.unit0;
-    off = sm.off0;
+    from = off = sm.off0;
     i0 = 0;
     set(sm.row0, sm.rows, total);
   }
+  // another run of this unit follows
+  __device__ __forceinline__ bool more(int total) const { return i1 < total && off + (i1 - i0) < tiles; }
   template <class A>
   __device__ __forceinline__ void next(const A &g, int total) {
+    if (more(total)) {
+      off += i1 - i0;
+      i0 = i1;
+      end_run(total);
+      return;
+    }
     ++unit;
-    off = 0;
+    from = off = 0;
     i0 = i1;
     const Rows r = unit_rows(g, unit);
     set(int(r.r0), r.n, total);
@@ -538,7 +558,7 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
   w.begin(sm, total);
   for (;;) {
     const int t = g.packed() ? __ldcg(&g.plan->unit[w.unit].t0) : w.unit / g.groups;
-    if (lane == 0 && w.i0 > 0) prefetch_queries(g, w.unit);
+    if (lane == 0 && w.i0 > 0 && w.off == w.from) prefetch_queries(g, w.unit);
     bool fresh = true;
     // a list's entries are on their way a tile ahead
     int entry[2] = {0, 0};
@@ -726,6 +746,42 @@ __device__ __forceinline__ void store_output(const A &g, Smem &sm, uint32_t tmem
   }
 }
 
+// A run's output joined to what the part holds of the runs before it (`again`); after
+// a whole unit's last one (`done`) the output from there.  X's warps.
+template <class A>
+__device__ __noinline__ void store_run(const A &g, Smem &sm, uint32_t tmem, Parts *parts, int unit, int part, int xw,
+                                       bool again, bool done) {
+  const int lane = threadIdx.x & 31, qd = xw & 3, half = xw >> 2;
+  const Columns col(g, unit);
+  if (32 * half < g.n_cols) {
+#pragma unroll 1
+    for (int k = 0; k < 2 * kDim / 128; ++k) {
+      const int hc = 32 * half + 16 * (k & 1);
+      uint32_t o[16];
+      tc_ld_x16(tmem + (uint32_t(32 * qd) << 16) + kOCol + 64u * (k >> 1) + uint32_t(hc), o);
+      tc_wait_ld();
+      float *po = &parts->o[part][hc][128 * (k >> 1) + 32 * qd + lane];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        if (hc + u < col.n) {
+          float v = __uint_as_float(o[u]) * sm.hinv[hc + u];
+          if (again) v = fmaf(po[u * kDim], sm.keep[hc + u], v);
+          po[u * kDim] = v;
+        }
+    }
+  }
+  if (!done) return;
+  named_bar_sync(kBarX, kXThreads);
+  for (int c = xw; c < col.n; c += kXWarps)
+    for (int d0 = 4 * lane; d0 < kDim; d0 += 128) {
+      const float4 o = __ldcg(reinterpret_cast<const float4 *>(&parts->o[part][c][d0]));
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+      const int d = 8 * v_chunk_back(d0 >> 3) + (d0 & 4);
+      *reinterpret_cast<uint2 *>(g.a.out + col.at(g, c, g.a.out_stride, kDim) + d) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+}
+
 template <class A>
 __device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   const int total = sm.total;
@@ -779,7 +835,7 @@ __device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHea
   const int half = warp >> 2, end = total - 1;
   wait_bar(sm, &sm.pvdone[end & 1][1], (end >> 1) & 1, hdr);
   tc_fence_after();
-  if (32 * half < g.n_cols)
+  if (sm.end_unit >= 0 && 32 * half < g.n_cols)
     store_output(g, sm, sm.tmem_base, parts, sm.end_unit, sm.end_part, warp & 3, half, kDim / 256, kDim / 128);
   tc_fence_before();
 }
@@ -1094,14 +1150,19 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       }
     }
     // the next unit's Q' (this one's last first product is done: its softmax is)
-    const bool last = w.i1 >= total;
+    const bool last = w.i1 >= total, more = w.more(total);
     if (!last) {
       wait_bar(sm, &sm.qtaken, seg & 1, hdr);  // (an S thread without a tile in this unit may not have seen its Q' yet)
-      make_query(g, sm, w.unit + 1, xw, lane);
+      if (!more) {
+        make_query(g, sm, w.unit + 1, xw, lane);
+      } else if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.qfull));  // the same
+      }
     }
     named_bar_sync(kBarX, kXThreads);
-    const bool whole = w.off == 0 && w.i1 - w.i0 == w.tiles;
-    const int part = 2 * int(blockIdx.x) + (w.off == 0 ? 1 : 0);
+    const bool whole = w.from == 0 && w.off + (w.i1 - w.i0) == w.tiles;
+    const bool again = w.off != w.from, runs = more || again;  // not the share's first run; not its only one
+    const int part = 2 * int(blockIdx.x) + (w.from == 0 ? 1 : 0);
     if (A::packed() && xt < kHeads) {  // (all 64: store_output looks at 32 at a time)
       const Columns col(g, w.unit);
       sm.out_at[xt] = xt < col.n ? col.at(g, xt, a.out_stride, kDim) : -1;
@@ -1109,31 +1170,45 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
     if (xt < g.n_cols) {
       const float tot = (sm.red[0][xt] + sm.red[1][xt]) + (sm.red[2][xt] + sm.red[3][xt]);
       // (m is finite or NaN)
-      sm.hinv[xt] = tot > 0.0f ? __frcp_rn(tot) * pow2f(-kTop) + 0.0f * sm.mh[xt] : 0.0f;
-      const float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
+      float inv = tot > 0.0f ? __frcp_rn(tot) * pow2f(-kTop) + 0.0f * sm.mh[xt] : 0.0f;
+      float l2 = tot > 0.0f ? sm.mh[xt] + log2f(tot) : -INFINITY;
+      if (runs) {
+        const float l0 = again ? sm.run2[xt] : -INFINITY, mx = fmaxf(l0, l2);
+        const float a = l0 == -INFINITY ? 0.0f : exp2f(l0 - mx), b = l2 == -INFINITY ? 0.0f : exp2f(l2 - mx), z = a + b;
+        if (z != 0.0f) {  // (NaN stays)
+          inv *= b / z;
+          l2 = mx + log2f(z);
+        }
+        sm.keep[xt] = z != 0.0f ? a / z : 0.0f;
+        sm.run2[xt] = l2;
+      }
+      sm.hinv[xt] = inv;
       const Columns col(g, w.unit);
-      if (xt < col.n) {
+      if (xt < col.n && !more) {
         if (!whole)
           parts->lse2[part][xt] = l2;
         else if (a.lse != nullptr)
           a.lse[col.at(g, xt, a.n_heads, 1)] = l2 * 0.6931471805599453f;
       }
     }
-    if (xt == 0 && !whole) parts->unit[part] = w.unit;
-    if (xt == 0 && g.few && w.off == 0) {
-      parts->span[w.unit] = make_int2(int(blockIdx.x), whole ? 1 : unit_parts(g, sm.cut0 + w.i0 + w.tiles, sm.all));
+    if (xt == 0 && !whole && !more) parts->unit[part] = w.unit;
+    if (xt == 0 && g.few && w.from == 0 && !more) {
+      parts->span[w.unit] = make_int2(int(blockIdx.x), whole ? 1 : unit_parts(g, sm.cut0 + w.i0 - w.off + w.tiles, sm.all));
     }
     named_bar_sync(kBarX, kXThreads);
     wait_bar(sm, &sm.pvdone[(w.i1 - 1) & 1][1], ((w.i1 - 1) >> 1) & 1, hdr);
     tc_fence_after();
     if (last) {
       if (xt == 0) {
-        sm.end_unit = w.unit;
+        sm.end_unit = runs ? -1 : w.unit;
         sm.end_part = whole ? -1 : part;
       }
       named_bar_sync(kBarEnd, kXThreads + 32 * kWWarps);  // W, done with its tiles, takes half of the output
     }
-    if (busy) store_output(g, sm, tmem, parts, w.unit, whole ? -1 : part, qd, half, 0, last ? kDim / 256 : kDim / 128);
+    if (runs)
+      store_run(g, sm, tmem, parts, w.unit, part, xw, again, whole);
+    else if (busy)
+      store_output(g, sm, tmem, parts, w.unit, whole ? -1 : part, qd, half, 0, last ? kDim / 256 : kDim / 128);
     tc_fence_before();
     if (w.i1 >= total) break;
     w.next(g, total);

@@ -44,7 +44,7 @@ def attend(pages, page_rows, table, cu, end, q, ws, begin=None, scale=SCALE, sta
 
 
 @pytest.mark.parametrize("heads", [64, 16])
-@pytest.mark.parametrize("n", [1 << 15])
+@pytest.mark.parametrize("n", [1 << 15, 1 << 20])
 def test_a_row_above_many_small_ones(n, heads):
     """One row far above flat ones, each token's rows all one worker's: the many small
     weights together are a part of the output that must not be lost.
@@ -94,6 +94,59 @@ def test_a_row_above_many_small_ones(n, heads):
         err = np.abs(o - ref)
         assert np.all(err <= tol), (t, (err / np.maximum(size, 1e-30)).max(), (tol / np.maximum(size, 1e-30)).min())
         assert np.all(np.abs(l - ref_lse) <= dl[:, 0] + 2.0 ** -18 * 20)
+
+
+@pytest.mark.parametrize("heads, per", [(64, 1), (100, 1), (16, 3), (5, 8)])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_units_of_several_runs(heads, per, uneven):
+    """Units longer than one sum goes over (512 tiles of 64 rows): ends at, before and
+    behind a run's, shares of one, two and three runs, whole and cut units, several
+    tokens a unit, empty tokens among them; the same bits again.
+
+    Bound: paged_path's, with the products' sum of a run (2^-8, above)."""
+    B = require_gpu()
+    R, run_rows = 64, 512 * 64
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device="cuda")
+    g.manual_seed(30)
+    pages, _ = appended(torch.randn((1, 16 * R, 512), generator=g, device="cuda") + 0.25, R)
+    S = 12 if uneven else sms * 2
+    room = 1 << (20 if uneven else 17)
+    table = (torch.arange(room // R, dtype=torch.int32, device="cuda") * 7 % 16).expand(S, -1).contiguous()
+    rng = np.random.default_rng(31)
+    some = np.array([run_rows - 1, run_rows, run_rows + 1, 2 * run_rows, 2 * run_rows + 64, 3 * run_rows + 17, 0, 5, room])
+    end = np.sort(rng.choice(some[some <= room], (S, per)), axis=1) if not uneven else room - np.sort(rng.integers(0, 200000, (S, per)))[:, ::-1]
+    begin = np.where(rng.random((S, per)) < 0.3, rng.integers(0, 3000, (S, per)), 0)
+    end, begin = end.reshape(-1), begin.reshape(-1)
+    bits, qv = queries(S * per, heads, 32, 2.0)
+    q = bf16_dev(bits)
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * per
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    de, db = dev(end.astype(np.int64)), dev(begin.astype(np.int64))
+    out, lse = attend(pages, R, table, cu, de, q, ws, begin=db)
+    o2, l2 = attend(pages, R, table, cu, de, q, ws, begin=db)
+    assert same_bits(out, o2) and same_bits(lse, l2)
+    pool = Pool([16 * R], R, 33, x=[np.zeros((16 * R, 512), np.float32)])
+    pool.pages, pool.table = pages.cpu().numpy(), np.arange(16)[None]
+    v = pool.values(0, np.arange(16 * R))
+    page = table[0].cpu().numpy()
+    for t in sorted({0, 1, S * per - 1, *rng.choice(S * per, 20).tolist()}):
+        rows = np.arange(begin[t], max(begin[t], end[t]))
+        count = np.bincount(page[rows // R] * R + rows % R, minlength=16 * R)
+        o, l = out[t].double().cpu().numpy(), lse[t].double().cpu().numpy()
+        if len(rows) == 0:
+            assert np.all(o == 0) and np.all(np.isneginf(l))
+            continue
+        logit = np.where(count > 0, qv[t] @ v.T * SCALE, -np.inf)
+        top = logit.max(axis=1, keepdims=True)
+        w = np.exp(logit - top) * count
+        z = w.sum(axis=1, keepdims=True)
+        p, ref_lse = w / z, (top + np.log(z))[:, 0]
+        size = p @ np.abs(v)
+        dl = (32 * 2.0 ** -23 * SCALE * (np.abs(qv[t]) @ np.abs(v).T)).max(axis=1) + 2.0 ** -21 * np.maximum(1, np.abs(top[:, 0]))
+        tol = 2.0 ** -8 * np.abs(p @ v) + (2.0 ** -11 + 2.0 ** -8 + 2 * dl[:, None]) * size + 2.0 ** -20
+        assert np.all(np.abs(o - p @ v) <= tol), (t, begin[t], end[t], np.abs(o - p @ v).max())
+        assert np.all(np.abs(l - ref_lse) <= dl + 2.0 ** -14 + 2.0 ** -22 * np.abs(ref_lse))
 
 
 def test_what_an_earlier_call_left_does_not_show():
