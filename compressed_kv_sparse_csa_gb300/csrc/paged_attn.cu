@@ -136,7 +136,7 @@ struct __align__(1024) Smem {
   int total;                        // its tiles
   uint32_t tmem_base;
   int abort_flag;
-  int wide;                         // a row so far has an exponent beyond +-kTame
+  unsigned long long wide[2];       // bit r: the tile's row r has an exponent beyond +-kTame
   int2 seen[kPackTokens];           // packed: the rows that each token sees, from the unit's first
   long long out_at[kHeads];         // packed: a column's output (-1: no column)
   int end_unit, end_part;           // the CTA's last unit (-1: W has no part in its output), and its part (-1: the whole unit)
@@ -811,13 +811,26 @@ __device__ __forceinline__ void role_w(const A &g, Smem &sm, Parts *parts, WsHea
     if (i >= 2) wait_bar(sm, &sm.pvdone[buf][1], ((i >> 1) - 1) & 1, hdr);
     widen_high<A>(row, x, l, off_b, raw[0]);
     widen_high<A>(row + 4 * 128, x ^ 64u, l, off_b, raw[1]);
+    bool wide = false;
     if (l < 2) {
       const uint32_t scw = l ? raw[1].sc.w : raw[0].sc.w;
       const int E = int((scw >> 16) & 0xffu) - 127;
       const bool none = scw >> 24;
-      sm.rowe[buf][r + 4 * l] = none ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                     : make_float4(pow2f(E), float(E), pow2f(-E - kTop), float(E + kTop));
-      if (!none && (E > kTame || E < -kTame)) sm.wide = 1;
+      // (2^-(E + 7) finite for any byte: another token's bytes that are no row meet it as 0 times it)
+      sm.rowe[buf][r + 4 * l] =
+          none ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+               : make_float4(pow2f(E), float(E), pow2f(-min(E, kPgExpMax) - kTop), float(E + kTop));
+      wide = !none && (E > kTame || E < -kTame);
+    }
+    // lane 8 q + l: the warp's row q + 4 l
+    const uint32_t wides = __ballot_sync(0xffffffffu, wide);
+    if (lane == 0) {
+      uint32_t rows = 0;
+      if (wides != 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) rows |= (wides >> (8 * (k & 3) + (k >> 2)) & 1u) << k;
+      }
+      reinterpret_cast<uint8_t *>(&sm.wide[buf])[warp] = uint8_t(rows);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[buf]));
@@ -996,6 +1009,9 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
     // bit k: no row so far for that head (for all heads or none, unless packed); m is 0
     // and not a maximum yet
     uint32_t fresh = busy ? 0xffu : 0u;
+    // bit k: that head has had a row with an exponent beyond +-kTame (for all heads or none, unless
+    // packed).  In the tiles' order and the run's own, so that nothing else shows in the sums' rounding.
+    uint32_t wide = 0;
     int lo = 0, hi = INT32_MAX;          // packed: the rows that all of the unit's tokens see
     if (A::packed()) {
       const int count = __ldcg(&g.plan->unit[w.unit].count);
@@ -1011,12 +1027,25 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       float d[16];  // x - m of row r0 + 8 r: d[4 j + 2 r + c]
       float inv[2] = {0.0f, 0.0f}, er[2] = {0.0f, 0.0f};  // the rows' 2^-(E_j + 7), E_j + 7
       float over = -INFINITY;
-      const bool wide = *reinterpret_cast<volatile int *>(&sm.wide) != 0;
       if (busy) {
         uint32_t s[16];
         tc_ld_16x256_x4(tmem + lane_base + kSCol + 64u * b + 32u * half, s);
         const float4 e0 = sm.rowe[b][r0], e1 = sm.rowe[b][r0 + 8];
         const float ef[2] = {e0.y, e1.y};
+        if (const unsigned long long rows = sm.wide[b]) {
+          if (!A::packed()) {
+            wide = 0xffu;
+          } else {
+            const int first = (w.off + (i - w.i0)) * kTile;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              const int j = ((hb + 8 * (k >> 1) + (k & 1)) * g.per_head) >> 16;
+              if (j >= kPackTokens) break;
+              const int from = max(0, sm.seen[j].x - first), to = min(kTile, sm.seen[j].y - first);
+              if (to > from && (rows >> from & ~0ull >> (kTile - (to - from)))) wide |= 1u << k;
+            }
+          }
+        }
         inv[0] = e0.z, inv[1] = e1.z;
         er[0] = e0.w, er[1] = e1.w;
         float2 qs[4];
@@ -1110,18 +1139,21 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
         // by itself.  (While all |E_j| <= kTame a lost part is below 2^-86 of the whole.)
         if (wide) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) sum[2 * (k >> 2) + (k & 1)] += ex2(d[k] - er[(k >> 1) & 1]);
+          for (int k = 0; k < 16; ++k) {
+            const int h = 2 * (k >> 2) + (k & 1);
+            if (!A::packed() || (wide >> h & 1)) sum[h] += ex2(d[k] - er[(k >> 1) & 1]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) d[k] = ex2(d[k]);
-        if (!wide) {
+        if (wide != 0xffu) {
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             const int row = (k >> 1) & 1, h = 2 * (k >> 2);
             const float2 t = fma2(make_float2(d[k], d[k + 1]), make_float2(inv[row], inv[row]),
                                   make_float2(sum[h], sum[h + 1]));
-            sum[h] = t.x;
-            sum[h + 1] = t.y;
+            if (!A::packed() || !(wide >> h & 1)) sum[h] = t.x;
+            if (!A::packed() || !(wide >> (h + 1) & 1)) sum[h + 1] = t.y;
           }
         }
 #pragma unroll
@@ -1312,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P> g, P
     mbar_init(smem_u32(&sm.qfull), kXWarps);
     mbar_init(smem_u32(&sm.qtaken), 2);
     mbar_init(smem_u32(&sm.drain), 3);
-    sm.abort_flag = sm.wide = 0;
+    sm.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMWarp0) {

@@ -43,6 +43,102 @@ def attend(pages, page_rows, table, cu, end, q, ws, begin=None, scale=SCALE, sta
     return out, lse
 
 
+def sized(shape, seed, low, high):
+    """Rows each at its own power of two, from 2^low to 2^high."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randn(shape, generator=g, device="cuda")
+    return x * torch.exp2(torch.randint(low, high + 1, (*shape[:-1], 1), generator=g, device="cuda").float())
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+def test_rows_of_different_size_give_the_same_bits_each_time(heads):
+    B = require_gpu()
+    S, n = 40, 5000
+    x = sized((S, n, 512), 2, -2, 2)
+    x[:, 700::900] = sized(x[:, 700::900].shape, 3, -40, -25)
+    x[:, 1500::1300] = sized(x[:, 1500::1300].shape, 4, 21, 24)
+    pages, table = appended(x, 64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    T = 3
+    q = (torch.randn((S * T, heads, 512), generator=g, device="cuda") * 2.0**-20).bfloat16()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * T
+    end = n - torch.arange(S * T, device="cuda") % T
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    out, lse = attend(pages, 64, table, cu, end, q, ws)
+    for _ in range(40):
+        o, l = attend(pages, 64, table, cu, end, q, ws)
+        assert same_bits(o, out) and same_bits(l, lse)
+    pool = Pool([n], 64, 6, x=[np.zeros((n, 512), np.float32)])
+    pool.pages, pool.table = pages.cpu().numpy(), table.cpu().numpy()
+    for t in (0, S * T - 1):
+        v = pool.values(t // T, np.arange(int(end[t])))
+        check_token(out[t].double().cpu().numpy(), lse[t].double().cpu().numpy(), v, q[t].double().cpu().numpy(), SCALE)
+
+
+def test_a_session_of_large_rows_does_not_touch_its_neighbours():
+    """Short sessions side by side, several a worker: every other one's rows at sizes
+    far apart, or not, leave the rest bit for bit."""
+    B = require_gpu()
+    S, n = 700, 128
+    x = sized((S, n, 512), 7, -1, 1)
+    y = x.clone()
+    y[1::2] = sized(y[1::2].shape, 8, -40, 40)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    q = torch.randn((S, 64, 512), generator=g, device="cuda").bfloat16()
+    cu, end = torch.arange(S + 1, dtype=torch.int32, device="cuda"), torch.full((S,), n, dtype=torch.int64, device="cuda")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    got = []
+    for z in (x, y):
+        pages, table = appended(z, 32)
+        got.append(attend(pages, 32, table, cu, end, q, ws))
+    assert same_bits(got[0][0][::2], got[1][0][::2]) and same_bits(got[0][1][::2], got[1][1][::2])
+    assert not same_bits(got[0][1][1::2], got[1][1][1::2])
+
+
+@pytest.mark.parametrize("heads", [5, 8, 20])
+def test_a_row_that_one_token_sees_leaves_the_others_bits(heads):
+    """Tokens that share a pass: the rows that only later ones see are ordinary, far
+    larger, far smaller, or bytes never written; the earlier ones' bits stay."""
+    B = require_gpu()
+    S, n, T, R = 150, 200, 8, 16
+    x = sized((S, n, 512), 10, -1, 1)
+    end = (n - T + 1 + torch.arange(S * T, device="cuda") % T)
+    begin = torch.arange(S * T, device="cuda") % 2 * 60  # and rows at the front that every other token sees
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    q = torch.randn((S * T, heads, 512), generator=g, device="cuda").bfloat16()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * T
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+
+    def bits(y, garbage=None):
+        pages, table = appended(y, R)
+        if garbage is not None:
+            for r in range(garbage, n):  # plausible scales, NaN for values
+                page = pages[table[:, r // R].long()]
+                page[:, R * 224 + 128 * (r % R):][:, :128] = 0xFF
+                page[:, R * 352 + 16 * (r % R):][:, :16] = 240 + r % 16
+                pages[table[:, r // R].long()] = page
+        o, l = attend(pages, R, table, cu, end, q, ws, begin=begin)
+        return o.view(S, T, heads, 512), l.view(S, T, heads)
+
+    out, lse = bits(x)
+    for t in (0, 3, 6):  # tokens up to t keep their rows
+        keep = n - T + 1 + t
+        for size in (30, -60, None):
+            y = x.clone()
+            if size is not None:
+                y[:, keep:] = sized(y[:, keep:].shape, 12, size - 1, size + 1)
+            o, l = bits(y, keep if size is None else None)
+            assert same_bits(o[:, :t + 1], out[:, :t + 1]) and same_bits(l[:, :t + 1], lse[:, :t + 1]), (t, size)
+    y = x.clone()
+    y[:, 5:60] = sized(y[:, 5:60].shape, 13, 25, 45)
+    o, l = bits(y)
+    assert same_bits(o[:, 1::2], out[:, 1::2]) and same_bits(l[:, 1::2], lse[:, 1::2])
+
+
 @pytest.mark.parametrize("heads", [64, 16])
 @pytest.mark.parametrize("n", [1 << 15, 1 << 20])
 def test_a_row_above_many_small_ones(n, heads):
