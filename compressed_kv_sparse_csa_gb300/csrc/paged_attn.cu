@@ -1172,13 +1172,18 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
     }
+    // (the mark is read before this barrier: behind it other warps write the next unit's)
+    if (busy && qd == 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m[k] += kTop + sm.qodd[hb + 8 * (k >> 1) + (k & 1)];
+    }
     named_bar_sync(kBarX, kXThreads);  // the last readers of red, mh and hinv are done
     if (busy && lane < 4) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int h = hb + 8 * (k >> 1) + (k & 1);
         sm.red[qd][h] = sum[k];
-        if (qd == 0) sm.mh[h] = m[k] + kTop + sm.qodd[h];
+        if (qd == 0) sm.mh[h] = m[k];
       }
     }
     // the next unit's Q' (this one's last first product is done: its softmax is)

@@ -43,6 +43,32 @@ def attend(pages, page_rows, table, cu, end, q, ws, begin=None, scale=SCALE, sta
     return out, lse
 
 
+def test_odd_queries_of_neighbouring_units():
+    """Eight units a worker, one tile each; NaN and infinite queries in some heads of
+    some tokens.  Each marks its own outputs and no others, time and again."""
+    B = require_gpu()
+    T, n = 8 * torch.cuda.get_device_properties(0).multi_processor_count, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    pages, table = appended(torch.randn((1, n, 512), generator=g, device="cuda"), 64)
+    q = torch.randn((T, 64, 512), generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    end = torch.full((T,), n, dtype=torch.int64, device="cuda")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    out, lse = attend(pages, 64, table, cu, end, q, ws)
+    hit = torch.rand((T, 64), generator=g, device="cuda") < 0.4
+    hit[::2] = False
+    hit[1::4] = True
+    bad = q.clone()
+    at = torch.randint(512, (T, 64, 1), generator=g, device="cuda")
+    odd = torch.where(torch.rand((T, 64, 1), generator=g, device="cuda") < 0.5, float("nan"), float("inf")).bfloat16()
+    bad.scatter_(2, at, torch.where(hit[..., None], odd, q.gather(2, at)))
+    for _ in range(20):
+        o, l = attend(pages, 64, table, cu, end, bad, ws)
+        assert same_bits(o[~hit], out[~hit]) and same_bits(l[~hit], lse[~hit])
+        assert torch.isnan(o[hit]).all() and torch.isnan(l[hit]).all()
+
+
 def sized(shape, seed, low, high):
     """Rows each at its own power of two, from 2^low to 2^high."""
     g = torch.Generator(device="cuda")
