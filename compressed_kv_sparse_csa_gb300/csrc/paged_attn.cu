@@ -334,6 +334,11 @@ __device__ __forceinline__ Rows token_rows(const PagedAttn &a, int t) {
   const int64_t e = min(room, int64_t(__ldcg(a.row_end + t)));
   return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
 }
+// Whether token t sees a row past what the table can place.
+__device__ __forceinline__ bool past_table(const PagedAttn &a, int t) {
+  const int64_t e = __ldcg(a.row_end + t);
+  return e > (int64_t(a.c.seq_pages) << a.c.page_log2) && (a.row_begin == nullptr || __ldcg(a.row_begin + t) < e);
+}
 template <class A>
 __device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
   if (!g.packed()) return token_rows(g.a, unit / g.groups);
@@ -521,8 +526,7 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // a range past what the table can place
   if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.packed())
     for (int t = t0; t < min(t1, valid); ++t)
-      if (__ldcg(a.row_end + t) > (int64_t(a.c.seq_pages) << a.c.page_log2))
-        atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      if (past_table(a, t)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   __syncthreads();
 }
 
@@ -1269,7 +1273,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
   const int valid = max(0, min(a.n_tokens, __ldcg(a.c.cu + n_seqs)));
   __syncthreads();
   auto cu = [&](int s) { return held ? cus[s] : __ldcg(a.c.cu + s); };
-  const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
   int base = 0;
   for (int c0 = 0; c0 < valid; c0 += kPlanThreads) {
     const int t = c0 + tid;
@@ -1290,7 +1293,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         int rest = 0;  // tokens whose rows do not meet those from lo to hi
         int64_t lo = 0, hi = 0;
         for (int j = 0; j < count; ++j) {
-          if (__ldcg(a.row_end + t + j) > room) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+          if (past_table(a, t + j)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
           const Rows r = token_rows(a, t + j);
           if (r.n == 0) continue;
           if (hi == 0) lo = r.r0, hi = r.r0 + r.n;

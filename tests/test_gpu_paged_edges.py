@@ -294,3 +294,18 @@ def test_what_an_earlier_call_left_does_not_show():
         out = C.bf16_decode(got).astype(np.float64)
         for t in (0, 1, 2, 3, 77, 78, T - 1):
             check_token(out[t], lse[t].astype(np.float64), pool.values(0, idx[t, 150:]), qv[t], SCALE)
+
+
+@pytest.mark.parametrize("heads", [64, 8])
+def test_an_empty_range_past_the_table_is_no_fault(heads):
+    """A token that sees nothing is zeros and flags nothing, wherever its range lies."""
+    pool = Pool([3000, 100], 16, 18)
+    tokens = [5, 3]
+    end = np.array([3000, 1 << 40, 1 << 62, 5, 1 << 33, 100, 1 << 40, 99])
+    begin = np.array([0, 1 << 40, (1 << 63) - 1, 7, 1 << 34, 0, 1 << 41, 3])
+    q, qv = queries(8, heads, 19)
+    got, lse = run(pool, tokens, q, begin=begin, end=end)
+    check(pool, tokens, qv, lambda t, s: np.arange(begin[t], max(end[t], begin[t])) if end[t] <= 3000 else np.arange(0), got, lse)
+    # one row past it is one
+    end[1], begin[1] = pool.table.shape[1] * 16 + 1, pool.table.shape[1] * 16
+    run(pool, tokens, q, begin=begin, end=end, status=-7)
