@@ -579,7 +579,9 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
       if (fresh) {  // (looked up while the first entries are on their way)
         if (sq.s < 0 || t >= sq.to) {
           sq = paged_seq_of(a.c, t, lane);
-          n_rows = a.idx != nullptr && sq.s >= 0 ? int(min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + sq.s)))) : INT32_MAX;
+          n_rows = INT32_MAX;
+          if (a.idx != nullptr && sq.s >= 0)  // (below 0: no row)
+            n_rows = int(max(int64_t(0), min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + sq.s)))));
         }
         fresh = false;
       }

@@ -309,3 +309,12 @@ def test_an_empty_range_past_the_table_is_no_fault(heads):
     # one row past it is one
     end[1], begin[1] = pool.table.shape[1] * 16 + 1, pool.table.shape[1] * 16
     run(pool, tokens, q, begin=begin, end=end, status=-7)
+
+
+@pytest.mark.parametrize("rows", [-1, -(1 << 31), -(1 << 32) + 90, -(1 << 63) + 90, -(1 << 63)])
+def test_a_sequence_of_fewer_than_no_rows_has_none(rows):
+    pool = Pool([100, 50], 32, 20)
+    q, qv = queries(2, 64, 21)
+    idx = np.tile(np.arange(50, dtype=np.int32), (2, 1))
+    got, lse = run(pool, [1, 1], q, idx=idx, n_rows=[rows, 50], status=-7)
+    check(pool, [1, 1], qv, lambda t, s: np.arange(50) if s else np.arange(0), got, lse)
