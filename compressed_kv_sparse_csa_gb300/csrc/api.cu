@@ -368,6 +368,16 @@ bool paged_vectors(const void *p, int32_t type, int64_t stride, int64_t dim) {
   return stride >= dim && stride <= (int64_t(1) << 40) && stride % (type == DS4X_BF16 ? 8 : 4) == 0;
 }
 
+// Whether two arrays of n vectors of `vec` bytes, as far apart as given, share a byte.
+// Vectors that interleave at one stride do not; of other strides only arrays apart.
+bool paged_overlap(const void *a, int64_t a_stride, const void *b, int64_t b_stride, int64_t vec, int64_t n) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  if (a0 >= b0 + uintptr_t(b_stride * (n - 1) + vec) || b0 >= a0 + uintptr_t(a_stride * (n - 1) + vec)) return false;
+  if (n == 1 || a_stride != b_stride) return true;
+  const uintptr_t s = uintptr_t(a_stride), d = b0 >= a0 ? (b0 - a0) % s : (s - (a0 - b0) % s) % s;
+  return d < uintptr_t(vec) || s - d < uintptr_t(vec);
+}
+
 int paged_attn(PagedAttn &a, const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
                int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, void *ws,
                size_t ws_bytes, ds4x_stream_t stream) {
@@ -380,10 +390,7 @@ int paged_attn(PagedAttn &a, const uint8_t *pages, int64_t n_pages, int32_t page
     return DS4X_EINVAL;
   if (a.lse != nullptr && !aligned_to(a.lse, 4)) return DS4X_EINVAL;
   // a token's heads may be computed apart, so its output must not lie where its query does
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(a.q), o0 = reinterpret_cast<uintptr_t>(a.out);
-  const uintptr_t q1 = q0 + 2 * uintptr_t(a.q_stride * (a.n_tokens - 1) + vec);
-  const uintptr_t o1 = o0 + 2 * uintptr_t(a.out_stride * (a.n_tokens - 1) + vec);
-  if (q0 < o1 && o0 < q1) return DS4X_EINVAL;
+  if (paged_overlap(a.q, 2 * a.q_stride, a.out, 2 * a.out_stride, 2 * vec, a.n_tokens)) return DS4X_EINVAL;
   if (ws_bytes < paged_attn_ws_bytes()) return DS4X_EWORKSPACE;
   const int arch = check_arch();
   if (arch != DS4X_OK) return arch;

@@ -572,7 +572,7 @@ size_t ds4x_paged_attn_workspace(void);
  *   q_bf16     bf16 [n_tokens][n_heads][512], q_stride elements from token to
  *              token (>= n_heads * 512, a multiple of 8)
  *   out_bf16   bf16 [n_tokens][n_heads][512], out_stride likewise; must not
- *              overlap q_bf16
+ *              overlap q_bf16 (of one stride, the two may interleave)
  *   lse        f32 [n_tokens][n_heads] or NULL
  *   ws         >= ds4x_paged_attn_workspace() bytes, zero-filled before first
  *              use; not for two calls that may overlap on the GPU (two

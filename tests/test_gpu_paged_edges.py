@@ -318,3 +318,21 @@ def test_a_sequence_of_fewer_than_no_rows_has_none(rows):
     idx = np.tile(np.arange(50, dtype=np.int32), (2, 1))
     got, lse = run(pool, [1, 1], q, idx=idx, n_rows=[rows, 50], status=-7)
     check(pool, [1, 1], qv, lambda t, s: np.arange(50) if s else np.arange(0), got, lse)
+
+
+@pytest.mark.parametrize("heads", [64, 12])
+def test_outputs_between_queries(heads):
+    """Queries and outputs of one buffer, token by token in turn: what the call gives apart."""
+    B = require_gpu()
+    pool = Pool([900, 300], 32, 22)
+    tokens = [9, 4]
+    q, qv = queries(13, heads, 23)
+    end = np.concatenate([np.arange(892, 901), np.arange(297, 301)])
+    want, want_lse = run(pool, tokens, q, end=end)
+    both = torch.full((13, 2, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    both[:, 0] = bf16_dev(q)
+    lse = torch.zeros((13, heads), device="cuda")
+    cu, ws = dev(np.array([0, 9, 13], dtype=np.int32)), new_ws(B.ds4x_paged_attn_workspace())
+    B.ds4x_paged_attn(dev(pool.pages), 32, dev(pool.table), cu, dev(end.astype(np.int64)), both[:, 0], SCALE, both[:, 1], lse, ws)
+    assert np.array_equal(bf16_host_bits(both[:, 1].contiguous()), want) and np.array_equal(lse.cpu().numpy(), want_lse)
+    assert np.array_equal(bf16_host_bits(both[:, 0].contiguous()), q)
