@@ -26,6 +26,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "paged.cuh"
 
 namespace ds4x {
@@ -52,11 +54,16 @@ __device__ __forceinline__ int paged_exponent(float amax, float g, int G) {
   if (amax == 0.0f) return kPgExpMin;
   return max(kPgExpMin, min(kPgExpMax, block_exponent(amax, g, G)));
 }
+// The largest |v|; NaN where one is.
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
   return m;
+}
+// NaN to zero, infinities to the largest floats.
+__device__ __forceinline__ float finite(float v) {
+  return v == v ? fminf(fmaxf(v, -FLT_MAX), FLT_MAX) : 0.0f;
 }
 
 // Eight values as they lie in memory.
@@ -200,6 +207,16 @@ paged_append_kernel(PagedCache c, const int64_t *__restrict__ row0, const void *
     }
     // block maxima over four lanes, the RoPE part's over lanes 24-31
     float ma = amax8(a), mb = amax8(b);
+    if (__any_sync(0xffffffffu, !(ma <= FLT_MAX && mb <= FLT_MAX))) {  // rows hold finite values only
+      if (lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = finite(a[i]);
+        b[i] = finite(b[i]);
+      }
+      ma = amax8(a);
+      mb = amax8(b);
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));

@@ -481,6 +481,8 @@ int ds4x_dense_attn_decode(const uint8_t *kv_rows, int64_t n_rows, const uint16_
  * table_stride entries between sequences, of which seq_pages are used: row j
  * of sequence s lies in page table[s][j / R] at j % R, j < seq_pages * R.
  * Entries that no call reaches may hold anything.
+ * Rows hold what ds4x_paged_append wrote; other bytes give the tokens that see
+ * them unspecified (memory-safe) results, and no other token.
  *
  * Tokens are ragged over the sequences: cu_tokens is i32 [n_seqs + 1],
  * non-decreasing, cu_tokens[0] = 0; sequence s has the tokens cu_tokens[s] ..
@@ -530,7 +532,10 @@ enum { DS4X_ROPE_INTERLEAVED = 0, DS4X_ROPE_HALVES = 1 };     /* rotated pairs  
  * 2^e, codes to nearest, ties to even, the sign kept; for the RoPE part the
  * largest of those and the least e in [-96, 96] with amax <= 8 * 2^e, values
  * rounded to FP16 (nearest even, saturating).  The codes and the blocks'
- * scales are bit-exact with that rule.
+ * scales are bit-exact with that rule.  A value that is NaN, once rotated,
+ * counts as zero, an infinite one (or one that the rotation takes past FP32's
+ * largest) as the largest float of its sign, and either flags DS4X_EDEVICE: a
+ * row holds finite values only.
  *
  * A page that two sequences of one call both write is the caller's error:
  * each of its rows holds bytes of either token.
