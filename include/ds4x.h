@@ -487,9 +487,10 @@ int ds4x_dense_attn_decode(const uint8_t *kv_rows, int64_t n_rows, const uint16_
  * Tokens are ragged over the sequences: cu_tokens is i32 [n_seqs + 1],
  * non-decreasing, cu_tokens[0] = 0; sequence s has the tokens cu_tokens[s] ..
  * cu_tokens[s + 1] - 1 of a call, any number of them.  Tokens from
- * cu_tokens[n_seqs] up to n_tokens are padding: nothing of theirs is read or
- * written.  cu_tokens and every array beside it are device memory, so a
- * captured call follows their contents.
+ * cu_tokens[n_seqs] up to n_tokens are padding: every array of n_tokens has
+ * entries for them, which may hold anything (some are read, none counts), and
+ * their outputs are not written.  cu_tokens and every array beside it are
+ * device memory, so a captured call follows their contents.
  *
  * A row that the table places nowhere (a row below 0 or beyond seq_pages * R,
  * a page outside [0, n_pages)) is left out and flags DS4X_EDEVICE in the
