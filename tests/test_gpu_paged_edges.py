@@ -336,3 +336,69 @@ def test_outputs_between_queries(heads):
     B.ds4x_paged_attn(dev(pool.pages), 32, dev(pool.table), cu, dev(end.astype(np.int64)), both[:, 0], SCALE, both[:, 1], lse, ws)
     assert np.array_equal(bf16_host_bits(both[:, 1].contiguous()), want) and np.array_equal(lse.cpu().numpy(), want_lse)
     assert np.array_equal(bf16_host_bits(both[:, 0].contiguous()), q)
+
+
+@pytest.mark.parametrize("heads", [5, 64])
+def test_runs_without_a_row(heads):
+    """A long unit whose first, middle or last runs' pages are nowhere (and flagged), one
+    without any row at all, NaN queries among them."""
+    B = require_gpu()
+    R, run = 64, 512
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    S = 4 * sms
+    g = torch.Generator(device="cuda")
+    g.manual_seed(34)
+    pages, _ = appended(torch.randn((1, 4 * R, 512), generator=g, device="cuda"), R)
+    table = (torch.arange(3 * run, dtype=torch.int32, device="cuda") % 4).expand(S, -1).contiguous()
+    table[0::4, :run], table[1::4, run:2 * run], table[2::4, 2 * run:], table[3::4] = -1, -1, -1, -1
+    q = torch.randn((S, heads, 512), generator=g, device="cuda").bfloat16()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    end = torch.full((S,), 3 * run * R, dtype=torch.int64, device="cuda")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    out, lse = attend(pages, R, table, cu, end, q, ws, status=-7)
+    assert torch.all(out[3::4] == 0) and torch.all(lse[3::4] == -float("inf"))
+    # 4 pages, each 256 times
+    v = Pool([4 * R], R, 35, x=[np.zeros((4 * R, 512), np.float32)])
+    v.pages, v.table = pages.cpu().numpy(), np.arange(4)[None]
+    rows = v.values(0, np.arange(4 * R))
+    for t in (0, 1, 2, S - 4, S - 3, S - 2):
+        check_token(out[t].double().cpu().numpy(), lse[t].double().cpu().numpy() - np.log(256), rows, q[t].double().cpu().numpy(), SCALE)
+    bad = q.clone()
+    bad[:, 1, 77] = float("nan")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    o, l = attend(pages, R, table, cu, end, bad, ws, status=-7)
+    keep = [h for h in range(heads) if h != 1]
+    seen = torch.arange(S, device="cuda") % 4 != 3
+    assert same_bits(o[:, keep], out[:, keep]) and same_bits(l[:, keep], lse[:, keep])
+    assert torch.isnan(o[seen, 1]).all() and torch.isnan(l[seen, 1]).all()
+    assert torch.all(o[~seen] == 0) and torch.all(l[~seen] == -float("inf"))
+
+
+@pytest.mark.parametrize("heads, lists", [(3, False), (65, False), (65, True)])
+def test_as_many_tokens_as_a_call_takes(heads, lists):
+    """65,535 tokens; with 65 heads the queries go past 2^31 elements."""
+    B = require_gpu()
+    T, S, n, R = 65535, 300, 70, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(36)
+    pages, table = appended(torch.randn((S, n, 512), generator=g, device="cuda"), R)
+    cuts = torch.sort(torch.randint(T + 1, (S - 1,), generator=g, device="cuda"))[0].int()
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), cuts, torch.full((1,), T, dtype=torch.int32, device="cuda")])
+    q = torch.randn((T, heads, 512), generator=g, device="cuda", dtype=torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((T, heads), device="cuda")
+    ws = new_ws(B.ds4x_paged_attn_workspace())
+    end = torch.randint(n + 1, (T,), generator=g, device="cuda")
+    idx = torch.randint(-1, n, (T, 40), generator=g, device="cuda", dtype=torch.int32)
+    if lists:
+        B.ds4x_paged_sparse_attn(pages, R, table, cu, torch.full((S,), n, dtype=torch.int64, device="cuda"), idx, q, SCALE, out, lse, ws)
+    else:
+        B.ds4x_paged_attn(pages, R, table, cu, end, q, SCALE, out, lse, ws)
+    assert B.ds4x_workspace_status(ws) == 0
+    pool = Pool([n] * S, R, 37, x=[np.zeros((n, 512), np.float32)] * S)
+    pool.pages, pool.table = pages.cpu().numpy(), table.cpu().numpy()
+    seq = torch.searchsorted(cu[1:], torch.arange(T, device="cuda", dtype=torch.int32), right=True).cpu().numpy()
+    for t in [0, 1, 2, 8191, 32767, 32768, *range(40000, 65535, 1771), T - 2, T - 1]:
+        rows = idx[t].cpu().numpy() if lists else np.arange(int(end[t]))
+        check_token(out[t].double().cpu().numpy(), lse[t].double().cpu().numpy(), pool.values(seq[t], rows[rows >= 0]), q[t].double().cpu().numpy(), SCALE)
+    del q, out
+    torch.cuda.empty_cache()
