@@ -63,14 +63,14 @@
 // because local loads queue behind W's.
 //
 // What bounds it.  Long histories and chunks: the chain of a tile, widen -> S ->
-// softmax -> O, about 3300 cycles a tile with the two V' buffers that shared memory
-// holds (64 KB each beside 64 KB of Q'), of which the products fill 55 % (M = 64
-// rows make S run at half the tensor rate): 64 heads over 1,048,576 rows 190 us
+// softmax -> O, about 3400 cycles a tile with the two V' buffers that shared memory
+// holds (64 KB each beside 64 KB of Q'), of which the products fill 56 % (M = 64
+// rows make S run at half the tensor rate): 64 heads over 1,048,576 rows 191 us
 // (2.0 TB/s of packed rows, 0.72 PFLOP/s), a chunk of 2048 tokens over 8192 rows
-// 2.43 ms (0.79 PFLOP/s).  Two tiles' loads in flight and a third product queue
+// 2.51 ms (0.77 PFLOP/s).  Two tiles' loads in flight and a third product queue
 // took it there from 307 us.  Short histories: latency, 10 us for the kernel (its
 // launch, the cuts, one round trip to the rows, three tiles' chain) and 1.4 to 3.5
-// us for the join: 777 rows 13.4 us, 8192 rows 18.4 us.
+// us for the join: 777 rows 13.4 us, 8192 rows 18.9 us.
 //
 // Every wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which no
 // wait blocks, so every role runs to its end.
@@ -1537,8 +1537,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
 // The same for at most kFewUnits units, where a call's latency counts: a block takes
 // 256 dims of a head, its parts dealt over four pairs of warps; no list to make first
 // (the units' spans are written by the CTAs that begin them).  A call over 777 rows
-// takes 13.4 us so, 15.6 by the list; 16 sessions of 8192 to 65536 rows 97.9 us, and
-// 105.5 where kFewUnits is 4.
+// takes 13.4 us so, 15.6 by the list.  Up to 16 units (kFewUnits), with cold caches: 9 of
+// 4096 to 8192 rows 38.9 us, 51.2 by the list, 16 of 600 to 1200 rows 34.8, 36.8; above,
+// 32 of those 43.0, 41.0, while 32 lists of 512 rows would take 28.7, 32.8.
 constexpr int kFewThreads = 256;
 __global__ void __launch_bounds__(kFewThreads) paged_combine_few_kernel(Args g, const Parts *__restrict__ parts) {
   __shared__ float wts[kMaxCtas], lsum, lmax;

@@ -480,6 +480,9 @@ int ds4x_dense_attn_decode(const uint8_t *kv_rows, int64_t n_rows, const uint16_
  * pages is u8 [n_pages][R * 368], 16-byte aligned.  table is i32 [n_seqs][..],
  * table_stride entries between sequences, of which seq_pages are used: row j
  * of sequence s lies in page table[s][j / R] at j % R, j < seq_pages * R.
+ * seq_pages may be less than a table's width: the attention's launches are laid
+ * out for that many pages, so a table made for the longest context is best
+ * passed with what the call's rows need (table_stride stays the width).
  * Entries that no call reaches may hold anything.
  * Rows hold what ds4x_paged_append wrote; other bytes give the tokens that see
  * them unspecified (memory-safe) results, and no other token.
