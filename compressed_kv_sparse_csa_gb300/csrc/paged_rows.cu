@@ -20,9 +20,9 @@
 // for the codes (4 bytes a lane, 128 consecutive bytes a warp); at the sizes that a
 // step has, the chain cu -> row0 -> table -> page, a round trip to memory each.
 // 16384 tokens in bf16 appended and read back: 23.4 us, 2.0 TB/s (in a graph, rows in L2,
-// 13.1 and 8.6 us); one token: 17 us, of which the calls' host side is 15.  Several tokens a warp let one search, one page and
-// one forming of the turns serve them, and the next one's words are on their way while
-// one is worked on.
+// 13.1 and 8.6 us); one token: 17 us, of which the calls' host side is 15.  Several tokens
+// a warp let one search, one page and one forming of the turns serve them, and the next
+// one's words are on their way while one is worked on.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
