@@ -68,6 +68,13 @@ _SIGNATURES = {
     "ds4x_paged_sparse_attn": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p,
                                               _c_i32, _c_i32, _c_i32, _c_p, _c_i64, _c_f32, _c_p, _c_i64, _c_p, _c_p,
                                               _c_size, _c_p]),
+    "ds4x_paged_tree_attn": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                            _c_i32, _c_i32, _c_p, _c_i64, _c_f32, _c_p, _c_i64, _c_p, _c_p, _c_size,
+                                            _c_p]),
+    "ds4x_verify_drafts": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i32,
+                                          _c_p, _c_p, _c_p, _c_p, _c_p, _c_size, _c_p]),
+    "ds4x_paged_keep": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                       _c_i64, _c_p, _c_size, _c_p]),
     "ds4x_index_score_topk_prefill": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_i32, _c_i64, _c_i32, _c_p, _c_p,
                                                       _c_p, _c_size, _c_p]),
 }
@@ -561,3 +568,60 @@ def ds4x_paged_sparse_attn(pages, page_rows, table, cu_tokens, n_rows, idx, q, s
     _call("ds4x_paged_sparse_attn", *cache, _per(n_rows, torch.int64, "n_rows", cache[4], dev),
           _per(idx, torch.int32, "idx", idx.numel(), dev), idx.shape[1], n, heads, q.data_ptr(), qs,
           float(softmax_scale), out.data_ptr(), os, lp, wp, ws.numel(), _raw_stream(stream, dev))
+
+
+# ---- drafted tokens ----
+
+def ds4x_paged_tree_attn(pages, page_rows, table, cu_tokens, row0, parent, q, softmax_scale, out, lse, ws,
+                         row_begin=None, stream=None):
+    """Attention of each node q bf16 [n, heads, 512] of its sequence's draft
+    over the rows before it and its own line of ancestors: parent int32 [n]
+    (numbers within the sequence, -1 for a root), row0 int64 [n_seqs] (node j is
+    row row0 + j), row_begin int64 [n] or None (a window's first position); out,
+    lse and ws as ds4x_paged_attn."""
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    n, heads, qs, os, lp = _paged_qo(q, out, lse, dev)
+    _call("ds4x_paged_tree_attn", *cache, _per(row0, torch.int64, "row0", cache[4], dev),
+          _per(parent, torch.int32, "parent", n, dev),
+          None if row_begin is None else _per(row_begin, torch.int64, "row_begin", n, dev), n, heads, q.data_ptr(), qs,
+          float(softmax_scale), out.data_ptr(), os, lp, wp, ws.numel(), _raw_stream(stream, dev))
+
+
+def _probabilities(t, name, n, vocab, dtype, dev):
+    """A [n, vocab] tensor of contiguous rows: its stride from row to row."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}")
+    if t.dtype is not dtype or dtype not in _ELEMENT_TYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16, the target's type, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != vocab or (vocab > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{n}, {vocab}] with contiguous rows")
+    return t.stride(0) if n > 1 else -(-vocab // 8) * 8
+
+
+def ds4x_verify_drafts(cu_tokens, parent, tokens, target, draft, u, path, out_tokens, n_path, ws, stream=None):
+    """Which drafted tokens (int32 [n]) stand: target and draft (or None) f32 or
+    bf16 [n, vocab] probabilities after each node (rows may be strided), u f32
+    [n] random numbers; writes path and out_tokens int32 [n] and n_path int32
+    [n_seqs].  cu_tokens and parent as ds4x_paged_tree_attn; ws u8 >= 256 bytes."""
+    dev = target.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("target must be a CUDA tensor on the current device")
+    n, vocab, seqs = parent.numel(), target.shape[-1] if target.dim() == 2 else 0, n_path.numel()
+    ts = _probabilities(target, "target", n, vocab, target.dtype, dev)
+    ds = 0 if draft is None else _probabilities(draft, "draft", n, vocab, target.dtype, dev)
+    _call("ds4x_verify_drafts", _per(cu_tokens, torch.int32, "cu_tokens", seqs + 1, dev), seqs, n,
+          _per(parent, torch.int32, "parent", n, dev), _per(tokens, torch.int32, "tokens", n, dev), target.data_ptr(), ts,
+          None if draft is None else draft.data_ptr(), ds, _ELEMENT_TYPES[target.dtype], vocab,
+          _per(u, torch.float32, "u", n, dev), _per(path, torch.int32, "path", n, dev),
+          _per(out_tokens, torch.int32, "out_tokens", n, dev), _per(n_path, torch.int32, "n_path", seqs, dev),
+          _per(ws, torch.uint8, "ws", None, dev), ws.numel(), _raw_stream(stream, dev))
+
+
+def ds4x_paged_keep(pages, page_rows, table, cu_tokens, row0, path, n_path, ws, stream=None):
+    """The accepted nodes' rows moved together: row row0[s] + path[i] of a
+    sequence to row0[s] + i, i < n_path[s] (path int32 [n], n_path int32
+    [n_seqs], as ds4x_verify_drafts writes them)."""
+    dev, wp, cache = _paged(pages, page_rows, table, cu_tokens, ws)
+    _call("ds4x_paged_keep", *cache, _per(row0, torch.int64, "row0", cache[4], dev),
+          _per(path, torch.int32, "path", path.numel(), dev), _per(n_path, torch.int32, "n_path", cache[4], dev),
+          path.numel(), wp, ws.numel(), _raw_stream(stream, dev))

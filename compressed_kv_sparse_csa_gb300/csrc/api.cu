@@ -378,6 +378,12 @@ bool paged_overlap(const void *a, int64_t a_stride, const void *b, int64_t b_str
   return d < uintptr_t(vec) || s - d < uintptr_t(vec);
 }
 
+// Whether two arrays share no byte.
+bool apart(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 >= b0 + uintptr_t(b_bytes) || b0 >= a0 + uintptr_t(a_bytes);
+}
+
 int paged_attn(PagedAttn &a, const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
                int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, void *ws,
                size_t ws_bytes, ds4x_stream_t stream) {
@@ -433,6 +439,58 @@ int ds4x_paged_gather(const uint8_t *pages, int64_t n_pages, int32_t page_rows, 
   return from_cuda(launch_paged_gather(c, row0, out, out_type == DS4X_BF16, out_stride, n_tokens, ws, stream));
 }
 
+int ds4x_paged_keep(uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                    int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                    const int32_t *path, const int32_t *n_path, int64_t n_tokens, void *ws, size_t ws_bytes,
+                    ds4x_stream_t stream) {
+  PagedCache c;
+  const int e = paged_cache(pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, &c);
+  if (e != DS4X_OK) return e;
+  if (row0 == nullptr || path == nullptr || n_path == nullptr) return DS4X_EINVAL;
+  if (!aligned_to(row0, 8) || !aligned_to(path, 4) || !aligned_to(n_path, 4)) return DS4X_EINVAL;
+  if (n_tokens < 1 || n_tokens > int64_t(INT32_MAX)) return DS4X_EINVAL;
+  if (ws_bytes < kWsHeaderBytes) return DS4X_EWORKSPACE;
+  const int arch = check_arch();
+  if (arch != DS4X_OK) return arch;
+  return from_cuda(launch_paged_keep(c, row0, path, n_path, n_tokens, ws, stream));
+}
+
+int ds4x_verify_drafts(const int32_t *cu_tokens, int32_t n_seqs, int64_t n_tokens, const int32_t *parent,
+                       const int32_t *tokens, const void *target, int64_t target_stride, const void *draft,
+                       int64_t draft_stride, int32_t type, int32_t vocab, const float *u, int32_t *path,
+                       int32_t *out_tokens, int32_t *n_path, void *ws, size_t ws_bytes, ds4x_stream_t stream) {
+  if (cu_tokens == nullptr || parent == nullptr || tokens == nullptr || u == nullptr || path == nullptr ||
+      out_tokens == nullptr || n_path == nullptr || ws == nullptr)
+    return DS4X_EINVAL;
+  if (!aligned_to(cu_tokens, 4) || !aligned_to(parent, 4) || !aligned_to(tokens, 4) || !aligned_to(u, 4) ||
+      !aligned_to(path, 4) || !aligned_to(out_tokens, 4) || !aligned_to(n_path, 4) || !aligned16(ws))
+    return DS4X_EINVAL;
+  if (n_seqs < 1 || n_seqs == INT32_MAX || n_tokens < 1 || n_tokens > int64_t(INT32_MAX) || vocab < 1 ||
+      vocab > DS4X_VERIFY_MAX_VOCAB)
+    return DS4X_EINVAL;
+  if (!paged_vectors(target, type, target_stride, vocab) ||
+      (draft != nullptr && !paged_vectors(draft, type, draft_stride, vocab)))
+    return DS4X_EINVAL;
+  // no output shares memory with another array
+  const int64_t tb = 4 * n_tokens, sb = 4 * int64_t(n_seqs), row = vocab * int64_t(type == DS4X_BF16 ? 2 : 4);
+  const struct {
+    const void *p;
+    int64_t bytes;
+  } with[] = {{path, tb}, {out_tokens, tb}, {n_path, sb}, {cu_tokens, sb + 4}, {parent, tb}, {tokens, tb}, {u, tb},
+              {ws, int64_t(kWsHeaderBytes)},
+              {target, row + (n_tokens - 1) * target_stride * (type == DS4X_BF16 ? 2 : 4)},
+              {draft, draft != nullptr ? row + (n_tokens - 1) * draft_stride * (type == DS4X_BF16 ? 2 : 4) : 0}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 10; ++j)
+      if (with[j].bytes > 0 && !apart(with[i].p, with[i].bytes, with[j].p, with[j].bytes)) return DS4X_EINVAL;
+  if (ws_bytes < kWsHeaderBytes) return DS4X_EWORKSPACE;
+  const int arch = check_arch();
+  if (arch != DS4X_OK) return arch;
+  return from_cuda(launch_verify(Verify{cu_tokens, n_seqs, n_tokens, parent, tokens, target, draft, target_stride,
+                                        draft_stride, vocab, u, path, out_tokens, n_path},
+                                 type == DS4X_BF16, ws, stream));
+}
+
 size_t ds4x_paged_attn_workspace(void) { return paged_attn_ws_bytes(); }
 
 int ds4x_paged_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
@@ -456,6 +514,21 @@ int ds4x_paged_sparse_attn(const uint8_t *pages, int64_t n_pages, int32_t page_r
   if (k < 1 || k > DS4X_PAGED_MAX_LIST) return DS4X_EINVAL;
   PagedAttn a{PagedCache{}, nullptr, nullptr, n_rows, idx, k, n_tokens, n_heads, q_bf16, q_stride,
               softmax_scale, out_bf16, out_stride, lse};
+  return paged_attn(a, pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, ws_bytes,
+                    stream);
+}
+
+int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
+                         int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens,
+                         const int64_t *row0, const int32_t *parent, const int64_t *row_begin, int32_t n_tokens,
+                         int32_t n_heads, const uint16_t *q_bf16, int64_t q_stride, float softmax_scale,
+                         uint16_t *out_bf16, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                         ds4x_stream_t stream) {
+  if (row0 == nullptr || parent == nullptr || !aligned_to(row0, 8) || !aligned_to(parent, 4) ||
+      !aligned_to(row_begin, 8))
+    return DS4X_EINVAL;
+  PagedAttn a{PagedCache{}, row_begin, nullptr, nullptr, nullptr, 0, n_tokens, n_heads, q_bf16, q_stride,
+              softmax_scale, out_bf16, out_stride, lse, row0, parent};
   return paged_attn(a, pages, n_pages, page_rows, table, n_seqs, seq_pages, table_stride, cu_tokens, ws, ws_bytes,
                     stream);
 }

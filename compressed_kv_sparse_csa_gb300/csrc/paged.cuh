@@ -77,8 +77,27 @@ cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const 
 cudaError_t launch_paged_gather(const PagedCache &c, const int64_t *row0, void *out, bool out_bf16,
                                 int64_t out_stride, int64_t n, void *ws, cudaStream_t stream);
 
-// Attention over row ranges (idx null: [row_begin, row_end) per token) or
-// lists (idx [n][k] with n_rows per sequence).
+// Moves row row0 + path[i] of each sequence to row0 + i, i < n_path.
+cudaError_t launch_paged_keep(const PagedCache &c, const int64_t *row0, const int32_t *path, const int32_t *n_path,
+                              int64_t n, void *ws, cudaStream_t stream);
+
+// The walk over drafted tokens (csrc/verify.cu).
+struct Verify {
+  const int32_t *cu;
+  int32_t n_seqs;
+  int64_t n_tokens;
+  const int32_t *parent, *tokens;
+  const void *target, *draft;  // draft may be null
+  int64_t target_stride, draft_stride;
+  int32_t vocab;
+  const float *u;
+  int32_t *path, *out, *n_path;
+};
+cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t stream);
+
+// Attention over row ranges (idx null: [row_begin, row_end) per token), lists
+// (idx [n][k] with n_rows per sequence) or trees (parent [n] with tree_row0 per
+// sequence; row_begin a position).
 struct PagedAttn {
   PagedCache c;
   const int64_t *row_begin, *row_end;
@@ -92,6 +111,8 @@ struct PagedAttn {
   uint16_t *out;
   int64_t out_stride;
   float *lse;
+  const int64_t *tree_row0;
+  const int32_t *parent;
 };
 size_t paged_attn_ws_bytes();
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream);

@@ -77,6 +77,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -107,6 +109,7 @@ constexpr int kTop = 7;                       // log2 of the largest weight, whe
 constexpr float kLazy = 8.0f + kTop;          // ... and at most
 constexpr int kTame = 20;
 constexpr int kRunTiles = 512;     // tiles that one sum goes over, at most
+constexpr int kTreeWords = DS4X_TREE_MAX_NODES / 64;
 enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 
 // Where a row lies: its codes (null: no row), and from there to its RoPE part and
@@ -140,6 +143,11 @@ struct __align__(1024) Smem {
   int2 seen[kPackTokens];           // packed: the rows that each token sees, from the unit's first
   long long out_at[kHeads];         // packed: a column's output (-1: no column)
   int end_unit, end_part;           // the CTA's last unit (-1: W has no part in its output), and its part (-1: the whole unit)
+  // trees: bit r of a tile's [token]: the token sees the tile's row r; [kPackTokens]: all tokens do.
+  // L writes a tile's when W has taken the rows of four tiles before, so when X is done with eight before.
+  unsigned long long sees[2 * kAhead][kPackTokens + 1];
+  unsigned long long line[kPackTokens][kTreeWords + 1];  // a token's node and its ancestors (L's)
+  int16_t parent[DS4X_TREE_MAX_NODES];                   // the sequence's (L's)
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
@@ -172,12 +180,16 @@ struct Args {
   uint64_t per_grid;  // 2^64 / CTAs, rounded up
   int32_t few;        // at most kFewUnits units
   __device__ __forceinline__ bool packed() const { return plan != nullptr; }
+  __device__ __forceinline__ bool tree() const { return a.parent != nullptr; }
 };
-// The same where the kernel is compiled for either: unpacked units cost nothing for the others.
-template <bool P>
+// The same where the kernel is compiled for one form: the others' units cost it nothing.
+// A tree's units are packed ones, of a token at least; heads beyond 64 in groups.
+enum class Form { kSingle, kPacked, kTree };
+template <Form F>
 struct ArgsFor : Args {
   ArgsFor(const Args &g) : Args(g) {}
-  static __device__ __forceinline__ constexpr bool packed() { return P; }
+  static __device__ __forceinline__ constexpr bool packed() { return F != Form::kSingle; }
+  static __device__ __forceinline__ constexpr bool tree() { return F == Form::kTree; }
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -296,6 +308,12 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
+// Which of the plan's entries a packed unit is (a tree's may be one group of its heads).
+template <class A>
+__device__ __forceinline__ int plan_unit(const A &g, int unit) {
+  return g.tree() && g.groups > 1 ? unit / g.groups : unit;
+}
+
 // A unit's query vectors ("columns"): heads h0 .. of token t0, or, packed, all heads
 // of count tokens from t0, head by head.
 struct Columns {
@@ -303,10 +321,11 @@ struct Columns {
   template <class A>
   __device__ __forceinline__ Columns(const A &g, int unit) {
     if (g.packed()) {
-      const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[unit]));
+      const int group = g.tree() && g.groups > 1 ? unit % g.groups : 0;
+      const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[plan_unit(g, unit)]));
       t0 = p.x;
-      h0 = 0;
-      n = p.y * g.a.n_heads;
+      h0 = group * g.group;
+      n = g.tree() && g.groups > 1 ? min(g.group, g.a.n_heads - h0) : p.y * g.a.n_heads;
     } else {
       t0 = unit / g.groups;
       h0 = (unit % g.groups) * g.group;
@@ -342,8 +361,22 @@ __device__ __forceinline__ bool past_table(const PagedAttn &a, int t) {
 template <class A>
 __device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
   if (!g.packed()) return token_rows(g.a, unit / g.groups);
-  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[unit]) + 1);
+  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[plan_unit(g, unit)]) + 1);
   return Rows{p.x, p.y};
+}
+// The rows of node t - from of a tree behind row row0 of its sequence, from the first
+// that it may see to its own; `odd`: some lie where the table does not go, or the node
+// has no place (then it sees nothing).
+__device__ __forceinline__ Rows tree_rows(const PagedAttn &a, int t, int from, int64_t row0, bool *odd) {
+  const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
+  if (row0 < 0 || t - from >= DS4X_TREE_MAX_NODES) {
+    *odd = true;
+    return Rows{0, 0};
+  }
+  const int64_t b = a.row_begin != nullptr ? min(row0, max(int64_t(0), int64_t(__ldcg(a.row_begin + t)))) : 0;
+  const int64_t e = min(room, min(row0, room) + (t - from) + 1);
+  if (row0 > room - (t - from) - 1) *odd = true;
+  return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
 }
 // A token without a row still has a tile (of rows that are not there): it writes the zeros.
 __device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
@@ -443,7 +476,7 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // the count of valid ones is on its way with their rows)
   const int per = (a.n_tokens + kThreads - 1) / kThreads;
   const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
-  auto rows_of = [&](int t) { return g.packed() ? unit_rows(g, t) : token_rows(a, t); };
+  auto rows_of = [&](int t) { return g.packed() ? unit_rows(g, t * (g.tree() ? g.groups : 1)) : token_rows(a, t); };
   const Rows first_rows = t0 < t1 ? rows_of(t0) : Rows{0, 0};
   // tokens behind are padding
   const int valid = g.packed() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
@@ -540,7 +573,7 @@ __device__ __forceinline__ void prefetch_queries(const A &g, int unit) {
   const auto fetch = [](const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
   };
-  const int heads = A::packed() ? g.a.n_heads : col.n;
+  const int heads = A::packed() && !(A::tree() && g.groups > 1) ? g.a.n_heads : col.n;
   for (int c = 0; c < col.n; c += heads)
     fetch(g.a.q + col.at(g, c, g.a.q_stride, kDim), uint32_t(heads) * kDim * 2);
 }
@@ -549,6 +582,61 @@ __device__ __forceinline__ void load_entries(const A &g, int t, int pos, int n, 
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (pos + 32 * k < n) entry[k] = __ldcg(g.a.idx + int64_t(t) * g.a.k + pos + 32 * k);
+}
+
+// Trees.  A lane a token of the unit: what its rows are.
+struct Sight {
+  int32_t lo, tree;  // absolute: the first row that it may see, the tree's first
+};
+// The lines of the unit's tokens t0 .. t0 + count - 1 (nodes t0 - from ..): each lane walks
+// from its own to the root, over the parents in shared memory.
+__device__ __noinline__ void tree_lines(const PagedAttn &a, Smem &sm, int t0, int count, int from, int64_t row0,
+                                        WsHeader *hdr) {
+  const int lane = threadIdx.x & 31, last = min(t0 + count - 1 - from, DS4X_TREE_MAX_NODES - 1);
+  __syncwarp();
+  bool odd = false;
+  for (int k = lane; k <= last; k += 32) {
+    const int32_t p = __ldcg(a.parent + from + k);
+    odd = odd || p < -1 || p >= k;
+    sm.parent[k] = int16_t(p < -1 || p >= k ? -1 : p);
+  }
+  if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  __syncwarp();
+  if (lane >= count) return;
+  unsigned long long *line = sm.line[lane];
+  for (int w = 0; w <= kTreeWords; ++w) line[w] = 0;
+  const int node = t0 + lane - from;
+  if (node > last) return;
+  // a node's position is row0 + its depth: those before the token's first are not seen
+  int steps = INT32_MAX;
+  if (a.row_begin != nullptr) {
+    int depth = 0;
+    for (int k = sm.parent[node]; k >= 0; k = sm.parent[k]) ++depth;
+    const int64_t b = __ldcg(a.row_begin + t0 + lane);
+    steps = int(max(int64_t(-1), min(int64_t(INT32_MAX), row0 + depth - max(b, int64_t(0)))));
+  }
+  for (int k = node; k >= 0 && steps >= 0; k = sm.parent[k], --steps) line[k >> 6] |= 1ull << (k & 63);
+}
+// Which of the 64 rows from row `first` on a lane's token sees.
+__device__ __forceinline__ unsigned long long tree_sees(const unsigned long long *line, Sight s, int64_t first) {
+  const int64_t lo = s.lo - first, to = s.tree - first;  // committed rows: bits lo .. to - 1
+  unsigned long long bits = 0;
+  if (to > 0 && lo < 64) {
+    bits = to >= 64 ? ~0ull : (1ull << to) - 1;
+    if (lo > 0) bits = bits >> lo << lo;
+  }
+  if (to < 64) {
+    const int64_t k = -to;  // bit 0 is node k
+    if (k <= 0)
+      bits |= line[0] << -k;
+    else if (k < DS4X_TREE_MAX_NODES)
+      bits |= line[k >> 6] >> (k & 63) | (k & 63 ? line[(k >> 6) + 1] << (64 - (k & 63)) : 0ull);
+  }
+  return bits;
+}
+__device__ __forceinline__ unsigned long long warp_or(unsigned long long v) {
+  return (unsigned long long)(__reduce_or_sync(0xffffffffu, uint32_t(v >> 32))) << 32 |
+         __reduce_or_sync(0xffffffffu, uint32_t(v));
 }
 
 template <class A>
@@ -561,8 +649,13 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
   Walk w;
   w.begin(sm, total);
   for (;;) {
-    const int t = g.packed() ? __ldcg(&g.plan->unit[w.unit].t0) : w.unit / g.groups;
+    const int t = g.packed() ? __ldcg(&g.plan->unit[plan_unit(g, w.unit)].t0) : w.unit / g.groups;
     if (lane == 0 && w.i0 > 0 && w.off == w.from) prefetch_queries(g, w.unit);
+    int count = 0;
+    bool lines = false;  // the unit's are there
+    int64_t row0 = 0;
+    Sight sight{0, 0};
+    if (A::tree()) count = __ldcg(&g.plan->unit[plan_unit(g, w.unit)].count);
     bool fresh = true;
     // a list's entries are on their way a tile ahead
     int entry[2] = {0, 0};
@@ -583,7 +676,30 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
           if (a.idx != nullptr && sq.s >= 0)  // (below 0: no row)
             n_rows = int(max(int64_t(0), min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + sq.s)))));
         }
+        if (A::tree() && sq.s >= 0) {
+          row0 = __ldcg(a.tree_row0 + sq.s);
+          sight.tree = int32_t(min(max(row0, int64_t(0)), int64_t(a.c.seq_pages) << a.c.page_log2));
+          if (a.row_begin != nullptr && lane < count)
+            sight.lo = int32_t(min(int64_t(sight.tree), max(int64_t(0), int64_t(__ldcg(a.row_begin + t + lane)))));
+        }
         fresh = false;
+      }
+      if (A::tree()) {
+        const int64_t first = int64_t(w.r0) + pos - lane;
+        if (!lines && sq.s >= 0 && first + kTile > sight.tree) {
+          tree_lines(a, sm, t, count, max(0, sq.from), row0, hdr);
+          lines = true;
+        }
+        // (before the tree's first row no line is looked at)
+        unsigned long long bits = lane < count ? tree_sees(sm.line[lane], sight, first) : 0;
+        if (w.n == 0) bits = 0;
+        unsigned long long all = ~warp_or(lane < count ? ~bits : 0), any = warp_or(bits);
+        if (i >= kAhead) wait_bar(sm, &sm.lfree[i % kAhead], (i / kAhead - 1) & 1, hdr);
+        if (lane < kPackTokens) sm.sees[i % (2 * kAhead)][lane] = bits;
+        if (lane == 0) sm.sees[i % (2 * kAhead)][kPackTokens] = all;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (!(any >> (lane + 32 * k) & 1)) row[k] = -1;
       }
       const int seq = sq.s;
       int2 at[2];
@@ -939,7 +1055,7 @@ __device__ __forceinline__ void role_o(const A &g, Smem &sm, WsHeader *hdr) {
 template <class A>
 __device__ __forceinline__ void make_query(const A &g, Smem &sm, int unit, int xw, int lane) {
   const Columns col(g, unit);
-  if (g.packed() && xw == 0 && lane < kPackTokens) {  // (warp 0)
+  if (g.packed() && !A::tree() && xw == 0 && lane < kPackTokens) {  // (warp 0)
     const Rows u = unit_rows(g, unit);
     const Rows r = lane * g.a.n_heads < col.n ? token_rows(g.a, col.t0 + lane) : Rows{0, 0};
     const int lo = r.n > 0 ? int(r.r0 - u.r0) : 0;
@@ -1005,7 +1121,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
   // P^T: row r0, heads hb, hb + 1; heads 8 j on at the 16-byte chunk's number ^ j
   const uint32_t p0 = smem_u32(sm.p[0]) + r0 * 128 + (((4 * half) ^ (r0 & 7)) << 4) + 4 * (lane & 3);
   make_query(g, sm, sm.unit0, xw, lane);
-  if (A::packed()) named_bar_sync(kBarX, kXThreads);  // `seen`
+  if (A::packed() && !A::tree()) named_bar_sync(kBarX, kXThreads);  // `seen`
   Walk w;
   w.begin(sm, total);
   for (int seg = 0;; ++seg) {
@@ -1019,7 +1135,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
     // packed).  In the tiles' order and the run's own, so that nothing else shows in the sums' rounding.
     uint32_t wide = 0;
     int lo = 0, hi = INT32_MAX;          // packed: the rows that all of the unit's tokens see
-    if (A::packed()) {
+    if (A::packed() && !A::tree()) {
       const int count = __ldcg(&g.plan->unit[w.unit].count);
       for (int j = 0; j < count; ++j) {
         lo = max(lo, sm.seen[j].x);
@@ -1047,6 +1163,10 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
             for (int k = 0; k < 8; ++k) {
               const int j = ((hb + 8 * (k >> 1) + (k & 1)) * g.per_head) >> 16;
               if (j >= kPackTokens) break;
+              if (A::tree()) {
+                if (rows & sm.sees[i % (2 * kAhead)][j]) wide |= 1u << k;
+                continue;
+              }
               const int from = max(0, sm.seen[j].x - first), to = min(kTile, sm.seen[j].y - first);
               if (to > from && (rows >> from & ~0ull >> (kTile - (to - from)))) wide |= 1u << k;
             }
@@ -1073,7 +1193,16 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       bool moves = over > kLazy || fresh != 0;
       if (A::packed()) {
         const int first = (w.off + (i - w.i0)) * kTile;
-        if (busy && (first < lo || first > hi - kTile)) {  // rows that some token does not see
+        if (A::tree()) {
+          const unsigned long long *sees = sm.sees[i % (2 * kAhead)];
+          if (busy && ~sees[kPackTokens] != 0) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int j = ((hb + 8 * (k >> 2) + (k & 1)) * g.per_head) >> 16;
+              if (j < kPackTokens && !(sees[j] >> (r0 + 8 * ((k >> 1) & 1)) & 1)) d[k] = -INFINITY;
+            }
+          }
+        } else if (busy && (first < lo || first > hi - kTile)) {  // rows that some token does not see
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int row = first + r0 + 8 * ((k >> 1) & 1), j = ((hb + 8 * (k >> 2) + (k & 1)) * g.per_head) >> 16;
@@ -1294,9 +1423,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         count = min(pack, to - t);
         int rest = 0;  // tokens whose rows do not meet those from lo to hi
         int64_t lo = 0, hi = 0;
+        bool odd = false;
+        const int64_t row0 = a.parent != nullptr ? __ldcg(a.tree_row0 + s) : 0;
         for (int j = 0; j < count; ++j) {
-          if (past_table(a, t + j)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-          const Rows r = token_rows(a, t + j);
+          if (a.parent == nullptr) odd = odd || past_table(a, t + j);
+          const Rows r = a.parent != nullptr ? tree_rows(a, t + j, from, row0, &odd) : token_rows(a, t + j);
           if (r.n == 0) continue;
           if (hi == 0) lo = r.r0, hi = r.r0 + r.n;
           else if (r.r0 > hi || r.r0 + r.n < lo) ++rest;
@@ -1304,7 +1435,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         }
         // Rows between the tokens' ranges, which no token sees, must not be read (and
         // would be work for nothing): then each token is its own unit.
-        units = rest > 0 ? count : 1;
+        // (A tree's tokens all see its first row, or their windows end up to it.)
+        if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+        units = rest > 0 && a.parent == nullptr ? count : 1;
         u = Pack{t, count, int32_t(lo), int32_t(hi - lo)};
       }
     }
@@ -1332,8 +1465,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
   if (tid == 0) plan->n_units = base;
 }
 
-template <bool P>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P> g, Parts *__restrict__ parts,
+template <Form F>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<F> g, Parts *__restrict__ parts,
                                                                  WsHeader *__restrict__ hdr) {
   // (no static shared memory: the dynamic begins at the window's start, as aligned as Smem asks)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1672,10 +1805,11 @@ __global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args
 size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts) + sizeof(Plan); }
 
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream) {
-  static std::atomic<uint64_t> smem_set[2];
+  static std::atomic<uint64_t> smem_set[3];
   const int smem = int(sizeof(Smem));
-  cudaError_t e = set_max_smem_once(paged_attn_kernel<false>, smem, smem_set[0]);
-  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<true>, smem, smem_set[1]);
+  cudaError_t e = set_max_smem_once(paged_attn_kernel<Form::kSingle>, smem, smem_set[0]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<Form::kPacked>, smem, smem_set[1]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<Form::kTree>, smem, smem_set[2]);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
@@ -1695,22 +1829,28 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   // launch costs more than the passes that it saves.  Packed / single, us a call:
   // 1 sequence x 2 tokens x 20 heads x 700 rows 17.1 / 12.2, 8 x 2 x 16 x 2000
   // 22.4 / 23.0, 24 x 5 x 20 x 4500 66 / 130, 1 x 512 x 16 x 4096 124 / 420.
-  const int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
-  const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas;
+  const bool tree = a.parent != nullptr;
+  const int fits = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
+  const int pack = tree && fits < 1 ? 1 : fits;
+  const bool packed = tree || (a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas);
   Args g{a, packed ? plan : nullptr, groups, 0, 0, 0, 0, 0};
   g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;
-  g.group = packed ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
-  g.per_head = 65536 / a.n_heads + 1;
+  g.group = packed && groups == 1 ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
+  g.per_head = groups == 1 ? 65536 / a.n_heads + 1 : 0;  // (of heads in groups, a unit's are one token's)
   g.n_cols = (g.group + 15) / 16 * 16;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
   if (packed) {
     e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
     if (e != cudaSuccess) return e;
   }
-  e = packed ? launch_pdl(paged_attn_kernel<true>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
-                          ArgsFor<true>(g), parts, hdr)
-             : launch_pdl(paged_attn_kernel<false>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
-                          ArgsFor<false>(g), parts, hdr);
+  const auto launch = [&](auto form) {
+    constexpr Form F = decltype(form)::value;
+    return launch_pdl(paged_attn_kernel<F>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, ArgsFor<F>(g),
+                      parts, hdr);
+  };
+  e = tree     ? launch(std::integral_constant<Form, Form::kTree>{})
+      : packed ? launch(std::integral_constant<Form, Form::kPacked>{})
+               : launch(std::integral_constant<Form, Form::kSingle>{});
   if (e != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;  // nothing is split
   if (g.few && (rows + kTile - 1) / kTile <= kShortParts)

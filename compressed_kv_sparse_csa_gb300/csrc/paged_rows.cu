@@ -356,6 +356,61 @@ paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__rest
   }
 }
 
+// ---- keeping accepted rows ---------------------------------------------------------
+
+// A block a sequence.  Its rows move kKeepRows at a time, all read before any is
+// written: entry i reads at or behind i, so what a later round reads no earlier one has
+// written.
+constexpr int kRowWords = DS4X_PAGED_ROW_BYTES / 16;  // 14 of codes, 8 of the RoPE part, 1 of scales
+constexpr int kKeepPerWarp = 4, kKeepRows = kWarps * kKeepPerWarp;
+
+__device__ __forceinline__ uint4 *row_word(const PagedCache &c, const PagedRow &p, int lane) {
+  const int64_t at = lane < 14   ? paged_code_off(p) + 16 * lane
+                     : lane < 22 ? paged_tail_off(c, p) + 16 * (lane - 14)
+                                 : paged_scale_off(c, p);
+  return reinterpret_cast<uint4 *>(const_cast<uint8_t *>(p.page) + at);
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+paged_keep_kernel(PagedCache c, const int64_t *__restrict__ row0, const int32_t *__restrict__ path,
+                  const int32_t *__restrict__ n_path, int64_t n_tokens, WsHeader *__restrict__ hdr) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x;
+  const int64_t from = max(0, __ldcg(c.cu + s)), to = min(n_tokens, int64_t(__ldcg(c.cu + s + 1)));
+  const int64_t nodes = max(int64_t(0), to - from), first = __ldcg(row0 + s);
+  int64_t n = __ldcg(n_path + s);
+  bool odd = n > nodes;
+  n = min(n, nodes);
+  for (int64_t i0 = 0; i0 < n; i0 += kKeepRows) {
+    uint4 w[kKeepPerWarp];
+    uint4 *to_row[kKeepPerWarp];
+#pragma unroll
+    for (int k = 0; k < kKeepPerWarp; ++k) {
+      const int64_t i = i0 + warp + kWarps * k;
+      to_row[k] = nullptr;
+      if (i >= n) continue;
+      const int64_t j = __ldcg(path + from + i);
+      if (j == i) continue;
+      const bool in = j > i && j < nodes;
+      const PagedRow src = in ? paged_row(c, s, first + j) : PagedRow{nullptr, 0};
+      const PagedRow dst = in ? paged_row(c, s, first + i) : PagedRow{nullptr, 0};
+      if (src.page == nullptr || dst.page == nullptr) {
+        odd = true;
+      } else if (lane < kRowWords) {
+        w[k] = __ldcg(row_word(c, src, lane));
+        to_row[k] = row_word(c, dst, lane);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKeepPerWarp; ++k)
+      if (to_row[k] != nullptr) __stcg(to_row[k], w[k]);
+    __syncthreads();
+  }
+  if (odd && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+}
+
 }  // namespace
 
 namespace {
@@ -385,6 +440,12 @@ cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const 
   WsHeader *hdr = static_cast<WsHeader *>(ws);
   return launch_pdl(in_bf16 ? paged_append_kernel<true> : paged_append_kernel<false>, blocks, kWarps * 32, 0, stream,
                     c, row0, in, in_stride, n, per, pos, inv_freq, int(halves), hdr);
+}
+
+cudaError_t launch_paged_keep(const PagedCache &c, const int64_t *row0, const int32_t *path, const int32_t *n_path,
+                              int64_t n, void *ws, cudaStream_t stream) {
+  return launch_pdl(paged_keep_kernel, unsigned(c.n_seqs), kWarps * 32, 0, stream, c, row0, path, n_path, n,
+                    static_cast<WsHeader *>(ws));
 }
 
 cudaError_t launch_paged_gather(const PagedCache &c, const int64_t *row0, void *out, bool out_bf16,

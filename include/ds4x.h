@@ -619,6 +619,126 @@ int ds4x_paged_sparse_attn(const uint8_t *pages, int64_t n_pages, int32_t page_r
                            const uint16_t *q_bf16, int64_t q_stride, float softmax_scale, uint16_t *out_bf16,
                            int64_t out_stride, float *lse, void *ws, size_t ws_bytes, ds4x_stream_t stream);
 
+/* ---- Drafted tokens over the paged cache -----------------------------------
+ *
+ * A step that checks drafts: ds4x_paged_append of every sequence's nodes,
+ * ds4x_paged_tree_attn in each layer, the model's probabilities,
+ * ds4x_verify_drafts, and ds4x_paged_keep in each layer.  The pages have no
+ * counterpart to it.
+ *
+ * A sequence's tokens of the call (cu_tokens, as above) are the nodes of its
+ * draft, at most DS4X_TREE_MAX_NODES: parent is i32 [n_tokens], the number
+ * within its sequence of the node that a node follows, below its own, or -1
+ * for one that follows the rows before the draft.  Another value flags
+ * DS4X_EDEVICE and counts as -1.  A chain has parent[j] = j - 1.  A node's
+ * depth is the number of its ancestors; its position is row0[s] + depth
+ * (ds4x_paged_append's pos).
+ */
+enum { DS4X_TREE_MAX_NODES = 1024 }; /* a sequence's draft */
+
+/*
+ * Attention of each node over the rows before its sequence's draft and over
+ * itself and its ancestors, but no other node: softmax, out and lse as
+ * ds4x_paged_attn.  (Over lists of selected rows a draft needs no call of its
+ * own: its nodes' ancestors go into the lists of ds4x_paged_sparse_attn.)
+ *
+ *   row0       i64 [n_seqs]: node j of sequence s is the sequence's row
+ *              row0[s] + j, as ds4x_paged_append places it
+ *   row_begin  i64 [n_tokens] or NULL: the first position that a node sees (a
+ *              sliding window): of the rows before the draft those from
+ *              row_begin on, of its line the nodes whose position is at least
+ *              that; below 0: 0
+ *   the rest as ds4x_paged_attn, the workspace too
+ *
+ * A node that sees no row gets zeros and lse -inf; so do nodes beyond the
+ * first DS4X_TREE_MAX_NODES of a sequence and those of a sequence with row0
+ * below 0, which also flag DS4X_EDEVICE.  Rows that a node does not see have
+ * no part in its results, whatever they hold.
+ */
+int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table,
+                         int32_t n_seqs, int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens,
+                         const int64_t *row0, const int32_t *parent, const int64_t *row_begin, int32_t n_tokens,
+                         int32_t n_heads, const uint16_t *q_bf16, int64_t q_stride, float softmax_scale,
+                         uint16_t *out_bf16, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                         ds4x_stream_t stream);
+
+/*
+ * Decides which drafted tokens stand, so that each sequence's new tokens are
+ * distributed as if the target had drawn them one by one.  Node 0 of a sequence
+ * is its newest token; the walk starts there.  At a node with target
+ * probabilities p and draft probabilities q, its children j are tried in
+ * order, x = tokens[j]:
+ *
+ *   accepted (the walk goes on from j) iff  u[j] q(x) C < w(x),
+ *     w(y) = max(p(y) - t q(y), 0), at first t = 0 and C = 1;
+ *   after one that is not, t grows by C and C = sum_y w(y)
+ *
+ * which is p(x) / q(x) for the first child and the same of the renormalised
+ * rest of p for the others.  Without draft probabilities (draft NULL: the
+ * drafts are not draws, say the likeliest tokens) q counts as 1: w(y) = p(y),
+ * 0 for tokens tried before, and C = 1 less what p gave those.  Where no child
+ * is left the last token is drawn from w: the least y with
+ *
+ *   sum_{z <= y} w(z) > u[node 0] sum_z w(z)
+ *
+ * (every probability where there were no children).  Comparisons and sums are
+ * good to 2^-40 of the sum, so a result may differ from the exact one's only
+ * where u is that near to a border.
+ *
+ *   cu_tokens  i32 [n_seqs + 1], as above
+ *   n_tokens   1 .. 2^31 - 1
+ *   tokens     i32 [n_tokens]: the drafted tokens (node 0's is not looked at);
+ *              one outside [0, vocab) is not accepted and flags DS4X_EDEVICE
+ *   target     f32 or bf16 (type) [n_tokens][vocab]: row t is the target's
+ *              distribution of the token after node t; target_stride
+ *              elements from row to row (>= vocab, a multiple of 8 (bf16) or
+ *              4 (f32))
+ *   draft      the same type, draft_stride likewise, or NULL: row t is what
+ *              node t's children were drawn from, independently
+ *   vocab      1 .. DS4X_VERIFY_MAX_VOCAB
+ *   u          f32 [n_tokens] in [0, 1): uniform random numbers
+ *   path       i32 [n_tokens]: per sequence the accepted nodes' numbers, from
+ *              node 0 on, then -1
+ *   out_tokens i32 [n_tokens]: the new tokens, as many: tokens[path[1]] ..,
+ *              then the one drawn last; then -1
+ *   n_path     i32 [n_seqs]: how many those are (0 for a sequence without a
+ *              token, or of more than DS4X_TREE_MAX_NODES, which flags
+ *              DS4X_EDEVICE)
+ *   ws         the status header: 256 bytes, zero before first use
+ *
+ * Probabilities need not sum to exactly 1 (the last draw is by their sum).
+ * Negative ones and NaN count as zero.  Where all that is left is zero, the last
+ * token is -1 and DS4X_EDEVICE is flagged.
+ * Common errors as above; DS4X_EINVAL also for an output that overlaps another
+ * array of the call.
+ */
+enum { DS4X_VERIFY_MAX_VOCAB = 1 << 20 };
+int ds4x_verify_drafts(const int32_t *cu_tokens, int32_t n_seqs, int64_t n_tokens, const int32_t *parent,
+                       const int32_t *tokens, const void *target, int64_t target_stride, const void *draft,
+                       int64_t draft_stride, int32_t type, int32_t vocab, const float *u, int32_t *path,
+                       int32_t *out_tokens, int32_t *n_path, void *ws, size_t ws_bytes, ds4x_stream_t stream);
+
+/*
+ * Keeps the accepted nodes' rows: the sequence's row row0[s] + path[i] moves to
+ * row0[s] + i, i = 0 .. n_path[s] - 1 (path and n_path as ds4x_verify_drafts
+ * writes them).  The sequence then has row0[s] + n_path[s] rows; those behind,
+ * and rows before row0, are as they were.
+ *
+ *   path       i32 [n_tokens], cu_tokens[s] + i for entry i of sequence s;
+ *              i <= path[i] < the sequence's tokens; others are left out
+ *              (the row stays as it was) and flag DS4X_EDEVICE
+ *   n_path     i32 [n_seqs]: 0 .. the sequence's tokens; a larger one counts
+ *              as that and flags DS4X_EDEVICE, one below 0 counts as 0
+ *   n_tokens   1 .. 2^31 - 1
+ *   ws         the status header: 256 bytes, zero before first use
+ *
+ * Sequences must not share a page that a move writes.
+ */
+int ds4x_paged_keep(uint8_t *pages, int64_t n_pages, int32_t page_rows, const int32_t *table, int32_t n_seqs,
+                    int32_t seq_pages, int64_t table_stride, const int32_t *cu_tokens, const int64_t *row0,
+                    const int32_t *path, const int32_t *n_path, int64_t n_tokens, void *ws, size_t ws_bytes,
+                    ds4x_stream_t stream);
+
 /* ---- Packed-row checkpoints (host memory, no CUDA call) -----------------
  *
  * A checkpoint holds, per layer, the native packed rows: the raw sliding
