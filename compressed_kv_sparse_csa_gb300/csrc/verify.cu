@@ -1,7 +1,29 @@
 // Which drafted tokens stand: the walk over each sequence's draft by the target's
 // and the draft's probabilities (include/ds4x.h, ds4x_verify_drafts).
 //
-// A block a sequence.
+// With p and q of the node where the walk stands and t draws of q taken off, the
+// rest of p is max(p - t q, 0) / C.  One rejection more makes it max(that - q, 0),
+// renormalised: max(p - (t + C) q, 0) / C'.  So a node's whole history is the two
+// numbers t and C, and each rejection is one pass over the rows for the next C.
+// Without q the rest is p without the tokens tried, and C = 1 less theirs.
+//
+// What is read.  A child's decision needs p and q at one token: those of all
+// children are fetched at once, beforehand, so the walk runs in shared memory.
+// Only the node where it ends, and nodes with a second child, need rows: one pass
+// of V probabilities each, which also leaves a sum for each 1024 of them, so that
+// the last token is found by prefix sums and one look at 1024 again.
+//
+// Sums.  A token is chosen among up to 2^20 by where u falls between partial sums,
+// so those must be far better than fp32: pairs of floats, hi + lo, by error-free
+// additions (Knuth's two-sum) and products (by fma), good to 2^-44 or so.  Not fp64:
+// a warp's instruction takes some 50 cycles of an SM's one pipe.  256 sequences of
+// 131,072 tokens took 2.77 ms in fp64 throughout, and 206 us with fp64 from a warp's
+// 1024 on alone.
+//
+// Work split.  A cluster of 1 to 16 blocks a sequence, a contiguous slice of the
+// vocabulary each; every block walks by itself (the same numbers, the same order, so
+// the same decisions), and after a pass they swap their sums through distributed
+// shared memory.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -9,146 +31,486 @@
 namespace ds4x {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChunk = 1024;          // probabilities a warp sums at a time
+constexpr int kMaxChunks = DS4X_VERIFY_MAX_VOCAB / kChunk;
+constexpr int kMaxCluster = 16;
+constexpr int kMaxNodes = DS4X_TREE_MAX_NODES;
 
-template <bool BF16>
-__device__ __forceinline__ float prob(const void *p, int64_t at) {
-  const float v = BF16 ? __bfloat162float(__ushort_as_bfloat16(__ldcg(static_cast<const uint16_t *>(p) + at)))
-                       : __ldcg(static_cast<const float *>(p) + at);
-  return fmaxf(v, 0.0f);
+// A number in two floats, hi + lo (|lo| at most half a step of hi).
+struct __align__(8) Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair pair(float h, float l) {  // |l| below |h|
+  const float s = __fadd_rn(h, l);
+  return Pair{s, __fadd_rn(l, -__fadd_rn(s, -h))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float s = __fadd_rn(a.h, b.h), bb = __fadd_rn(s, -a.h);
+  const float e = __fadd_rn(__fadd_rn(a.h, -__fadd_rn(s, -bb)), __fadd_rn(b.h, -bb));
+  return pair(s, __fadd_rn(e, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair operator*(float a, Pair b) {
+  const float h = __fmul_rn(a, b.h);
+  return pair(h, __fmaf_rn(a, b.l, __fmaf_rn(a, b.h, -h)));
+}
+__device__ __forceinline__ Pair operator-(Pair a) { return Pair{-a.h, -a.l}; }
+__device__ __forceinline__ bool operator>(Pair a, Pair b) {
+  return __fadd_rn(__fadd_rn(a.h, -b.h), __fadd_rn(a.l, -b.l)) > 0.0f;
+}
+__device__ __forceinline__ bool some(Pair a) { return a.h > 0.0f; }
+__device__ __forceinline__ Pair shfl_up(Pair a, int o) {
+  return Pair{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+}
+__device__ __forceinline__ Pair shfl(Pair a, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
+// A lane's sum over the lanes up to it.
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair x = shfl_up(v, o);
+    if (lane >= o) v = x + v;
+  }
+  return v;
 }
 
-__device__ __forceinline__ double block_sum(double v, double *red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Shared {
+  Pair sums[kMaxChunks];              // the block's chunks' sums of the latest pass
+  Pair total[2][kMaxCluster];         // the blocks' (written by all of them), of this pass and the one before
+  Pair red[kWarps];
+  float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // of each node's token, after its parent
+  int32_t token[kMaxNodes];           // outside the vocabulary: -1
+  int16_t parent[kMaxNodes], path[kMaxNodes];
+  Pair base;
+  int chunk, found;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of the cluster's block r
+__device__ __forceinline__ void store_remote(Pair *p, uint32_t r, Pair v) {
+  const uint32_t a = uint32_t(__cvta_generic_to_shared(p));
+  asm volatile("{\n\t.reg .b32 x;\n\tmapa.shared::cluster.u32 x, %0, %1;\n\tst.shared::cluster.v2.f32 [x], {%2, %3};\n\t}" ::"r"(a),
+               "r"(r), "f"(v.h), "f"(v.l)
+               : "memory");
+}
+
+// NaN and negative ones count as zero.
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, 0.0f); }
+
+// N probabilities in a row, from element y on (a multiple of N; past the vocabulary: 0).
+template <bool BF16, int N>
+struct Probs {
+  static_assert(N * (BF16 ? 2 : 4) <= 16, "one load");
+  uint32_t w[N * (BF16 ? 2 : 4) / 4];
+  __device__ __forceinline__ void load(const void *row, int y, int vocab) {
+    if (y + N <= vocab) {
+      const uint8_t *at = static_cast<const uint8_t *>(row) + int64_t(y) * (BF16 ? 2 : 4);
+      if constexpr (sizeof(w) == 16) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(at));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(at));
+        w[0] = v.x, w[1] = v.y;
+      }
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int k = 0; k < kThreads / 32; ++k) v += red[k];
+      for (uint32_t &v : w) v = 0;
+      for (int i = 0; i < N; ++i)
+        if (y + i < vocab) {
+          if constexpr (BF16) {
+            const uint32_t v = __ldcg(static_cast<const uint16_t *>(row) + y + i);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k)
+              if (k == i / 2) w[k] |= v << (16 * (i & 1));
+          } else {
+            const uint32_t v = __ldcg(static_cast<const uint32_t *>(row) + y + i);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+              if (k == i) w[k] = v;
+          }
+        }
+    }
+  }
+  __device__ __forceinline__ float2 two(int k) const {  // elements 2 k, 2 k + 1
+    const float a = __uint_as_float(BF16 ? w[k] << 16 : w[2 * k]);
+    const float b = __uint_as_float(BF16 ? w[k] & 0xffff0000u : w[2 * k + 1]);
+    return make_float2(clean(a), clean(b));
+  }
+};
+
+// Two pairs, by instructions of two fp32 operations.
+struct Pair2 {
+  float2 hi, lo;
+  __device__ __forceinline__ Pair first() const { return pair(hi.x, lo.x); }
+  __device__ __forceinline__ Pair second() const { return pair(hi.y, lo.y); }
+};
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+// hi + lo = a + b, exactly
+__device__ __forceinline__ Pair2 two_sum(float2 a, float2 b) {
+  const float2 s = add2(a, b), bb = sub2(s, a);
+  return Pair2{s, add2(sub2(a, sub2(s, bb)), sub2(b, bb))};
+}
+// max(p - t q, 0), t = th + tl
+__device__ __forceinline__ Pair2 rest(float2 p, float2 q, Pair t) {
+  const float2 minus = make_float2(-t.h, -t.h), h = mul2(minus, q);  // -th q = h + e
+  const float2 e = fma2(make_float2(-t.l, -t.l), q, fma2(minus, q, make_float2(-h.x, -h.y)));
+  Pair2 d = two_sum(p, h);
+  d.lo = add2(d.lo, e);
+  const float2 s = add2(d.hi, d.lo);
+  if (!(s.x > 0.0f)) d.hi.x = d.lo.x = 0.0f;
+  if (!(s.y > 0.0f)) d.hi.y = d.lo.y = 0.0f;
+  return d;
+}
+
+// Where the walk stands.
+struct Stand {
+  int cur;        // the node
+  int last;       // its latest child tried, or itself
+  Pair t, C;
+};
+
+// The rows of the node where it stands, and what is taken off them.
+struct Rows {
+  const void *p, *q;  // q null: t is 0 or there is none
+  Pair t;
+};
+
+// Whether some child of `cur` up to node `end` - 1 has token y.  All lanes ask alike.
+__device__ __forceinline__ bool among_children(const Shared &sm, int cur, int end, int32_t y, int lane) {
+  for (int b = cur + 1; b < end; b += 32) {
+    const int i = b + lane;
+    if (__any_sync(0xffffffffu, i < end && sm.parent[i] == cur && sm.token[i] == y)) return true;
+  }
+  return false;
+}
+
+// A chunk's sum, by a warp.  `nodes`: the draft's, where tokens tried are left out, else 0.
+template <bool BF16>
+__device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int chunk, int vocab, int cur, int nodes,
+                                            int lane) {
+  constexpr int N = BF16 ? 8 : 4, kSteps = kChunk / (32 * N), kAtOnce = 4;
+  Pair2 acc{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int s0 = 0; s0 < kSteps; s0 += kAtOnce) {
+    Probs<BF16, N> p[kAtOnce], q[kAtOnce];
+    const int y0 = chunk * kChunk + 32 * N * s0 + N * lane;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      p[k].load(r.p, y0 + 32 * N * k, vocab);
+      if (r.q != nullptr) q[k].load(r.q, y0 + 32 * N * k, vocab);
+    }
+    for (int b = cur + 1; b < nodes; b += 32) {
+      const int i = b + lane;
+      const int32_t at = i < nodes && sm.parent[i] == cur && sm.token[i] >= 0
+                             ? sm.token[i] - (chunk * kChunk + 32 * N * s0) : -1;
+      for (uint32_t m = __ballot_sync(0xffffffffu, at >= 0 && at < 32 * N * kAtOnce); m != 0; m &= m - 1) {
+        const int x = __shfl_sync(0xffffffffu, at, __ffs(int(m)) - 1);  // of step x / (32 N), lane (x / N) % 32
+        if ((x / N) % 32 == lane) {
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (k == x / (32 * N) && w == (BF16 ? x % N / 2 : x % N))
+                p[k].w[w] &= BF16 ? (x & 1 ? 0x0000ffffu : 0xffff0000u) : 0u;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        Pair2 w{p[k].two(i), make_float2(0.0f, 0.0f)};
+        if (r.q != nullptr) w = rest(w.hi, q[k].two(i), r.t);
+        const Pair2 s = two_sum(acc.hi, w.hi);
+        acc.hi = s.hi;
+        acc.lo = add2(acc.lo, r.q != nullptr ? add2(s.lo, w.lo) : s.lo);
+      }
+  }
+  Pair v = acc.first() + acc.second();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = v + Pair{__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
   return v;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) verify_kernel(Verify v, WsHeader *__restrict__ hdr) {
-  __shared__ double red[kThreads / 32];
-  __shared__ int16_t parent[DS4X_TREE_MAX_NODES];
-  __shared__ int found;
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader *__restrict__ hdr) {
+  __shared__ Shared sm;
+  // (waited for below: no block writes to one that has not begun)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank(), blocks = cluster_size();
+  const int s = int(blockIdx.x / blocks);
   const int64_t from = max(0, __ldcg(v.cu + s)), to = min(v.n_tokens, int64_t(__ldcg(v.cu + s + 1)));
   const int64_t all = max(int64_t(0), to - from);
-  const bool many = all > DS4X_TREE_MAX_NODES;
+  const bool many = all > kMaxNodes;
   const int nodes = many ? 0 : int(all);
+  const int size = BF16 ? 2 : 4;
+  const auto row_of = [&](const void *m, int64_t stride, int node) {
+    return static_cast<const void *>(static_cast<const uint8_t *>(m) + (from + node) * stride * size);
+  };
+  const auto one = [&](const void *row, int y) {
+    Probs<BF16, 2> p;
+    if constexpr (BF16)
+      p.w[0] = __ldcg(static_cast<const uint16_t *>(row) + y);
+    else
+      p.w[0] = __ldcg(static_cast<const uint32_t *>(row) + y);
+    return clean(__uint_as_float(BF16 ? p.w[0] << 16 : p.w[0]));
+  };
   bool odd = many;
-  for (int64_t i = tid; i < all; i += kThreads) {
-    v.path[from + i] = v.out[from + i] = -1;
-    if (many) continue;
-    const int32_t p = __ldcg(v.parent + from + i);
-    const bool bad = p < -1 || p >= i;
+  for (int i = tid; i < nodes; i += kThreads) {
+    const int32_t up = __ldcg(v.parent + from + i);
+    int32_t x = __ldcg(v.tokens + from + i);
+    sm.u[i] = __ldcg(v.u + from + i);
+    const bool bad = up < -1 || up >= i;
+    const int at = bad ? -1 : up;
     odd = odd || bad;
-    parent[i] = int16_t(bad ? -1 : p);
+    if (x < 0 || x >= v.vocab) x = -1;
+    sm.parent[i] = int16_t(at);
+    sm.token[i] = x;
+    if (at >= 0 && x >= 0) {
+      sm.p[i] = one(row_of(v.target, v.target_stride, at), x);
+      if (v.draft != nullptr) sm.q[i] = one(row_of(v.draft, v.draft_stride, at), x);
+    } else {
+      sm.p[i] = sm.q[i] = 0.0f;
+    }
   }
-  if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  if (odd && rank == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   __syncthreads();
-  if (nodes == 0) {
-    if (tid == 0) v.n_path[s] = 0;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (nodes == 0) {  // (all blocks of the cluster leave here)
+    for (int64_t i = rank * kThreads + tid; i < all; i += blocks * kThreads) v.path[from + i] = v.out[from + i] = -1;
+    if (rank == 0 && tid == 0) v.n_path[s] = 0;
     return;
   }
-  // the walk, the same in every thread
-  int cur = 0, count = 1, last = 0;  // last: the latest child of cur that was tried (0: none)
-  double t = 0.0, C = 1.0;
-  if (tid == 0) v.path[from] = 0;
-  const auto p_at = [&](int64_t y) { return prob<BF16>(v.target, (from + cur) * v.target_stride + y); };
-  const auto q_at = [&](int64_t y) { return prob<BF16>(v.draft, (from + cur) * v.draft_stride + y); };
-  const auto tried = [&](int32_t y) {  // without the draft's probabilities
-    for (int j = cur + 1; j <= last; ++j)
-      if (parent[j] == cur && __ldcg(v.tokens + from + j) == y) return true;
-    return false;
+
+  // the block's chunks
+  const int chunks = (v.vocab + kChunk - 1) / kChunk, per = (chunks + int(blocks) - 1) / int(blocks);
+  const int c0 = min(chunks, int(rank) * per), c1 = min(chunks, c0 + per);
+  int passes = 0;
+  // sums of what is left at the node, by chunk and by block: the total, and what this block's chunks come behind
+  Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}};
+  const auto pass = [&](const Stand &at, Pair &before) {
+    rows.p = row_of(v.target, v.target_stride, at.cur);
+    rows.q = v.draft != nullptr && some(at.t) ? row_of(v.draft, v.draft_stride, at.cur) : nullptr;
+    rows.t = at.t;
+    Pair mine{0.0f, 0.0f};
+    for (int c = c0 + warp; c < c1; c += kWarps) {
+      const Pair sum = chunk_sum<BF16>(sm, rows, c, v.vocab, at.cur, v.draft == nullptr ? at.last + 1 : 0, lane);
+      if (lane == 0) sm.sums[c - c0] = sum;
+      mine = mine + sum;
+    }
+    if (lane == 0) sm.red[warp] = mine;
+    __syncthreads();
+    Pair *total = sm.total[passes++ & 1];
+    if (tid < int(blocks)) {
+      Pair sum = sm.red[0];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) sum = sum + sm.red[k];
+      store_remote(&total[rank], uint32_t(tid), sum);
+    }
+    cluster_barrier();
+    Pair sum{0.0f, 0.0f};
+    for (int k = 0; k < int(blocks); ++k) {
+      if (k == int(rank)) before = sum;
+      sum = sum + total[k];
+    }
+    return sum;
   };
-  const auto weight = [&](int32_t y) {
-    if (v.draft != nullptr) return fmax(double(p_at(y)) - t * double(q_at(y)), 0.0);
-    return tried(y) ? 0.0 : double(p_at(y));
-  };
-  for (int j = 1; j < nodes; ++j) {
-    if (parent[j] != cur) continue;
-    const int32_t x = __ldcg(v.tokens + from + j);
-    const bool in = x >= 0 && x < v.vocab;
-    if (!in && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-    const double w = in ? weight(x) : 0.0, q = v.draft == nullptr ? 1.0 : in ? double(q_at(x)) : 0.0;
-    if (double(__ldcg(v.u + from + j)) * q * C < w) {
-      if (tid == 0) {
-        v.path[from + count] = j;
-        v.out[from + count - 1] = x;
-      }
-      cur = j;
+
+  // ---- the walk, the same in every warp -------------------------------------------------
+  Stand at{0, 0, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
+  int count = 1;
+  bool summed = false;  // the sums are of what is left now
+  Pair left{0.0f, 0.0f}, before{0.0f, 0.0f};
+  if (tid == 0) sm.path[0] = 0;
+  for (;;) {
+    int j = -1;  // the next child
+    for (int b = at.last + 1; b < nodes && j < 0; b += 32) {
+      const int i = b + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, i < nodes && sm.parent[i] == at.cur);
+      if (m != 0) j = b + __ffs(int(m)) - 1;
+    }
+    if (j < 0) break;
+    const int32_t x = sm.token[j];
+    if (x < 0 && rank == 0 && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+    Pair w{sm.p[j], 0.0f}, bar = sm.u[j] * at.C;
+    if (v.draft != nullptr) {
+      const float q = sm.q[j];
+      // (not max(.., 0): what it is compared with is not below 0)
+      if (some(at.t)) w = w + -(q * at.t);
+      bar = q * bar;
+    } else if (at.last > at.cur && among_children(sm, at.cur, j, x, lane)) {
+      w.h = 0.0f;
+    }
+    if (w > bar) {
+      if (tid == 0) sm.path[count] = int16_t(j);
       ++count;
-      last = 0;
-      t = 0.0;
-      C = 1.0;
+      at = Stand{j, j, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
+      summed = false;
       continue;
     }
-    last = j;
+    at.last = j;
     if (v.draft != nullptr) {
-      t += C;
-      double sum = 0.0;
-      for (int y = tid; y < v.vocab; y += kThreads) sum += weight(y);
-      C = block_sum(sum, red);
+      at.t = at.t + at.C;
+      at.C = left = pass(at, before);
+      summed = true;
     } else {
-      C -= w;
+      at.C = at.C + -w;
     }
   }
-  // the last token
-  double sum = 0.0;
-  for (int y = tid; y < v.vocab; y += kThreads) sum += weight(y);
-  const double total = block_sum(sum, red), want = double(__ldcg(v.u + from)) * total;
-  double before = 0.0;
-  if (tid == 0) found = -1;
-  int latest = -1;  // the last token with a weight
-  for (int y0 = 0; y0 < v.vocab; y0 += kThreads) {
-    const int y = y0 + tid;
-    const double w = y < v.vocab ? weight(y) : 0.0;
-    double incl = w;
+  if (!summed) left = pass(at, before);
+
+  // ---- the last token ---------------------------------------------------------------------
+  const Pair want = sm.u[0] * left;
+  // the block in whose slice it lies: the first whose sum passes it (by rounding none: the last with any)
+  int holder = -1;
+  {
+    const Pair *total = sm.total[(passes - 1) & 1];
+    Pair sum{0.0f, 0.0f};
+    int last = -1;
+    for (int k = 0; k < int(blocks); ++k) {
+      sum = sum + total[k];
+      if (some(total[k])) last = k;
+      if (holder < 0 && some(total[k]) && sum > want) holder = k;
+    }
+    if (holder < 0) holder = last;
+  }
+  if (rank == 0) {
+    __syncthreads();  // `path`
+    for (int i = tid; i < nodes; i += kThreads) {
+      v.path[from + i] = i < count ? sm.path[i] : -1;
+      if (i != count - 1) v.out[from + i] = i < count ? sm.token[sm.path[i + 1]] : -1;
+    }
+    if (tid == 0) {
+      v.n_path[s] = count;
+      if (holder < 0) {
+        v.out[from + count - 1] = -1;
+        atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      }
+    }
+  }
+  if (holder != int(rank)) return;
+  if (warp == 0) {
+    // the chunk, likewise
+    Pair base = before, pick_base{0.0f, 0.0f}, last_base{0.0f, 0.0f};
+    int pick = -1, last = -1;
+    for (int b = 0; b < c1 - c0 && pick < 0; b += 32) {
+      const Pair mine = b + lane < c1 - c0 ? sm.sums[b + lane] : Pair{0.0f, 0.0f};
+      const Pair upto = base + warp_scan(mine, lane);
+      const uint32_t any = __ballot_sync(0xffffffffu, some(mine));
+      const uint32_t over = __ballot_sync(0xffffffffu, some(mine) && upto > want);
+      const int k = over != 0 ? __ffs(int(over)) - 1 : any != 0 ? 31 - __clz(any) : 0;
+      const Pair prev = shfl(upto, max(k - 1, 0)), from_k = k > 0 ? prev : base;
+      if (over != 0) pick = b + k, pick_base = from_k;
+      if (any != 0) last = b + k, last_base = from_k;
+      base = shfl(upto, 31);
+    }
+    if (lane == 0) {
+      sm.chunk = c0 + (pick >= 0 ? pick : last);
+      sm.base = pick >= 0 ? pick_base : last_base;
+      sm.found = INT32_MAX;
+    }
+  }
+  __syncthreads();
+  // its tokens, four a lane
+  const int y0 = sm.chunk * kChunk + 4 * tid;
+  Probs<BF16, 4> p, q;
+  p.load(rows.p, y0, v.vocab);
+  if (rows.q != nullptr) q.load(rows.q, y0, v.vocab);
+  Pair w[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = incl;
-    __syncthreads();
-    double base = before, whole = before;
-    for (int k = 0; k < kThreads / 32; ++k) {
-      if (k < warp) base += red[k];
-      whole += red[k];
-    }
-    if (w > 0.0) {
-      latest = y;
-      if (base + incl > want) atomicCAS(&found, -1, y), atomicMin(&found, y);
-    }
-    __syncthreads();
-    if (found >= 0) break;
-    before = whole;
+  for (int i = 0; i < 2; ++i) {
+    Pair2 d{p.two(i), make_float2(0.0f, 0.0f)};
+    if (rows.q != nullptr) d = rest(d.hi, q.two(i), rows.t);
+    w[2 * i] = d.first();
+    w[2 * i + 1] = d.second();
   }
-  if (found < 0) {  // (rounding, or no weight at all)
-    __syncthreads();
-    atomicMax(&found, latest);
-    __syncthreads();
+  if (v.draft == nullptr)
+    for (int i = at.cur + 1; i <= at.last; ++i)
+      if (sm.parent[i] == at.cur && (sm.token[i] & ~3) == y0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k == (sm.token[i] & 3)) w[k] = Pair{0.0f, 0.0f};
+  const Pair upto = warp_scan((w[0] + w[1]) + (w[2] + w[3]), lane);
+  if (lane == 31) sm.red[warp] = upto;
+  const Pair prev = shfl_up(upto, 1);
+  __syncthreads();
+  Pair sum = sm.base;
+  for (int k = 0; k < warp; ++k) sum = sum + sm.red[k];
+  if (lane > 0) sum = sum + prev;
+  int first = INT32_MAX, latest = -1;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sum = sum + w[k];
+    if (some(w[k])) {
+      latest = y0 + k;
+      if (sum > want) first = min(first, y0 + k);
+    }
   }
-  if (tid == 0) {
-    v.out[from + count - 1] = found;
-    v.n_path[s] = count;
-    if (found < 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  first = __reduce_min_sync(0xffffffffu, first);
+  if (lane == 0 && first != INT32_MAX) atomicMin(&sm.found, first);
+  __syncthreads();
+  if (sm.found == INT32_MAX) {  // (by rounding)
+    __syncthreads();
+    if (tid == 0) sm.chunk = -1;
+    __syncthreads();
+    atomicMax(&sm.chunk, latest);
+    __syncthreads();
+    if (tid == 0) sm.found = sm.chunk;
   }
+  if (tid == 0) v.out[from + count - 1] = sm.found;
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t stream) {
-  return launch_pdl(bf16 ? verify_kernel<true> : verify_kernel<false>, unsigned(v.n_seqs), unsigned(kThreads), 0, stream,
-                    v, static_cast<WsHeader *>(ws));
+  static std::atomic<uint64_t> set[2];
+  auto *kernel = bf16 ? verify_kernel<true> : verify_kernel<false>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(set[bf16].load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    set[bf16].fetch_or(bit, std::memory_order_acq_rel);
+  }
+  // as many blocks a sequence as are resident at once, and have a chunk for each warp
+  const int chunks = (v.vocab + kChunk - 1) / kChunk;
+  int blocks = 1;
+  while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && 2 * blocks * kWarps <= chunks)
+    blocks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(v.n_seqs) * unsigned(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(blocks);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, v, static_cast<WsHeader *>(ws));
 }
 
 }  // namespace ds4x
