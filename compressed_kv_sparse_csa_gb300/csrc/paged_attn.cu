@@ -172,24 +172,25 @@ struct Plan {
 
 struct Args {
   PagedAttn a;
-  const Plan *plan;   // several tokens a unit (n_heads columns each), or null
+  const Plan *plan;   // the units' tokens and rows, where they are several a unit or a tree's; or null
+  bool multi;         // several tokens a unit (n_heads columns each)
   int32_t groups;     // head groups a token
   int32_t group;      // a unit's columns at most: heads a group (the last may have fewer), or tokens x heads
   int32_t per_head;   // 2^16 / n_heads, rounded up
   int32_t n_cols;     // `group` rounded up to 16: the products' N
   uint64_t per_grid;  // 2^64 / CTAs, rounded up
   int32_t few;        // at most kFewUnits units
-  __device__ __forceinline__ bool packed() const { return plan != nullptr; }
-  __device__ __forceinline__ bool tree() const { return a.parent != nullptr; }
+  __device__ __forceinline__ bool packed() const { return multi; }
+  __device__ __forceinline__ bool planned() const { return plan != nullptr; }
 };
 // The same where the kernel is compiled for one form: the others' units cost it nothing.
-// A tree's units are packed ones, of a token at least; heads beyond 64 in groups.
-enum class Form { kSingle, kPacked, kTree };
-template <Form F>
+// P: several tokens a unit.  T: trees.
+template <bool P, bool T>
 struct ArgsFor : Args {
   ArgsFor(const Args &g) : Args(g) {}
-  static __device__ __forceinline__ constexpr bool packed() { return F != Form::kSingle; }
-  static __device__ __forceinline__ constexpr bool tree() { return F == Form::kTree; }
+  static __device__ __forceinline__ constexpr bool packed() { return P; }
+  static __device__ __forceinline__ constexpr bool tree() { return T; }
+  static __device__ __forceinline__ constexpr bool planned() { return P || T; }
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -284,12 +285,6 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
-// Which of the plan's entries a packed unit is (a tree's may be one group of its heads).
-template <class A>
-__device__ __forceinline__ int plan_unit(const A &g, int unit) {
-  return g.tree() && g.groups > 1 ? unit / g.groups : unit;
-}
-
 // A unit's query vectors ("columns"): heads h0 .. of token t0, or, packed, all heads
 // of count tokens from t0, head by head.
 struct Columns {
@@ -297,11 +292,10 @@ struct Columns {
   template <class A>
   __device__ __forceinline__ Columns(const A &g, int unit) {
     if (g.packed()) {
-      const int group = g.tree() && g.groups > 1 ? unit % g.groups : 0;
-      const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[plan_unit(g, unit)]));
+      const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[unit]));
       t0 = p.x;
-      h0 = group * g.group;
-      n = g.tree() && g.groups > 1 ? min(g.group, g.a.n_heads - h0) : p.y * g.a.n_heads;
+      h0 = 0;
+      n = p.y * g.a.n_heads;
     } else {
       t0 = unit / g.groups;
       h0 = (unit % g.groups) * g.group;
@@ -336,8 +330,8 @@ __device__ __forceinline__ bool past_table(const PagedAttn &a, int t) {
 }
 template <class A>
 __device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
-  if (!g.packed()) return token_rows(g.a, unit / g.groups);
-  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[plan_unit(g, unit)]) + 1);
+  if (!g.planned()) return token_rows(g.a, unit / g.groups);
+  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[g.packed() ? unit : unit / g.groups]) + 1);
   return Rows{p.x, p.y};
 }
 // The rows of node t - from of a tree behind row row0 of its sequence, from the first
@@ -452,10 +446,10 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // the count of valid ones is on its way with their rows)
   const int per = (a.n_tokens + kThreads - 1) / kThreads;
   const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
-  auto rows_of = [&](int t) { return g.packed() ? unit_rows(g, t * (g.tree() ? g.groups : 1)) : token_rows(a, t); };
+  auto rows_of = [&](int t) { return g.planned() ? unit_rows(g, g.packed() ? t : t * g.groups) : token_rows(a, t); };
   const Rows first_rows = t0 < t1 ? rows_of(t0) : Rows{0, 0};
   // tokens behind are padding
-  const int valid = g.packed() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
+  const int valid = g.planned() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
   auto tiles_of = [&](int t) { return t < valid ? rows_tiles(rows_of(t).n) : 0; };
   const int first = t0 < min(t1, valid) ? rows_tiles(first_rows.n) : 0;
   long long mine = first;
@@ -533,7 +527,7 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // (padding has no parts)
   if (blockIdx.x == 0 && g.few && tid < kFewUnits && tid / g.groups >= valid) parts->span[tid] = make_int2(0, 0);
   // a range past what the table can place
-  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.packed())
+  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.planned())
     for (int t = t0; t < min(t1, valid); ++t)
       if (past_table(a, t)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   __syncthreads();
@@ -549,7 +543,7 @@ __device__ __forceinline__ void prefetch_queries(const A &g, int unit) {
   const auto fetch = [](const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
   };
-  const int heads = A::packed() && !(A::tree() && g.groups > 1) ? g.a.n_heads : col.n;
+  const int heads = A::packed() ? g.a.n_heads : col.n;
   for (int c = 0; c < col.n; c += heads)
     fetch(g.a.q + col.at(g, c, g.a.q_stride, kDim), uint32_t(heads) * kDim * 2);
 }
@@ -625,13 +619,13 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
   Walk w;
   w.begin(sm, total);
   for (;;) {
-    const int t = g.packed() ? __ldcg(&g.plan->unit[plan_unit(g, w.unit)].t0) : w.unit / g.groups;
+    const int t = g.packed() ? __ldcg(&g.plan->unit[w.unit].t0) : w.unit / g.groups;
     if (lane == 0 && w.i0 > 0 && w.off == w.from) prefetch_queries(g, w.unit);
-    int count = 0;
+    int count = 1;
     bool lines = false;  // the unit's are there
     int64_t row0 = 0;
     Sight sight{0, 0};
-    if (A::tree()) count = __ldcg(&g.plan->unit[plan_unit(g, w.unit)].count);
+    if (A::tree() && A::packed()) count = __ldcg(&g.plan->unit[w.unit].count);
     bool fresh = true;
     // a list's entries are on their way a tile ahead
     int entry[2] = {0, 0};
@@ -669,10 +663,14 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
         // (before the tree's first row no line is looked at)
         unsigned long long bits = lane < count ? tree_sees(sm.line[lane], sight, first) : 0;
         if (w.n == 0) bits = 0;
-        unsigned long long all = ~warp_or(lane < count ? ~bits : 0), any = warp_or(bits);
-        if (i >= kAhead) wait_bar(sm, &sm.lfree[i % kAhead], (i / kAhead - 1) & 1, hdr);
-        if (lane < kPackTokens) sm.sees[i % (2 * kAhead)][lane] = bits;
-        if (lane == 0) sm.sees[i % (2 * kAhead)][kPackTokens] = all;
+        // a row that none of the unit's tokens sees is not there
+        const unsigned long long any = A::packed() ? warp_or(bits) : __shfl_sync(0xffffffffu, bits, 0);
+        if (A::packed()) {
+          const unsigned long long all = ~warp_or(lane < count ? ~bits : 0);
+          if (i >= kAhead) wait_bar(sm, &sm.lfree[i % kAhead], (i / kAhead - 1) & 1, hdr);
+          if (lane < kPackTokens) sm.sees[i % (2 * kAhead)][lane] = bits;
+          if (lane == 0) sm.sees[i % (2 * kAhead)][kPackTokens] = all;
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (!(any >> (lane + 32 * k) & 1)) row[k] = -1;
@@ -1441,8 +1439,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
   if (tid == 0) plan->n_units = base;
 }
 
-template <Form F>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<F> g, Parts *__restrict__ parts,
+template <bool P, bool T>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P, T> g, Parts *__restrict__ parts,
                                                                  WsHeader *__restrict__ hdr) {
   // (no static shared memory: the dynamic begins at the window's start, as aligned as Smem asks)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1781,11 +1779,12 @@ __global__ void __launch_bounds__(kShortThreads) paged_combine_short_kernel(Args
 size_t paged_attn_ws_bytes() { return kWsHeaderBytes + sizeof(Parts) + sizeof(Plan); }
 
 cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream) {
-  static std::atomic<uint64_t> smem_set[3];
+  static std::atomic<uint64_t> smem_set[4];
   const int smem = int(sizeof(Smem));
-  cudaError_t e = set_max_smem_once(paged_attn_kernel<Form::kSingle>, smem, smem_set[0]);
-  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<Form::kPacked>, smem, smem_set[1]);
-  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<Form::kTree>, smem, smem_set[2]);
+  cudaError_t e = set_max_smem_once(paged_attn_kernel<false, false>, smem, smem_set[0]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<true, false>, smem, smem_set[1]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<false, true>, smem, smem_set[2]);
+  if (e == cudaSuccess) e = set_max_smem_once(paged_attn_kernel<true, true>, smem, smem_set[3]);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
@@ -1806,27 +1805,26 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   // 1 sequence x 2 tokens x 20 heads x 700 rows 17.1 / 12.2, 8 x 2 x 16 x 2000
   // 22.4 / 23.0, 24 x 5 x 20 x 4500 66 / 130, 1 x 512 x 16 x 4096 124 / 420.
   const bool tree = a.parent != nullptr;
-  const int fits = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
-  const int pack = tree && fits < 1 ? 1 : fits;
-  const bool packed = tree || (a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas);
-  Args g{a, packed ? plan : nullptr, groups, 0, 0, 0, 0, 0};
+  const int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
+  const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas;
+  Args g{a, packed || tree ? plan : nullptr, packed, groups, 0, 0, 0, 0, 0};
   g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;
-  g.group = packed && groups == 1 ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
-  g.per_head = groups == 1 ? 65536 / a.n_heads + 1 : 0;  // (of heads in groups, a unit's are one token's)
+  g.group = packed ? pack * a.n_heads : (a.n_heads + g.groups - 1) / g.groups;
+  g.per_head = 65536 / a.n_heads + 1;
   g.n_cols = (g.group + 15) / 16 * 16;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
-  if (packed) {
-    e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
+  if (packed || tree) {
+    e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, packed ? pack : 1, plan, hdr);
     if (e != cudaSuccess) return e;
   }
-  const auto launch = [&](auto form) {
-    constexpr Form F = decltype(form)::value;
-    return launch_pdl(paged_attn_kernel<F>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream, ArgsFor<F>(g),
-                      parts, hdr);
+  const auto launch = [&](auto p, auto t) {
+    constexpr bool P = decltype(p)::value, T = decltype(t)::value;
+    return launch_pdl(paged_attn_kernel<P, T>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
+                      ArgsFor<P, T>(g), parts, hdr);
   };
-  e = tree     ? launch(std::integral_constant<Form, Form::kTree>{})
-      : packed ? launch(std::integral_constant<Form, Form::kPacked>{})
-               : launch(std::integral_constant<Form, Form::kSingle>{});
+  using Yes = std::true_type;
+  using No = std::false_type;
+  e = packed ? (tree ? launch(Yes{}, Yes{}) : launch(Yes{}, No{})) : (tree ? launch(No{}, Yes{}) : launch(No{}, No{}));
   if (e != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;  // nothing is split
   if (g.few && (rows + kTile - 1) / kTile <= kShortParts)
