@@ -95,8 +95,9 @@ constexpr int kWWarp0 = 4, kWWarps = 8, kXWarp0 = 12, kXWarps = 8;
 constexpr int kXThreads = 32 * kXWarps;
 constexpr int kThreads = 32 * (kXWarp0 + kXWarps);  // 640
 // registers a thread: at launch, then by role
-constexpr int kRegs = 96, kRegsLM = 64, kRegsW = 96, kRegsX = 104;
-static_assert(4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsX <= kThreads / 32 * kRegs, "register split");
+constexpr int kRegs = 96, kRegsLM = 64, kRegsW = 96, kRegsX = 104, kRegsXPacked = 112;
+static_assert(kRegsX <= kRegsXPacked && 4 * kRegsLM + kWWarps * kRegsW + kXWarps * kRegsXPacked <= kThreads / 32 * kRegs,
+              "register split");
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
 constexpr int kPackTokens = 8;     // tokens a unit, at most
@@ -117,6 +118,10 @@ enum { kBarX = 1, kBarEnd = 2 };  // named barriers
 struct __align__(16) Found {
   const uint8_t *codes;
   int32_t tail, scales;
+};
+
+struct __align__(16) TreeAt {
+  int32_t s, from, row0, count;
 };
 
 struct __align__(1024) Smem {
@@ -148,6 +153,7 @@ struct __align__(1024) Smem {
   unsigned long long sees[2 * kAhead][kPackTokens + 1];
   unsigned long long line[kPackTokens][kTreeWords + 1];  // a token's node and its ancestors (L's)
   int16_t parent[DS4X_TREE_MAX_NODES];                   // the sequence's (L's)
+  TreeAt at0;                                            // unit0's
 };
 static_assert(sizeof(Smem) <= 232448, "shared-memory budget");
 
@@ -165,14 +171,25 @@ struct Parts {
 struct __align__(16) Pack {
   int32_t t0, count, r0, n;
 };
+// Trees: the sequence of an entry, its first token, the draft's first row (as far as the
+// table goes), and the entry's tokens; and a CTA's run: where it begins (tile `off` of unit
+// `unit`, that unit's rows r0 .. r0 + n - 1 and its entry) and its tiles.
+struct __align__(16) Run {
+  int32_t unit, off, r0, n;
+  TreeAt at;
+  int32_t total, pad[3];
+};
 struct Plan {
   int32_t n_units, pad[3];
   Pack unit[DS4X_PAGED_MAX_TOKENS];
+  TreeAt tree[DS4X_PAGED_MAX_TOKENS];
+  int64_t tiles[DS4X_PAGED_MAX_TOKENS];  // a tree's entries': the tiles before it, of one head group
+  Run run[kMaxCtas];
 };
 
 struct Args {
   PagedAttn a;
-  const Plan *plan;   // the units' tokens and rows, where they are several a unit or a tree's; or null
+  Plan *plan;         // the units' tokens and rows, where they are several a unit or a tree's; or null
   bool multi;         // several tokens a unit (n_heads columns each)
   int32_t groups;     // head groups a token
   int32_t group;      // a unit's columns at most: heads a group (the last may have fewer), or tokens x heads
@@ -328,12 +345,6 @@ __device__ __forceinline__ bool past_table(const PagedAttn &a, int t) {
   const int64_t e = __ldcg(a.row_end + t);
   return e > (int64_t(a.c.seq_pages) << a.c.page_log2) && (a.row_begin == nullptr || __ldcg(a.row_begin + t) < e);
 }
-template <class A>
-__device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
-  if (!g.planned()) return token_rows(g.a, unit / g.groups);
-  const int2 p = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[g.packed() ? unit : unit / g.groups]) + 1);
-  return Rows{p.x, p.y};
-}
 // The rows of node t - from of a tree behind row row0 of its sequence, from the first
 // that it may see to its own; `odd`: some lie where the table does not go, or the node
 // has no place (then it sees nothing).
@@ -347,6 +358,17 @@ __device__ __forceinline__ Rows tree_rows(const PagedAttn &a, int t, int from, i
   const int64_t e = min(room, min(row0, room) + (t - from) + 1);
   if (row0 > room - (t - from) - 1) *odd = true;
   return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
+}
+// A planned unit's entry: its own, or, of a token in head groups, the token's.
+template <class A>
+__device__ __forceinline__ int plan_entry(const A &g, int unit) {
+  return g.packed() ? unit : unit / g.groups;
+}
+template <class A>
+__device__ __forceinline__ Rows unit_rows(const A &g, int unit) {
+  if (!g.planned()) return token_rows(g.a, unit / g.groups);
+  const int2 r = __ldcg(reinterpret_cast<const int2 *>(&g.plan->unit[plan_entry(g, unit)]) + 1);
+  return Rows{r.x, r.y};
 }
 // A token without a row still has a tile (of rows that are not there): it writes the zeros.
 __device__ __forceinline__ int rows_tiles(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
@@ -446,10 +468,10 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // the count of valid ones is on its way with their rows)
   const int per = (a.n_tokens + kThreads - 1) / kThreads;
   const int t0 = min(a.n_tokens, tid * per), t1 = min(a.n_tokens, t0 + per);
-  auto rows_of = [&](int t) { return g.planned() ? unit_rows(g, g.packed() ? t : t * g.groups) : token_rows(a, t); };
+  auto rows_of = [&](int t) { return g.packed() ? unit_rows(g, t) : token_rows(a, t); };
   const Rows first_rows = t0 < t1 ? rows_of(t0) : Rows{0, 0};
   // tokens behind are padding
-  const int valid = g.planned() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
+  const int valid = g.packed() ? __ldcg(&g.plan->n_units) : __ldcg(a.c.cu + a.c.n_seqs);
   auto tiles_of = [&](int t) { return t < valid ? rows_tiles(rows_of(t).n) : 0; };
   const int first = t0 < min(t1, valid) ? rows_tiles(first_rows.n) : 0;
   long long mine = first;
@@ -527,7 +549,7 @@ __device__ void find_cuts(const A &g, Smem &sm, Parts *parts, WsHeader *hdr) {
   // (padding has no parts)
   if (blockIdx.x == 0 && g.few && tid < kFewUnits && tid / g.groups >= valid) parts->span[tid] = make_int2(0, 0);
   // a range past what the table can place
-  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.planned())
+  if (blockIdx.x == gridDim.x - 1 && a.idx == nullptr && !g.packed())
     for (int t = t0; t < min(t1, valid); ++t)
       if (past_table(a, t)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
   __syncthreads();
@@ -621,11 +643,14 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
   for (;;) {
     const int t = g.packed() ? __ldcg(&g.plan->unit[w.unit].t0) : w.unit / g.groups;
     if (lane == 0 && w.i0 > 0 && w.off == w.from) prefetch_queries(g, w.unit);
-    int count = 1;
     bool lines = false;  // the unit's are there
-    int64_t row0 = 0;
     Sight sight{0, 0};
-    if (A::tree() && A::packed()) count = __ldcg(&g.plan->unit[w.unit].count);
+    TreeAt at_unit = sm.at0;
+    if (A::tree() && w.i0 > 0) {
+      const int4 v = __ldcg(reinterpret_cast<const int4 *>(&g.plan->tree[plan_entry(g, w.unit)]));
+      at_unit = TreeAt{v.x, v.y, v.z, v.w};
+    }
+    const int count = at_unit.count;
     bool fresh = true;
     // a list's entries are on their way a tile ahead
     int entry[2] = {0, 0};
@@ -640,15 +665,17 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
       }
       if (a.idx != nullptr && i + 1 < w.i1) load_entries(g, t, pos + kTile, w.n, entry);
       if (fresh) {  // (looked up while the first entries are on their way)
-        if (sq.s < 0 || t >= sq.to) {
+        if (A::tree()) {
+          sq = PagedSeq{at_unit.s, at_unit.from, 0};
+          n_rows = INT32_MAX;
+        } else if (sq.s < 0 || t >= sq.to) {
           sq = paged_seq_of(a.c, t, lane);
           n_rows = INT32_MAX;
           if (a.idx != nullptr && sq.s >= 0)  // (below 0: no row)
             n_rows = int(max(int64_t(0), min(int64_t(INT32_MAX), int64_t(__ldcg(a.n_rows + sq.s)))));
         }
         if (A::tree() && sq.s >= 0) {
-          row0 = __ldcg(a.tree_row0 + sq.s);
-          sight.tree = int32_t(min(max(row0, int64_t(0)), int64_t(a.c.seq_pages) << a.c.page_log2));
+          sight.tree = at_unit.row0;
           if (a.row_begin != nullptr && lane < count)
             sight.lo = int32_t(min(int64_t(sight.tree), max(int64_t(0), int64_t(__ldcg(a.row_begin + t + lane)))));
         }
@@ -657,7 +684,7 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
       if (A::tree()) {
         const int64_t first = int64_t(w.r0) + pos - lane;
         if (!lines && sq.s >= 0 && first + kTile > sight.tree) {
-          tree_lines(a, sm, t, count, max(0, sq.from), row0, hdr);
+          tree_lines(a, sm, t, count, sq.from, sight.tree, hdr);
           lines = true;
         }
         // (before the tree's first row no line is looked at)
@@ -1037,15 +1064,19 @@ __device__ __forceinline__ void make_query(const A &g, Smem &sm, int unit, int x
   }
   const long long mine = col.at(g, 8 * xw + (A::packed() ? lane & 7 : 0), g.a.q_stride, kDim);
   const uint4 *q = reinterpret_cast<const uint4 *>(g.a.q + (A::packed() ? 0 : mine)) + lane;
-  uint4 qv[16];
+  // (packed trees: four columns at a time, or role X spills)
+  constexpr int kCols = A::packed() && A::tree() ? 4 : 8;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 8; k0 += kCols) {
+  uint4 qv[2 * kCols];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = 8 * xw + (i >> 1);
-    const long long at = A::packed() ? __shfl_sync(0xffffffffu, mine, i >> 1) / 8 + 32 * (i & 1) : 32 * i;
+  for (int i = 0; i < 2 * kCols; ++i) {
+    const int c = 8 * xw + k0 + (i >> 1);
+    const long long at = A::packed() ? __shfl_sync(0xffffffffu, mine, k0 + (i >> 1)) / 8 + 32 * (i & 1) : 32 * i;
     qv[i] = c < col.n ? __ldcg(q + at) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kCols; ++k) {
     // the column's largest exponent field e, and the scale that brings it to 14
     uint32_t m = 0;
 #pragma unroll
@@ -1057,7 +1088,7 @@ __device__ __forceinline__ void make_query(const A &g, Smem &sm, int unit, int x
     const int e = int(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) >> 7);
     const int c = max(-113, min(126, 14 + 127 - max(e, 1)));
     const float f = pow2f(c);
-    const int h = 8 * xw + k;
+    const int h = 8 * xw + k0 + k;
     // A column with NaN or infinity (all its logits are, so all its results) is computed
     // as zeros, so that rows that are not there stay out, and marked: out and lse are NaN.
     const bool odd = e == 255;
@@ -1076,6 +1107,7 @@ __device__ __forceinline__ void make_query(const A &g, Smem &sm, int unit, int x
         o[u] = odd ? 0u : half2_bits(__uint_as_float(w4[u] << 16) * f, __uint_as_float(w4[u] & 0xffff0000u) * f);
       sts16(smem_u32(sm.q) + (P >> 3) * 8192 + h * 128 + (((P & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
     }
+  }
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
@@ -1183,11 +1215,16 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
             if (j < kPackTokens && (row < sm.seen[j].x || row >= sm.seen[j].y)) d[k] = -INFINITY;
           }
         }
-        moves = false;  // a maximum is passed, or a first row sets one, however small
+        // a maximum is passed, or a first row sets one, however small
+        if (A::tree() && fresh == 0 && ~sm.sees[i % (2 * kAhead)][kPackTokens] == 0) {
+          moves = over > kLazy;  // (every row counts, for every column)
+        } else {
+          moves = false;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          moves = moves || d[k] > ((fresh >> (2 * (k >> 2) + (k & 1)) & 1) ? -INFINITY : kLazy);
-        moves = moves && busy;
+          for (int k = 0; k < 16; ++k)
+            moves = moves || d[k] > ((fresh >> (2 * (k >> 2) + (k & 1)) & 1) ? -INFINITY : kLazy);
+          moves = moves && busy;
+        }
       }
       if (named_bar_or(kBarX, kXThreads, moves)) {
         // some head's maximum moves: each head's maximum over the tile
@@ -1338,7 +1375,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
       }
     }
     if (xt == 0 && !whole && !more) parts->unit[part] = w.unit;
-    if (xt == 0 && g.few && w.from == 0 && !more) {
+    if (xt == 0 && g.few && !A::tree() && w.from == 0 && !more) {
       parts->span[w.unit] = make_int2(int(blockIdx.x), whole ? 1 : unit_parts(g, sm.cut0 + w.i0 - w.off + w.tiles, sm.all));
     }
     named_bar_sync(kBarX, kXThreads);
@@ -1397,11 +1434,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         count = min(pack, to - t);
         int rest = 0;  // tokens whose rows do not meet those from lo to hi
         int64_t lo = 0, hi = 0;
-        bool odd = false;
-        const int64_t row0 = a.parent != nullptr ? __ldcg(a.tree_row0 + s) : 0;
         for (int j = 0; j < count; ++j) {
-          if (a.parent == nullptr) odd = odd || past_table(a, t + j);
-          const Rows r = a.parent != nullptr ? tree_rows(a, t + j, from, row0, &odd) : token_rows(a, t + j);
+          if (past_table(a, t + j)) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+          const Rows r = token_rows(a, t + j);
           if (r.n == 0) continue;
           if (hi == 0) lo = r.r0, hi = r.r0 + r.n;
           else if (r.r0 > hi || r.r0 + r.n < lo) ++rest;
@@ -1409,9 +1444,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
         }
         // Rows between the tokens' ranges, which no token sees, must not be read (and
         // would be work for nothing): then each token is its own unit.
-        // (A tree's tokens all see its first row, or their windows end up to it.)
-        if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-        units = rest > 0 && a.parent == nullptr ? count : 1;
+        units = rest > 0 ? count : 1;
         u = Pack{t, count, int32_t(lo), int32_t(hi - lo)};
       }
     }
@@ -1437,6 +1470,185 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
     __syncthreads();
   }
   if (tid == 0) plan->n_units = base;
+}
+
+// The same for trees, and the cuts, so that the attention's CTAs find their runs made:
+// entries of up to `pack` neighbouring nodes of a sequence (a tree's tokens all see its
+// first row, or their windows end up to it), their tiles' prefix sums, then a thread a
+// cut.  One block.
+//
+// A unit's start and end hold up its CTA (queries in, output out, while no product runs)
+// for as long as some kUnitCost tiles take, so cuts count that many more tiles a unit,
+// where CTAs have several tiles each (24 drafts of 7 to 13 nodes x 20 heads: a CTA that had
+// four units took 100 us beside others' 66).
+constexpr int kUnitCost = 5, kCostTiles = 8;
+constexpr int kTreePlanSeqs = 2048, kTreePlanUnits = 2048;  // held in shared memory
+__global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn a, int pack, int groups, int ctas,
+                                                                       int few, Plan *__restrict__ plan,
+                                                                       Parts *__restrict__ parts,
+                                                                       WsHeader *__restrict__ hdr) {
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int32_t cus[kTreePlanSeqs + 1], sum_units[kWarps];
+  __shared__ int64_t sum_tiles[kWarps], first[kTreePlanUnits], cut_tile[kMaxCtas + 1];
+  __shared__ int2 rows[kTreePlanUnits];
+  __shared__ int32_t cut_unit[kMaxCtas + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_seqs = a.c.n_seqs;
+  const bool held = n_seqs <= kTreePlanSeqs;
+  if (held)
+    for (int i = tid; i <= n_seqs; i += kPlanThreads) cus[i] = __ldcg(a.c.cu + i);
+  const int valid = max(0, min(a.n_tokens, __ldcg(a.c.cu + n_seqs)));
+  __syncthreads();
+  auto cu = [&](int s) { return held ? cus[s] : __ldcg(a.c.cu + s); };
+  int base = 0;
+  int64_t tiles_base = 0;
+  for (int c0 = 0; c0 < valid; c0 += kPlanThreads) {
+    const int t = c0 + tid;
+    int unit = 0, tiles = 0;
+    Pack u{t, 1, 0, 0};
+    TreeAt at{-1, 0, 0, 1};
+    if (t < valid) {
+      int s = 0, n = n_seqs;  // the last sequence that begins at or before t
+      while (n > 1) {
+        const int half = n / 2;
+        if (cu(s + half) <= t) s += half, n -= half;
+        else n = half;
+      }
+      const int from = cu(s), to = min(valid, cu(s + 1));
+      if (!(0 <= from && from <= t && t < to)) {  // (cu is not what it should be: a unit without a row)
+        unit = 1;
+      } else if ((t - from) % pack == 0) {
+        const int count = min(pack, to - t);
+        const int64_t row0 = __ldcg(a.tree_row0 + s);
+        int64_t lo = 0, hi = 0;
+        bool odd = false;
+        for (int j = 0; j < count; ++j) {
+          const Rows r = tree_rows(a, t + j, from, row0, &odd);
+          if (r.n == 0) continue;
+          lo = hi == 0 ? r.r0 : min(lo, r.r0);
+          hi = max(hi, r.r0 + r.n);
+        }
+        if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+        unit = 1;
+        u = Pack{t, count, int32_t(lo), int32_t(hi - lo)};
+        at = TreeAt{s, from, int32_t(max(int64_t(0), min(row0, int64_t(a.c.seq_pages) << a.c.page_log2))), count};
+      }
+      if (unit) tiles = rows_tiles(u.n);
+    }
+    int incl = unit;
+    int64_t tincl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int64_t w = __shfl_up_sync(0xffffffffu, tincl, o);
+      if (lane >= o) incl += v, tincl += w;
+    }
+    if (lane == 31) sum_units[warp] = incl, sum_tiles[warp] = tincl;
+    __syncthreads();
+    int my = base + incl - unit;
+    int64_t before = tiles_base + tincl - tiles;
+#pragma unroll 8
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) my += sum_units[k], before += sum_tiles[k];
+      base += sum_units[k];
+      tiles_base += sum_tiles[k];
+    }
+    if (unit) {
+      plan->unit[my] = u;
+      plan->tree[my] = at;
+      plan->tiles[my] = before;
+      if (my < kTreePlanUnits) {
+        first[my] = before;
+        rows[my] = make_int2(u.r0, u.n);
+      }
+    }
+    __syncthreads();
+  }
+  // Entry p's units are p groups .. + groups - 1, of the same tiles each.
+  const int64_t all = tiles_base * groups;
+  const int units = base * groups;
+  const auto tiles_before = [&](int p) { return p >= base ? tiles_base : p < kTreePlanUnits ? first[p] : __ldcg(&plan->tiles[p]); };
+  const int cost = all >= int64_t(kCostTiles) * ctas ? kUnitCost : 0;
+  const int64_t total = all + int64_t(cost) * units;
+  // few tiles a CTA: cuts at whole multiples (see kOnes)
+  const int64_t even = (all + ctas - 1) / ctas;
+  const int64_t step = cost != 0 ? 0 : max(int64_t(all > kOnes ? 2 : 1), even);
+  // a cut so near to a unit's end moves there
+  const int64_t tol = cost != 0 ? min(int64_t(kSnap), total / ctas >> 2) : min(int64_t(kSnap), all / ctas >> 2);
+  for (int c = tid; c <= ctas; c += kPlanThreads) {
+    int64_t x = c >= ctas ? total : step != 0 ? min(c * step, total) : total / ctas * c + total % ctas * c / ctas;
+    int unit = units;
+    int64_t tile = all;
+    if (x < total) {
+      // the last entry that begins at or before x
+      int p = 0, n = base;
+      while (n > 1) {
+        const int half = n / 2, m = p + half;
+        if (tiles_before(m) * groups + int64_t(cost) * groups * m <= x) p = m, n -= half;
+        else n = half;
+      }
+      const int64_t begin = tiles_before(p), mine = tiles_before(p + 1) - begin, w = mine + cost;
+      int64_t off = x - (begin * groups + int64_t(cost) * groups * p);
+      int k = 0;
+      while (off >= w) off -= w, ++k;
+      off -= cost;
+      if (off <= tol) off = 0;
+      else if (mine - off <= tol) off = 0, ++k;
+      unit = p * groups + k;  // (k = groups: the next entry's first)
+      tile = begin * groups + mine * k + off;
+    }
+    cut_tile[c] = tile;
+    cut_unit[c] = unit;
+  }
+  __syncthreads();
+  for (int c = tid; c < ctas; c += kPlanThreads) {
+    const int unit = cut_unit[c], p = min(unit / groups, max(base - 1, 0));
+    const int64_t run = cut_tile[c + 1] - cut_tile[c];
+    Run r{unit, 0, 0, 0, TreeAt{-1, 0, 0, 1}, int32_t(min(run, int64_t(INT32_MAX - 8))), {0, 0, 0}};
+    if (run > INT32_MAX - 8) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));  // (months of work)
+    if (run > 0) {
+      const int64_t begin = tiles_before(p), mine = tiles_before(p + 1) - begin;
+      const int2 u = p < kTreePlanUnits ? rows[p] : *reinterpret_cast<const int2 *>(&plan->unit[p].r0);
+      r.off = int32_t(cut_tile[c] - begin * groups - mine * (unit - p * groups));
+      r.r0 = u.x;
+      r.n = u.y;
+      r.at = plan->tree[p];
+    }
+    plan->run[c] = r;
+  }
+  if (few && warp < kFewUnits) {  // a unit's CTAs, for the joins
+    int2 span = make_int2(0, 0);
+    if (warp < units) {
+      const int p = warp / groups, k = warp % groups;
+      const int64_t mine = tiles_before(p + 1) - tiles_before(p), t0 = tiles_before(p) * groups + mine * k;
+      int c0 = 0, c1 = 0;  // the last CTA that begins no later than it; before its end
+      for (int c = lane; c < ctas; c += 32) {
+        if (cut_tile[c] <= t0) c0 = c;
+        if (cut_tile[c] < t0 + mine) c1 = c;
+      }
+      c0 = __reduce_max_sync(0xffffffffu, c0);
+      span = make_int2(c0, __reduce_max_sync(0xffffffffu, c1) - c0 + 1);
+    }
+    if (lane == 0) parts->span[warp] = span;
+  }
+  if (tid == 0) plan->n_units = base;
+}
+
+// A tree's CTA takes its run from the plan.  All threads.
+__device__ __forceinline__ void take_run(const Plan *plan, Smem &sm) {
+  if (threadIdx.x == 0) {
+    const int4 *run = reinterpret_cast<const int4 *>(&plan->run[blockIdx.x]);
+    const int4 r = __ldcg(run), at = __ldcg(run + 1);
+    sm.total = __ldcg(&plan->run[blockIdx.x].total);
+    sm.at0 = TreeAt{at.x, at.y, at.z, at.w};
+    sm.unit0 = r.x;
+    sm.off0 = r.y;
+    sm.row0 = r.z;
+    sm.rows = r.w;
+  }
+  __syncthreads();
 }
 
 template <bool P, bool T>
@@ -1473,11 +1685,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P, T> g
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < 2) parts->unit[2 * blockIdx.x + tid] = -1;
   tc_fence_before();
-  find_cuts(g, sm, parts, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
+  if (T)
+    take_run(g.plan, sm);
+  else
+    find_cuts(g, sm, parts, hdr);  // (its barriers also publish the barriers and the tensor memory's address)
   tc_fence_after();
   if (sm.total > 0) {
     if (warp >= kXWarp0) {
-      set_regs_up<kRegsX>();
+      set_regs_up<P ? kRegsXPacked : kRegsX>();
       role_x(g, sm, parts, hdr);
     } else if (warp >= kWWarp0) {
       set_regs_down<kRegsW>();
@@ -1813,10 +2028,12 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   g.per_head = 65536 / a.n_heads + 1;
   g.n_cols = (g.group + 15) / 16 * 16;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
-  if (packed || tree) {
-    e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, packed ? pack : 1, plan, hdr);
-    if (e != cudaSuccess) return e;
-  }
+  if (tree)
+    e = launch_pdl(paged_tree_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, packed ? pack : 1, groups,
+                   ctas, g.few, plan, parts, hdr);
+  else if (packed)
+    e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
+  if (e != cudaSuccess) return e;
   const auto launch = [&](auto p, auto t) {
     constexpr bool P = decltype(p)::value, T = decltype(t)::value;
     return launch_pdl(paged_attn_kernel<P, T>, unsigned(ctas), unsigned(kThreads), size_t(smem), stream,
