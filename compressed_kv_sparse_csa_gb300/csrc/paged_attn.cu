@@ -345,18 +345,17 @@ __device__ __forceinline__ bool past_table(const PagedAttn &a, int t) {
   const int64_t e = __ldcg(a.row_end + t);
   return e > (int64_t(a.c.seq_pages) << a.c.page_log2) && (a.row_begin == nullptr || __ldcg(a.row_begin + t) < e);
 }
-// The rows of node t - from of a tree behind row row0 of its sequence, from the first
-// that it may see to its own; `odd`: some lie where the table does not go, or the node
-// has no place (then it sees nothing).
-__device__ __forceinline__ Rows tree_rows(const PagedAttn &a, int t, int from, int64_t row0, bool *odd) {
+// The rows of a node of a tree behind row row0 of its sequence, from the first that it may
+// see (`begin`) to its own; `odd`: some lie where the table does not go, or the node has no
+// place (then it sees nothing).
+__device__ __forceinline__ Rows tree_rows(const PagedAttn &a, int node, int64_t begin, int64_t row0, bool *odd) {
   const int64_t room = int64_t(a.c.seq_pages) << a.c.page_log2;
-  if (row0 < 0 || t - from >= DS4X_TREE_MAX_NODES) {
+  if (row0 < 0 || node >= DS4X_TREE_MAX_NODES) {
     *odd = true;
     return Rows{0, 0};
   }
-  const int64_t b = a.row_begin != nullptr ? min(row0, max(int64_t(0), int64_t(__ldcg(a.row_begin + t)))) : 0;
-  const int64_t e = min(room, min(row0, room) + (t - from) + 1);
-  if (row0 > room - (t - from) - 1) *odd = true;
+  const int64_t b = min(row0, max(int64_t(0), begin)), e = min(room, min(row0, room) + node + 1);
+  if (row0 > room - node - 1) *odd = true;
   return b < e ? Rows{b, int32_t(e - b)} : Rows{0, 0};
 }
 // A planned unit's entry: its own, or, of a token in head groups, the token's.
@@ -1481,10 +1480,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
 // for as long as some kUnitCost tiles take, so cuts count that many more tiles a unit,
 // where CTAs have several tiles each (24 drafts of 7 to 13 nodes x 20 heads: a CTA that had
 // four units took 100 us beside others' 66).
-constexpr int kUnitCost = 5, kCostTiles = 8;
+constexpr int kUnitCost = 5, kCostTiles = 8, kTreeSnap = 1;
 constexpr int kTreePlanSeqs = 2048, kTreePlanUnits = 2048;  // held in shared memory
 __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn a, int pack, int groups, int ctas,
-                                                                       int few, Plan *__restrict__ plan,
+                                                                       uint64_t per_grid, int few, Plan *__restrict__ plan,
                                                                        Parts *__restrict__ parts,
                                                                        WsHeader *__restrict__ hdr) {
   constexpr int kWarps = kPlanThreads / 32;
@@ -1524,8 +1523,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn
         const int64_t row0 = __ldcg(a.tree_row0 + s);
         int64_t lo = 0, hi = 0;
         bool odd = false;
-        for (int j = 0; j < count; ++j) {
-          const Rows r = tree_rows(a, t + j, from, row0, &odd);
+        int64_t begin[kPackTokens] = {};
+        if (a.row_begin != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kPackTokens; ++j)
+            if (j < count) begin[j] = __ldcg(a.row_begin + t + j);
+        }
+#pragma unroll
+        for (int j = 0; j < kPackTokens; ++j) {
+          if (j >= count) break;
+          const Rows r = tree_rows(a, t + j - from, begin[j], row0, &odd);
           if (r.n == 0) continue;
           lo = hi == 0 ? r.r0 : min(lo, r.r0);
           hi = max(hi, r.r0 + r.n);
@@ -1573,12 +1580,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn
   const int cost = all >= int64_t(kCostTiles) * ctas ? kUnitCost : 0;
   const int64_t total = all + int64_t(cost) * units;
   // few tiles a CTA: cuts at whole multiples (see kOnes)
-  const int64_t even = (all + ctas - 1) / ctas;
+  const int64_t even = ctas > 1 ? int64_t(__umul64hi(uint64_t(all) + (ctas - 1), per_grid)) : all;
   const int64_t step = cost != 0 ? 0 : max(int64_t(all > kOnes ? 2 : 1), even);
   // a cut so near to a unit's end moves there
-  const int64_t tol = cost != 0 ? min(int64_t(kSnap), total / ctas >> 2) : min(int64_t(kSnap), all / ctas >> 2);
+  const int64_t tol = all >= int64_t(4) * ctas ? kTreeSnap : 0;
   for (int c = tid; c <= ctas; c += kPlanThreads) {
-    int64_t x = c >= ctas ? total : step != 0 ? min(c * step, total) : total / ctas * c + total % ctas * c / ctas;
+    const int64_t x = c >= ctas ? total : step != 0 ? min(c * step, total) : int64_t(__umul64hi(uint64_t(c) * uint64_t(total), per_grid));
     int unit = units;
     int64_t tile = all;
     if (x < total) {
@@ -1727,6 +1734,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P, T> g
 // blocks then read 9 or 10 parts a warp).  Sums go in a fixed order.
 constexpr int kJoinWarps = 16, kJoinThreads = 32 * kJoinWarps, kJoinFew = 16;
 
+// A tree's list comes from the plan, which was complete before the attention began: it is
+// made while the attention ends.
+template <bool T>
 __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, const Parts *__restrict__ parts,
                                                                          int ctas) {
   __shared__ int unit[2 * kMaxCtas];
@@ -1735,9 +1745,24 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
   __shared__ float wts[kJoinWarps][kMaxCtas];
   __shared__ float4 part_sum[kJoinWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = tid; i < 2 * kMaxCtas; i += kJoinThreads) unit[i] = i < 2 * ctas ? __ldcg(parts->unit + i) : -1;
+  if (T) {
+    const Run *run = g.plan->run;
+    for (int c = tid; c < kMaxCtas; c += kJoinThreads) {
+      int goes_on = -1, begins = -1;
+      if (c < ctas && __ldcg(&run[c].total) > 0) {
+        const int2 at = __ldcg(reinterpret_cast<const int2 *>(&run[c]));
+        const int2 next = c + 1 < ctas ? __ldcg(reinterpret_cast<const int2 *>(&run[c + 1])) : make_int2(0, 0);
+        if (at.y > 0) goes_on = at.x;
+        if (next.y > 0 && (next.x != at.x || at.y == 0)) begins = next.x;
+      }
+      unit[2 * c] = goes_on;
+      unit[2 * c + 1] = begins;
+    }
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = tid; i < 2 * kMaxCtas; i += kJoinThreads) unit[i] = i < 2 * ctas ? __ldcg(parts->unit + i) : -1;
+  }
   __syncthreads();
   if (warp == 0) {
     constexpr int kWords = kMaxCtas / 32;
@@ -1789,6 +1814,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
     }
   }
   __syncthreads();
+  if (T) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   const int items = item0[n_units];
   for (int item = blockIdx.x, e = 0; item < items; item += gridDim.x) {
     while (item >= item0[e + 1]) ++e;
@@ -2030,7 +2059,7 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
   if (tree)
     e = launch_pdl(paged_tree_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, packed ? pack : 1, groups,
-                   ctas, g.few, plan, parts, hdr);
+                   ctas, g.per_grid, g.few, plan, parts, hdr);
   else if (packed)
     e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
   if (e != cudaSuccess) return e;
@@ -2050,7 +2079,7 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   if (g.few)
     return launch_pdl(paged_combine_few_kernel, unsigned(a.n_tokens * g.groups * 2 * kHeads), unsigned(kFewThreads),
                       size_t(0), stream, g, static_cast<const Parts *>(parts));
-  return launch_pdl(paged_combine_kernel, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
+  return launch_pdl(tree ? paged_combine_kernel<true> : paged_combine_kernel<false>, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
                     static_cast<const Parts *>(parts), ctas);
 }
 
