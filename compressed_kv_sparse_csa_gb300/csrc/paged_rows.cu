@@ -358,57 +358,69 @@ paged_gather_kernel(PagedCache c, const int64_t *__restrict__ row0, void *__rest
 
 // ---- keeping accepted rows ---------------------------------------------------------
 
-// A block a sequence.  Its rows move kKeepRows at a time, all read before any is
-// written: entry i reads at or behind i, so what a later round reads no earlier one has
-// written.
+// A cluster of blocks a sequence.  Rows move a round at a time, kKeepPerWarp a warp, all
+// read before any is written: entry i reads at or behind i, so what a later round reads no
+// earlier one has written.  A round is four round trips (path, table, rows, and the
+// sequence's own before the first), so one that takes all entries is what counts: a block
+// moves 64 rows a round, a cluster up to 256 (16 drafts of 500 to 1000 nodes, lines of up to 333:
+// see launch_paged_keep).
 constexpr int kRowWords = DS4X_PAGED_ROW_BYTES / 16;  // 14 of codes, 8 of the RoPE part, 1 of scales
-constexpr int kKeepPerWarp = 4, kKeepRows = kWarps * kKeepPerWarp;
 
-__device__ __forceinline__ uint4 *row_word(const PagedCache &c, const PagedRow &p, int lane) {
-  const int64_t at = lane < 14   ? paged_code_off(p) + 16 * lane
-                     : lane < 22 ? paged_tail_off(c, p) + 16 * (lane - 14)
-                                 : paged_scale_off(c, p);
-  return reinterpret_cast<uint4 *>(const_cast<uint8_t *>(p.page) + at);
+__device__ __forceinline__ int64_t row_word(const PagedCache &c, int32_t at, int lane) {
+  const PagedRow p{nullptr, at};
+  return lane < 14   ? paged_code_off(p) + 16 * lane
+         : lane < 22 ? paged_tail_off(c, p) + 16 * (lane - 14)
+                     : paged_scale_off(c, p);
 }
 
+template <int kKeepPerWarp>
 __global__ void __launch_bounds__(kWarps * 32)
 paged_keep_kernel(PagedCache c, const int64_t *__restrict__ row0, const int32_t *__restrict__ path,
                   const int32_t *__restrict__ n_path, int64_t n_tokens, WsHeader *__restrict__ hdr) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x;
+  uint32_t rank, blocks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = int(blockIdx.x / blocks);
   const int64_t from = max(0, __ldcg(c.cu + s)), to = min(n_tokens, int64_t(__ldcg(c.cu + s + 1)));
   const int64_t nodes = max(int64_t(0), to - from), first = __ldcg(row0 + s);
   int64_t n = __ldcg(n_path + s);
   bool odd = n > nodes;
   n = min(n, nodes);
-  for (int64_t i0 = 0; i0 < n; i0 += kKeepRows) {
+  const int warps = int(blocks) * kWarps, w0 = int(rank) * kWarps + warp;
+  const int64_t round = int64_t(warps) * kKeepPerWarp;
+  for (int64_t i0 = 0; i0 < n; i0 += round) {
+    // lane k finds the source of the warp's row k, lane kKeepPerWarp + k its place
+    const int64_t i = i0 + w0 + (lane % kKeepPerWarp) * warps;
+    const bool mine = lane < 2 * kKeepPerWarp && i < n;
+    const int64_t j = mine ? __ldcg(path + from + i) : i;
+    PagedRow at{nullptr, 0};
+    if (mine && j > i && j < nodes) at = paged_row(c, s, first + (lane < kKeepPerWarp ? j : i));
+    odd = odd || (mine && j != i && at.page == nullptr);
     uint4 w[kKeepPerWarp];
-    uint4 *to_row[kKeepPerWarp];
+    uint32_t moves = __ballot_sync(0xffffffffu, at.page != nullptr);  // both found
+    moves &= moves >> kKeepPerWarp;
 #pragma unroll
     for (int k = 0; k < kKeepPerWarp; ++k) {
-      const int64_t i = i0 + warp + kWarps * k;
-      to_row[k] = nullptr;
-      if (i >= n) continue;
-      const int64_t j = __ldcg(path + from + i);
-      if (j == i) continue;
-      const bool in = j > i && j < nodes;
-      const PagedRow src = in ? paged_row(c, s, first + j) : PagedRow{nullptr, 0};
-      const PagedRow dst = in ? paged_row(c, s, first + i) : PagedRow{nullptr, 0};
-      if (src.page == nullptr || dst.page == nullptr) {
-        odd = true;
-      } else if (lane < kRowWords) {
-        w[k] = __ldcg(row_word(c, src, lane));
-        to_row[k] = row_word(c, dst, lane);
-      }
+      const unsigned long long page = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at.page), k);
+      const int32_t r = __shfl_sync(0xffffffffu, at.at, k);
+      if ((moves >> k & 1) && lane < kRowWords)
+        w[k] = __ldcg(reinterpret_cast<const uint4 *>(page + row_word(c, r, lane)));
     }
-    __syncthreads();
+    if (blocks == 1)
+      __syncthreads();
+    else
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
-    for (int k = 0; k < kKeepPerWarp; ++k)
-      if (to_row[k] != nullptr) __stcg(to_row[k], w[k]);
-    __syncthreads();
+    for (int k = 0; k < kKeepPerWarp; ++k) {
+      const unsigned long long page =
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at.page), kKeepPerWarp + k);
+      const int32_t r = __shfl_sync(0xffffffffu, at.at, kKeepPerWarp + k);
+      if ((moves >> k & 1) && lane < kRowWords) __stcg(reinterpret_cast<uint4 *>(page + row_word(c, r, lane)), w[k]);
+    }
   }
-  if (odd && lane == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+  if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
 }
 
 }  // namespace
@@ -444,8 +456,15 @@ cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const 
 
 cudaError_t launch_paged_keep(const PagedCache &c, const int64_t *row0, const int32_t *path, const int32_t *n_path,
                               int64_t n, void *ws, cudaStream_t stream) {
-  return launch_pdl(paged_keep_kernel, unsigned(c.n_seqs), kWarps * 32, 0, stream, c, row0, path, n_path, n,
-                    static_cast<WsHeader *>(ws));
+  // an accepted line has seldom half of a draft's nodes
+  const int64_t nodes = n / c.n_seqs;
+  unsigned blocks = 1;
+  while (blocks < 4 && int64_t(blocks) * 8 * kWarps < nodes / 2 && 2 * int64_t(blocks) * c.n_seqs < INT32_MAX) blocks *= 2;
+  WsHeader *hdr = static_cast<WsHeader *>(ws);
+  if (nodes <= 64)
+    return launch_pdl(paged_keep_kernel<2>, unsigned(c.n_seqs), kWarps * 32, 0, stream, c, row0, path, n_path, n, hdr);
+  return launch_pdl_clusters(paged_keep_kernel<8>, blocks, unsigned(c.n_seqs) * blocks, unsigned(kWarps * 32), size_t(0), stream, c,
+                             row0, path, n_path, n, hdr);
 }
 
 cudaError_t launch_paged_gather(const PagedCache &c, const int64_t *row0, void *out, bool out_bf16,

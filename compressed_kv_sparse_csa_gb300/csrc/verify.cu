@@ -75,6 +75,41 @@ __device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
   return v;
 }
 
+// A sum over each N lanes, the same in all of them.
+template <int N = 32>
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, v.h, o), l = __shfl_xor_sync(0xffffffffu, v.l, o);
+    const float s = __fadd_rn(v.h, h), bb = __fadd_rn(s, -v.h);
+    const float e = __fadd_rn(__fadd_rn(v.h, -__fadd_rn(s, -bb)), __fadd_rn(h, -bb));
+    v = Pair{s, __fadd_rn(e, __fadd_rn(v.l, l))};  // (made a pair once, at the end)
+  }
+  return pair(v.h, v.l);
+}
+// The first of n numbers where base and the sum up to it pass `want`, and has a part in it;
+// without one (by rounding) the last that is not 0, or -1.  base: what comes before it then.
+__device__ __forceinline__ int first_past(const Pair *v, int n, Pair want, Pair &base, int lane) {
+  int found = -1;
+  Pair found_base = base;
+  for (int b = 0; b < n; b += 32) {
+    const Pair mine = b + lane < n ? v[b + lane] : Pair{0.0f, 0.0f};
+    const Pair upto = base + warp_scan(mine, lane);
+    const uint32_t any = __ballot_sync(0xffffffffu, some(mine));
+    const uint32_t over = __ballot_sync(0xffffffffu, some(mine) && upto > want);
+    const int k = over != 0 ? __ffs(int(over)) - 1 : any != 0 ? 31 - __clz(any) : 0;
+    const Pair prev = shfl(upto, max(k - 1, 0));
+    if (any != 0) {
+      found = b + k;
+      found_base = k > 0 ? prev : base;
+    }
+    if (over != 0) break;
+    base = shfl(upto, 31);
+  }
+  base = found_base;
+  return found;
+}
+
 struct Shared {
   Pair sums[kMaxChunks];              // the block's chunks' sums of the latest pass
   Pair total[2][kMaxCluster];         // the blocks' (written by all of them), of this pass and the one before
@@ -110,13 +145,13 @@ __device__ __forceinline__ void store_remote(Pair *p, uint32_t r, Pair v) {
 // NaN and negative ones count as zero.
 __device__ __forceinline__ float clean(float v) { return fmaxf(v, 0.0f); }
 
-// N probabilities in a row, from element y on (a multiple of N; past the vocabulary: 0).
+// N probabilities in a row, from element y on (a multiple of N; from `end` on: 0).
 template <bool BF16, int N>
 struct Probs {
   static_assert(N * (BF16 ? 2 : 4) <= 16, "one load");
   uint32_t w[N * (BF16 ? 2 : 4) / 4];
-  __device__ __forceinline__ void load(const void *row, int y, int vocab) {
-    if (y + N <= vocab) {
+  __device__ __forceinline__ void load(const void *row, int y, int end) {
+    if (y + N <= end) {
       const uint8_t *at = static_cast<const uint8_t *>(row) + int64_t(y) * (BF16 ? 2 : 4);
       if constexpr (sizeof(w) == 16) {
         const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(at));
@@ -128,19 +163,13 @@ struct Probs {
     } else {
 #pragma unroll
       for (uint32_t &v : w) v = 0;
+#pragma unroll
       for (int i = 0; i < N; ++i)
-        if (y + i < vocab) {
-          if constexpr (BF16) {
-            const uint32_t v = __ldcg(static_cast<const uint16_t *>(row) + y + i);
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k)
-              if (k == i / 2) w[k] |= v << (16 * (i & 1));
-          } else {
-            const uint32_t v = __ldcg(static_cast<const uint32_t *>(row) + y + i);
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-              if (k == i) w[k] = v;
-          }
+        if (y + i < end) {
+          if constexpr (BF16)
+            w[i / 2] |= uint32_t(__ldcg(static_cast<const uint16_t *>(row) + y + i)) << (16 * (i & 1));
+          else
+            w[i] = __ldcg(static_cast<const uint32_t *>(row) + y + i);
         }
     }
   }
@@ -198,10 +227,11 @@ __device__ __forceinline__ bool among_children(const Shared &sm, int cur, int en
 }
 
 // A chunk's sum, by a warp.  `nodes`: the draft's, where tokens tried are left out, else 0.
-template <bool BF16>
+// AtOnce: 16-byte words of a row that a lane has on their way.
+template <bool BF16, int AtOnce>
 __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int chunk, int vocab, int cur, int nodes,
                                             int lane) {
-  constexpr int N = BF16 ? 8 : 4, kSteps = kChunk / (32 * N), kAtOnce = 4;
+  constexpr int N = BF16 ? 8 : 4, kSteps = kChunk / (32 * N), kAtOnce = AtOnce < kSteps ? AtOnce : kSteps;
   Pair2 acc{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
   for (int s0 = 0; s0 < kSteps; s0 += kAtOnce) {
@@ -239,15 +269,11 @@ __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int c
         acc.lo = add2(acc.lo, r.q != nullptr ? add2(s.lo, w.lo) : s.lo);
       }
   }
-  Pair v = acc.first() + acc.second();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = v + Pair{__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
-  return v;
+  return warp_sum(acc.first() + acc.second());
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader *__restrict__ hdr) {
+template <bool BF16, int AtOnce>
+__global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Verify v, WsHeader *__restrict__ hdr) {
   __shared__ Shared sm;
   // (waited for below: no block writes to one that has not begun)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -303,41 +329,34 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader 
   const int chunks = (v.vocab + kChunk - 1) / kChunk, per = (chunks + int(blocks) - 1) / int(blocks);
   const int c0 = min(chunks, int(rank) * per), c1 = min(chunks, c0 + per);
   int passes = 0;
-  // sums of what is left at the node, by chunk and by block: the total, and what this block's chunks come behind
+  // sums of what is left at the node, by chunk, by block and in all
   Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}};
-  const auto pass = [&](const Stand &at, Pair &before) {
+  const auto pass = [&](const Stand &at) {
     rows.p = row_of(v.target, v.target_stride, at.cur);
     rows.q = v.draft != nullptr && some(at.t) ? row_of(v.draft, v.draft_stride, at.cur) : nullptr;
     rows.t = at.t;
     Pair mine{0.0f, 0.0f};
     for (int c = c0 + warp; c < c1; c += kWarps) {
-      const Pair sum = chunk_sum<BF16>(sm, rows, c, v.vocab, at.cur, v.draft == nullptr ? at.last + 1 : 0, lane);
+      const Pair sum = chunk_sum<BF16, AtOnce>(sm, rows, c, v.vocab, at.cur, v.draft == nullptr ? at.last + 1 : 0, lane);
       if (lane == 0) sm.sums[c - c0] = sum;
       mine = mine + sum;
     }
     if (lane == 0) sm.red[warp] = mine;
     __syncthreads();
     Pair *total = sm.total[passes++ & 1];
-    if (tid < int(blocks)) {
-      Pair sum = sm.red[0];
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) sum = sum + sm.red[k];
-      store_remote(&total[rank], uint32_t(tid), sum);
+    if (warp == 0) {
+      const Pair sum = warp_sum<kWarps>(sm.red[lane % kWarps]);
+      if (lane < int(blocks)) store_remote(&total[rank], uint32_t(lane), sum);
     }
     cluster_barrier();
-    Pair sum{0.0f, 0.0f};
-    for (int k = 0; k < int(blocks); ++k) {
-      if (k == int(rank)) before = sum;
-      sum = sum + total[k];
-    }
-    return sum;
+    return warp_sum<kMaxCluster>(lane % kMaxCluster < int(blocks) ? total[lane % kMaxCluster] : Pair{0.0f, 0.0f});
   };
 
   // ---- the walk, the same in every warp -------------------------------------------------
   Stand at{0, 0, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
   int count = 1;
   bool summed = false;  // the sums are of what is left now
-  Pair left{0.0f, 0.0f}, before{0.0f, 0.0f};
+  Pair left{0.0f, 0.0f};
   if (tid == 0) sm.path[0] = 0;
   for (;;) {
     int j = -1;  // the next child
@@ -368,29 +387,19 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader 
     at.last = j;
     if (v.draft != nullptr) {
       at.t = at.t + at.C;
-      at.C = left = pass(at, before);
+      at.C = left = pass(at);
       summed = true;
     } else {
       at.C = at.C + -w;
     }
   }
-  if (!summed) left = pass(at, before);
+  if (!summed) left = pass(at);
 
   // ---- the last token ---------------------------------------------------------------------
   const Pair want = sm.u[0] * left;
-  // the block in whose slice it lies: the first whose sum passes it (by rounding none: the last with any)
-  int holder = -1;
-  {
-    const Pair *total = sm.total[(passes - 1) & 1];
-    Pair sum{0.0f, 0.0f};
-    int last = -1;
-    for (int k = 0; k < int(blocks); ++k) {
-      sum = sum + total[k];
-      if (some(total[k])) last = k;
-      if (holder < 0 && some(total[k]) && sum > want) holder = k;
-    }
-    if (holder < 0) holder = last;
-  }
+  // the block in whose slice it lies, then its chunk
+  Pair base{0.0f, 0.0f};
+  const int holder = first_past(sm.total[(passes - 1) & 1], int(blocks), want, base, lane);
   if (rank == 0) {
     __syncthreads();  // `path`
     for (int i = tid; i < nodes; i += kThreads) {
@@ -407,23 +416,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader 
   }
   if (holder != int(rank)) return;
   if (warp == 0) {
-    // the chunk, likewise
-    Pair base = before, pick_base{0.0f, 0.0f}, last_base{0.0f, 0.0f};
-    int pick = -1, last = -1;
-    for (int b = 0; b < c1 - c0 && pick < 0; b += 32) {
-      const Pair mine = b + lane < c1 - c0 ? sm.sums[b + lane] : Pair{0.0f, 0.0f};
-      const Pair upto = base + warp_scan(mine, lane);
-      const uint32_t any = __ballot_sync(0xffffffffu, some(mine));
-      const uint32_t over = __ballot_sync(0xffffffffu, some(mine) && upto > want);
-      const int k = over != 0 ? __ffs(int(over)) - 1 : any != 0 ? 31 - __clz(any) : 0;
-      const Pair prev = shfl(upto, max(k - 1, 0)), from_k = k > 0 ? prev : base;
-      if (over != 0) pick = b + k, pick_base = from_k;
-      if (any != 0) last = b + k, last_base = from_k;
-      base = shfl(upto, 31);
-    }
+    const int pick = first_past(sm.sums, c1 - c0, want, base, lane);
     if (lane == 0) {
-      sm.chunk = c0 + (pick >= 0 ? pick : last);
-      sm.base = pick >= 0 ? pick_base : last_base;
+      sm.chunk = c0 + pick;
+      sm.base = base;
       sm.found = INT32_MAX;
     }
   }
@@ -480,37 +476,31 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Verify v, WsHeader 
 }  // namespace
 
 cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t stream) {
-  static std::atomic<uint64_t> set[2];
-  auto *kernel = bf16 ? verify_kernel<true> : verify_kernel<false>;
+  static std::atomic<uint64_t> set[3];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(set[bf16].load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    set[bf16].fetch_or(bit, std::memory_order_acq_rel);
-  }
-  // as many blocks a sequence as are resident at once, and have a chunk for each warp
+  // As many blocks a sequence as are resident at once and find a chunk for each warp (61
+  // sequences of 50,257 tokens: 22.0 us with 8 blocks each, 23.8 with 4).
   const int chunks = (v.vocab + kChunk - 1) / kChunk;
   int blocks = 1;
-  while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && 2 * blocks * kWarps <= chunks)
-    blocks *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(v.n_seqs) * unsigned(blocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(blocks);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, v, static_cast<WsHeader *>(ws));
+  while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && blocks * kWarps < chunks) blocks *= 2;
+  // Where each block may have half an SM a lane has all of its chunk on its way (one sequence
+  // of 131,072 tokens: 7.3 us, 7.9 with half of it), else half, and twice the blocks an SM (256
+  // sequences: 51.9 us, 58.6 with all of it).
+  const bool wide = !bf16 && int64_t(blocks) * v.n_seqs <= 2 * int64_t(sms);
+  auto *kernel = bf16 ? verify_kernel<true, 4> : wide ? verify_kernel<false, 8> : verify_kernel<false, 4>;
+  std::atomic<uint64_t> &known = set[bf16 ? 0 : wide ? 1 : 2];
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(known.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    known.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl_clusters(kernel, unsigned(blocks), unsigned(v.n_seqs) * unsigned(blocks), unsigned(kThreads), size_t(0),
+                             stream, v, static_cast<WsHeader *>(ws));
 }
 
 }  // namespace ds4x
