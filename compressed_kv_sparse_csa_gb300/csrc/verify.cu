@@ -22,20 +22,26 @@
 //
 // Work split.  A cluster of 1 to 16 blocks a sequence, a contiguous slice of the
 // vocabulary each; every block walks by itself (the same numbers, the same order, so
-// the same decisions), and after a pass they swap their sums through distributed
-// shared memory.
+// the same decisions), and after a pass each gives its sum to all blocks by an
+// asynchronous store that counts on their barriers (a cluster barrier took 0.7 us
+// longer).  That wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which none
+// blocks.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace ds4x {
 namespace {
+
+using namespace ptx;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 1024;          // probabilities a warp sums at a time
 constexpr int kMaxChunks = DS4X_VERIFY_MAX_VOCAB / kChunk;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = DS4X_TREE_MAX_NODES;
+constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
 
 // A number in two floats, hi + lo (|lo| at most half a step of hi).
 struct __align__(8) Pair {
@@ -118,7 +124,8 @@ struct Shared {
   int32_t token[kMaxNodes];           // outside the vocabulary: -1
   int16_t parent[kMaxNodes], path[kMaxNodes];
   Pair base;
-  int chunk, found;
+  int chunk, found, abort_flag;
+  unsigned long long given[2];        // barriers of the totals
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -131,15 +138,35 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// *p of the cluster's block r, and eight bytes on its barrier
+__device__ __forceinline__ void give(Pair *p, unsigned long long *bar, uint32_t r, Pair v) {
+  const unsigned long long bits =
+      (unsigned long long)(__float_as_uint(v.l)) << 32 | (unsigned long long)(__float_as_uint(v.h));
+  asm volatile(
+      "{\n\t.reg .b32 x, y;\n\tmapa.shared::cluster.u32 x, %0, %2;\n\tmapa.shared::cluster.u32 y, %1, %2;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [x], %3, [y];\n\t}" ::"r"(smem_u32(p)),
+      "r"(smem_u32(bar)), "r"(r), "l"(bits)
+      : "memory");
 }
-// *p of the cluster's block r
-__device__ __forceinline__ void store_remote(Pair *p, uint32_t r, Pair v) {
-  const uint32_t a = uint32_t(__cvta_generic_to_shared(p));
-  asm volatile("{\n\t.reg .b32 x;\n\tmapa.shared::cluster.u32 x, %0, %1;\n\tst.shared::cluster.v2.f32 [x], {%2, %3};\n\t}" ::"r"(a),
-               "r"(r), "f"(v.h), "f"(v.l)
-               : "memory");
+
+__device__ __forceinline__ void wait_slowly(Shared &sm, uint32_t bar, uint32_t parity, WsHeader *hdr) {
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (;;) {
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try_wait_sleep(bar, parity, 2000)) return;
+    if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > kTimeoutNs) {
+      atomicExch(&hdr->status, int32_t(DS4X_ETIMEOUT));
+      *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void wait_bar(Shared &sm, unsigned long long *bar, uint32_t parity, WsHeader *hdr) {
+  const uint32_t b = smem_u32(bar);
+  if (!mbar_try_wait(b, parity)) wait_slowly(sm, b, parity, hdr);
 }
 
 // NaN and negative ones count as zero.
@@ -248,14 +275,13 @@ __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int c
                              ? sm.token[i] - (chunk * kChunk + 32 * N * s0) : -1;
       for (uint32_t m = __ballot_sync(0xffffffffu, at >= 0 && at < 32 * N * kAtOnce); m != 0; m &= m - 1) {
         const int x = __shfl_sync(0xffffffffu, at, __ffs(int(m)) - 1);  // of step x / (32 N), lane (x / N) % 32
-        if ((x / N) % 32 == lane) {
+        // (in every word without a branch: one word by its number would put them all in local memory)
+        const int word = (x / N) % 32 == lane ? 4 * (x / (32 * N)) + (BF16 ? x % N / 2 : x % N) : -1;
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k)
+        for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              if (k == x / (32 * N) && w == (BF16 ? x % N / 2 : x % N))
-                p[k].w[w] &= BF16 ? (x & 1 ? 0x0000ffffu : 0xffff0000u) : 0u;
-        }
+          for (int w = 0; w < 4; ++w)
+            p[k].w[w] &= word == 4 * k + w ? (BF16 ? (x & 1 ? 0x0000ffffu : 0xffff0000u) : 0u) : 0xffffffffu;
       }
     }
 #pragma unroll
@@ -275,8 +301,14 @@ __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int c
 template <bool BF16, int AtOnce>
 __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Verify v, WsHeader *__restrict__ hdr) {
   __shared__ Shared sm;
-  // (waited for below: no block writes to one that has not begun)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // (waited for below: no block writes to one that has not made its barriers)
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&sm.given[0]), 1);
+    mbar_init(smem_u32(&sm.given[1]), 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -335,6 +367,10 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     rows.p = row_of(v.target, v.target_stride, at.cur);
     rows.q = v.draft != nullptr && some(at.t) ? row_of(v.draft, v.draft_stride, at.cur) : nullptr;
     rows.t = at.t;
+    // (a barrier is used again two passes on, when every warp here is past its first use: the one between)
+    unsigned long long *given = &sm.given[passes & 1];
+    Pair *total = sm.total[passes & 1];
+    if (tid == 0) mbar_arrive_expect_tx(smem_u32(given), 8 * blocks);
     Pair mine{0.0f, 0.0f};
     for (int c = c0 + warp; c < c1; c += kWarps) {
       const Pair sum = chunk_sum<BF16, AtOnce>(sm, rows, c, v.vocab, at.cur, v.draft == nullptr ? at.last + 1 : 0, lane);
@@ -343,12 +379,12 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     }
     if (lane == 0) sm.red[warp] = mine;
     __syncthreads();
-    Pair *total = sm.total[passes++ & 1];
     if (warp == 0) {
       const Pair sum = warp_sum<kWarps>(sm.red[lane % kWarps]);
-      if (lane < int(blocks)) store_remote(&total[rank], uint32_t(lane), sum);
+      if (lane < int(blocks)) give(&total[rank], given, uint32_t(lane), sum);
     }
-    cluster_barrier();
+    wait_bar(sm, given, (passes >> 1) & 1, hdr);
+    ++passes;
     return warp_sum<kMaxCluster>(lane % kMaxCluster < int(blocks) ? total[lane % kMaxCluster] : Pair{0.0f, 0.0f});
   };
 
@@ -438,11 +474,14 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     w[2 * i + 1] = d.second();
   }
   if (v.draft == nullptr)
-    for (int i = at.cur + 1; i <= at.last; ++i)
-      if (sm.parent[i] == at.cur && (sm.token[i] & ~3) == y0)
+    for (int i = at.cur + 1; i <= at.last; ++i) {
+      const int k = sm.parent[i] == at.cur ? sm.token[i] - y0 : -1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k == (sm.token[i] & 3)) w[k] = Pair{0.0f, 0.0f};
+      for (int j = 0; j < 4; ++j) {
+        w[j].h = k == j ? 0.0f : w[j].h;
+        w[j].l = k == j ? 0.0f : w[j].l;
+      }
+    }
   const Pair upto = warp_scan((w[0] + w[1]) + (w[2] + w[3]), lane);
   if (lane == 31) sm.red[warp] = upto;
   const Pair prev = shfl_up(upto, 1);
