@@ -219,15 +219,27 @@ __device__ __forceinline__ Pair2 two_sum(float2 a, float2 b) {
   const float2 s = add2(a, b), bb = sub2(s, a);
   return Pair2{s, add2(sub2(a, sub2(s, bb)), sub2(b, bb))};
 }
-// max(p - t q, 0), t = th + tl
+// What is left of the target's probabilities: all of them, max(p - q, 0) or max(p - t q, 0).
+enum class Rest { kAll, kOne, kAny };
+// As p - min(p, t q), so that the difference's rounding error comes in two operations (of
+// what is not larger) and nothing is compared where t is 1.
+template <Rest R>
 __device__ __forceinline__ Pair2 rest(float2 p, float2 q, Pair t) {
-  const float2 minus = make_float2(-t.h, -t.h), h = mul2(minus, q);  // -th q = h + e
-  const float2 e = fma2(make_float2(-t.l, -t.l), q, fma2(minus, q, make_float2(-h.x, -h.y)));
-  Pair2 d = two_sum(p, h);
-  d.lo = add2(d.lo, e);
-  const float2 s = add2(d.hi, d.lo);
-  if (!(s.x > 0.0f)) d.hi.x = d.lo.x = 0.0f;
-  if (!(s.y > 0.0f)) d.hi.y = d.lo.y = 0.0f;
+  if (R == Rest::kAll) return Pair2{p, make_float2(0.0f, 0.0f)};
+  float2 h = q, e = make_float2(0.0f, 0.0f);  // t q = h - e
+  if (R == Rest::kAny) {
+    const float2 minus = make_float2(-t.h, -t.h);
+    h = mul2(make_float2(t.h, t.h), q);
+    e = fma2(make_float2(-t.l, -t.l), q, fma2(minus, q, h));
+  }
+  const float2 m = make_float2(fminf(h.x, p.x), fminf(h.y, p.y)), s = sub2(p, m);
+  Pair2 d{s, sub2(sub2(p, s), m)};
+  if (R == Rest::kAny) {
+    d.lo = add2(d.lo, e);
+    // t q rounded is p or more: nothing is left but what the rounding took, if anything
+    if (!(s.x > 0.0f)) d.lo.x = h.x > p.x ? 0.0f : fmaxf(d.lo.x, 0.0f);
+    if (!(s.y > 0.0f)) d.lo.y = h.y > p.y ? 0.0f : fmaxf(d.lo.y, 0.0f);
+  }
   return d;
 }
 
@@ -240,8 +252,9 @@ struct Stand {
 
 // The rows of the node where it stands, and what is taken off them.
 struct Rows {
-  const void *p, *q;  // q null: t is 0 or there is none
+  const void *p, *q;
   Pair t;
+  Rest kind;
 };
 
 // Whether some child of `cur` up to node `end` - 1 has token y.  All lanes ask alike.
@@ -255,7 +268,7 @@ __device__ __forceinline__ bool among_children(const Shared &sm, int cur, int en
 
 // A chunk's sum, by a warp.  `nodes`: the draft's, where tokens tried are left out, else 0.
 // AtOnce: 16-byte words of a row that a lane has on their way.
-template <bool BF16, int AtOnce>
+template <bool BF16, int AtOnce, Rest R>
 __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int chunk, int vocab, int cur, int nodes,
                                             int lane) {
   constexpr int N = BF16 ? 8 : 4, kSteps = kChunk / (32 * N), kAtOnce = AtOnce < kSteps ? AtOnce : kSteps;
@@ -267,9 +280,9 @@ __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int c
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       p[k].load(r.p, y0 + 32 * N * k, vocab);
-      if (r.q != nullptr) q[k].load(r.q, y0 + 32 * N * k, vocab);
+      if (R != Rest::kAll) q[k].load(r.q, y0 + 32 * N * k, vocab);
     }
-    for (int b = cur + 1; b < nodes; b += 32) {
+    for (int b = cur + 1; R == Rest::kAll && b < nodes; b += 32) {
       const int i = b + lane;
       const int32_t at = i < nodes && sm.parent[i] == cur && sm.token[i] >= 0
                              ? sm.token[i] - (chunk * kChunk + 32 * N * s0) : -1;
@@ -288,11 +301,10 @@ __device__ __forceinline__ Pair chunk_sum(const Shared &sm, const Rows &r, int c
     for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
-        Pair2 w{p[k].two(i), make_float2(0.0f, 0.0f)};
-        if (r.q != nullptr) w = rest(w.hi, q[k].two(i), r.t);
+        const Pair2 w = rest<R>(p[k].two(i), R != Rest::kAll ? q[k].two(i) : make_float2(0.0f, 0.0f), r.t);
         const Pair2 s = two_sum(acc.hi, w.hi);
         acc.hi = s.hi;
-        acc.lo = add2(acc.lo, r.q != nullptr ? add2(s.lo, w.lo) : s.lo);
+        acc.lo = add2(acc.lo, R != Rest::kAll ? add2(s.lo, w.lo) : s.lo);
       }
   }
   return warp_sum(acc.first() + acc.second());
@@ -362,10 +374,11 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   const int c0 = min(chunks, int(rank) * per), c1 = min(chunks, c0 + per);
   int passes = 0;
   // sums of what is left at the node, by chunk, by block and in all
-  Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}};
+  Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}, Rest::kAll};
   const auto pass = [&](const Stand &at) {
     rows.p = row_of(v.target, v.target_stride, at.cur);
-    rows.q = v.draft != nullptr && some(at.t) ? row_of(v.draft, v.draft_stride, at.cur) : nullptr;
+    rows.kind = v.draft == nullptr || !some(at.t) ? Rest::kAll : at.t.h == 1.0f && at.t.l == 0.0f ? Rest::kOne : Rest::kAny;
+    if (rows.kind != Rest::kAll) rows.q = row_of(v.draft, v.draft_stride, at.cur);
     rows.t = at.t;
     // (a barrier is used again two passes on, when every warp here is past its first use: the one between)
     unsigned long long *given = &sm.given[passes & 1];
@@ -373,7 +386,10 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     if (tid == 0) mbar_arrive_expect_tx(smem_u32(given), 8 * blocks);
     Pair mine{0.0f, 0.0f};
     for (int c = c0 + warp; c < c1; c += kWarps) {
-      const Pair sum = chunk_sum<BF16, AtOnce>(sm, rows, c, v.vocab, at.cur, v.draft == nullptr ? at.last + 1 : 0, lane);
+      const int tried = v.draft == nullptr ? at.last + 1 : 0;
+      const Pair sum = rows.kind == Rest::kAll   ? chunk_sum<BF16, AtOnce, Rest::kAll>(sm, rows, c, v.vocab, at.cur, tried, lane)
+                       : rows.kind == Rest::kOne ? chunk_sum<BF16, AtOnce, Rest::kOne>(sm, rows, c, v.vocab, at.cur, 0, lane)
+                                                 : chunk_sum<BF16, AtOnce, Rest::kAny>(sm, rows, c, v.vocab, at.cur, 0, lane);
       if (lane == 0) sm.sums[c - c0] = sum;
       mine = mine + sum;
     }
@@ -395,41 +411,47 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   Pair left{0.0f, 0.0f};
   if (tid == 0) sm.path[0] = 0;
   for (;;) {
-    int j = -1;  // the next child
-    for (int b = at.last + 1; b < nodes && j < 0; b += 32) {
-      const int i = b + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, i < nodes && sm.parent[i] == at.cur);
-      if (m != 0) j = b + __ffs(int(m)) - 1;
-    }
-    if (j < 0) break;
-    const int32_t x = sm.token[j];
-    if (x < 0 && rank == 0 && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
-    Pair w{sm.p[j], 0.0f}, bar = sm.u[j] * at.C;
-    if (v.draft != nullptr) {
-      const float q = sm.q[j];
-      // (not max(.., 0): what it is compared with is not below 0)
-      if (some(at.t)) w = w + -(q * at.t);
-      bar = q * bar;
-    } else if (at.last > at.cur && among_children(sm, at.cur, j, x, lane)) {
-      w.h = 0.0f;
-    }
-    if (w > bar) {
-      if (tid == 0) sm.path[count] = int16_t(j);
-      ++count;
-      at = Stand{j, j, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
-      summed = false;
-      continue;
-    }
-    at.last = j;
-    if (v.draft != nullptr) {
-      at.t = at.t + at.C;
-      at.C = left = pass(at);
-      summed = true;
-    } else {
+    bool ends = false;
+    for (;;) {
+      int j = -1;  // the next child
+      for (int b = at.last + 1; b < nodes && j < 0; b += 32) {
+        const int i = b + lane;
+        const uint32_t m = __ballot_sync(0xffffffffu, i < nodes && sm.parent[i] == at.cur);
+        if (m != 0) j = b + __ffs(int(m)) - 1;
+      }
+      ends = j < 0;
+      if (ends) break;
+      const int32_t x = sm.token[j];
+      if (x < 0 && rank == 0 && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
+      Pair w{sm.p[j], 0.0f}, bar = sm.u[j] * at.C;
+      if (v.draft != nullptr) {
+        const float q = sm.q[j];
+        // (not max(.., 0): what it is compared with is not below 0)
+        if (some(at.t)) w = w + -(q * at.t);
+        bar = q * bar;
+      } else if (at.last > at.cur && among_children(sm, at.cur, j, x, lane)) {
+        w.h = 0.0f;
+      }
+      if (w > bar) {
+        if (tid == 0) sm.path[count] = int16_t(j);
+        ++count;
+        at = Stand{j, j, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
+        summed = false;
+        continue;
+      }
+      at.last = j;
+      if (v.draft != nullptr) {
+        at.t = at.t + at.C;
+        break;
+      }
       at.C = at.C + -w;
     }
+    if (ends && summed) break;
+    left = pass(at);
+    if (ends) break;
+    at.C = left;
+    summed = true;
   }
-  if (!summed) left = pass(at);
 
   // ---- the last token ---------------------------------------------------------------------
   const Pair want = sm.u[0] * left;
@@ -464,12 +486,13 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   const int y0 = sm.chunk * kChunk + 4 * tid;
   Probs<BF16, 4> p, q;
   p.load(rows.p, y0, v.vocab);
-  if (rows.q != nullptr) q.load(rows.q, y0, v.vocab);
+  if (rows.kind != Rest::kAll) q.load(rows.q, y0, v.vocab);
   Pair w[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     Pair2 d{p.two(i), make_float2(0.0f, 0.0f)};
-    if (rows.q != nullptr) d = rest(d.hi, q.two(i), rows.t);
+    if (rows.kind == Rest::kOne) d = rest<Rest::kOne>(d.hi, q.two(i), rows.t);
+    if (rows.kind == Rest::kAny) d = rest<Rest::kAny>(d.hi, q.two(i), rows.t);
     w[2 * i] = d.first();
     w[2 * i + 1] = d.second();
   }
@@ -522,13 +545,13 @@ cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t str
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // As many blocks a sequence as are resident at once and find a chunk for each warp (61
-  // sequences of 50,257 tokens: 22.0 us with 8 blocks each, 23.8 with 4).
+  // sequences of 50,257 tokens: 20.3 us with 8 blocks each, some 8 % more with 4).
   const int chunks = (v.vocab + kChunk - 1) / kChunk;
   int blocks = 1;
   while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && blocks * kWarps < chunks) blocks *= 2;
   // Where each block may have half an SM a lane has all of its chunk on its way (one sequence
-  // of 131,072 tokens: 7.3 us, 7.9 with half of it), else half, and twice the blocks an SM (256
-  // sequences: 51.9 us, 58.6 with all of it).
+  // of 131,072 tokens: 6.7 us, 7.3 with half of it), else half, and twice the blocks an SM (256
+  // sequences: 49 us, some 13 % more with all of it).
   const bool wide = !bf16 && int64_t(blocks) * v.n_seqs <= 2 * int64_t(sms);
   auto *kernel = bf16 ? verify_kernel<true, 4> : wide ? verify_kernel<false, 8> : verify_kernel<false, 4>;
   std::atomic<uint64_t> &known = set[bf16 ? 0 : wide ? 1 : 2];
