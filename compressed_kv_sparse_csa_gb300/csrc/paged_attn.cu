@@ -198,7 +198,6 @@ struct Args {
   uint64_t per_grid;  // 2^64 / CTAs, rounded up
   int32_t few;        // at most kFewUnits units
   __device__ __forceinline__ bool packed() const { return multi; }
-  __device__ __forceinline__ bool planned() const { return plan != nullptr; }
 };
 // The same where the kernel is compiled for one form: the others' units cost it nothing.
 // P: several tokens a unit.  T: trees.
@@ -1482,6 +1481,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedAttn a, i
 // four units took 100 us beside others' 66).
 constexpr int kUnitCost = 5, kCostTiles = 8, kTreeSnap = 1;
 constexpr int kTreePlanSeqs = 2048, kTreePlanUnits = 2048;  // held in shared memory
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn a, int pack, int groups, int ctas,
                                                                        uint64_t per_grid, int few, Plan *__restrict__ plan,
                                                                        Parts *__restrict__ parts,
@@ -1625,10 +1625,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn
     }
     plan->run[c] = r;
   }
-  if (few && warp < kFewUnits) {  // a unit's CTAs, for the joins
+  for (int u = warp; few && u < kFewUnits; u += kWarps) {  // a unit's CTAs, for the joins
     int2 span = make_int2(0, 0);
-    if (warp < units) {
-      const int p = warp / groups, k = warp % groups;
+    if (u < units) {
+      const int p = u / groups, k = u % groups;
       const int64_t mine = tiles_before(p + 1) - tiles_before(p), t0 = tiles_before(p) * groups + mine * k;
       int c0 = 0, c1 = 0;  // the last CTA that begins no later than it; before its end
       for (int c = lane; c < ctas; c += 32) {
@@ -1638,7 +1638,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn
       c0 = __reduce_max_sync(0xffffffffu, c0);
       span = make_int2(c0, __reduce_max_sync(0xffffffffu, c1) - c0 + 1);
     }
-    if (lane == 0) parts->span[warp] = span;
+    if (lane == 0) parts->span[u] = span;
   }
   if (tid == 0) plan->n_units = base;
 }
@@ -2058,8 +2058,11 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   g.n_cols = (g.group + 15) / 16 * 16;
   g.per_grid = ~uint64_t(0) / uint64_t(ctas) + 1;  // (one CTA: 0, and its one inner cut is 0)
   if (tree)
-    e = launch_pdl(paged_tree_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, packed ? pack : 1, groups,
-                   ctas, g.per_grid, g.few, plan, parts, hdr);
+    e = a.n_tokens <= 256
+            ? launch_pdl(paged_tree_plan_kernel<256>, 1u, 256u, size_t(0), stream, a, packed ? pack : 1, groups, ctas,
+                         g.per_grid, g.few, plan, parts, hdr)
+            : launch_pdl(paged_tree_plan_kernel<kPlanThreads>, 1u, unsigned(kPlanThreads), size_t(0), stream, a,
+                         packed ? pack : 1, groups, ctas, g.per_grid, g.few, plan, parts, hdr);
   else if (packed)
     e = launch_pdl(paged_plan_kernel, 1u, unsigned(kPlanThreads), size_t(0), stream, a, pack, plan, hdr);
   if (e != cudaSuccess) return e;

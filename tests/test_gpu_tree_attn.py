@@ -283,3 +283,35 @@ def test_many_sequences():
     q, qv = queries(int(nodes.sum()), 4, 73)
     got, lse = run(pool, trees, row0, q)
     check(pool, trees, row0, qv, got, lse)
+
+
+@pytest.mark.parametrize("heads", [1, 40])
+def test_as_many_tokens_as_a_call_takes(heads):
+    """65,535 nodes of 70 sequences, more units than the plan holds in shared
+    memory; some checked."""
+    rng = np.random.default_rng(74)
+    nodes = [936] * 69 + [65535 - 69 * 936]
+    trees = [D.tree(rng, n, "level") for n in nodes]
+    row0 = rng.integers(0, 90, 70)
+    pool = Pool([int(r + n) for r, n in zip(row0, nodes)], 64, 75)
+    q, qv = queries(65535, heads, 76)
+    got, lse = run(pool, trees, row0, q)
+    out = C.bf16_decode(got[::311]).astype(np.float64)
+    for k, t in enumerate(range(0, 65535, 311)):
+        s, j = divmod(t, 936)
+        check_token(out[k], lse[t].astype(np.float64), pool.values(s, D.sees(trees[s], j, int(row0[s]))), qv[t], SCALE)
+
+
+@pytest.mark.parametrize("heads", [20, 64])
+def test_wide_tables(heads):
+    """A table wider than the rows need changes how work is split only where
+    the call has few tiles; the values are within the bounds all the same."""
+    rng = np.random.default_rng(77)
+    nodes, row0 = [9, 4, 30], [500, 3, 1200]
+    trees = [D.tree(rng, n, "random") for n in nodes]
+    rows = [r + n for r, n in zip(row0, nodes)]
+    q, qv = queries(sum(nodes), heads, 78)
+    for extra in (0, 400):
+        pool = Pool(rows, 32, 79, extra_entries=extra)
+        got, lse = run(pool, trees, row0, q)
+        check(pool, trees, row0, qv, got, lse)
