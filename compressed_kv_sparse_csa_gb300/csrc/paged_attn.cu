@@ -64,8 +64,8 @@
 //
 // Trees (drafted tokens): a node sees the rows before the draft and its own line of
 // ancestors.  A node of 33 heads or more is a unit by itself, and a row off its line is a
-// row that is not there (L does not look it up); of fewer heads neighbouring nodes share a
-// unit, L gives each tile 64 bits a node, and X leaves out what they do not see.  L walks a
+// row that is not there (L does not look it up); of fewer heads up to 32 neighbouring nodes share
+// a unit, L gives each tile 64 bits a node, and X leaves out what they do not see.  L walks a
 // node's line over the parents in shared memory when it comes to the draft's first row, four
 // tiles ahead.  Units, tiles and cuts are made beforehand by one block
 // (paged_tree_plan_kernel), so the kernel begins with one load; cuts count what a unit's
@@ -111,6 +111,7 @@ static_assert(kRegsX <= kRegsXPacked && 4 * kRegsLM + kWWarps * kRegsW + kXWarps
 constexpr int kAhead = 4;                            // L's ring of found tiles
 constexpr int kMaxCtas = 160;
 constexpr int kPackTokens = 8;     // tokens a unit, at most
+constexpr int kTreePack = 32;      // a tree's (a lane each)
 constexpr int kFewUnits = 16;      // up to so many units are joined by a block a head's half each
 constexpr uint32_t kOCol = 0;      // O^T: dims 128 i .. as columns 64 i .. 64 i + 63
 constexpr uint32_t kSCol = 256;    // S^T: two buffers of 64 columns
@@ -158,10 +159,10 @@ struct __align__(1024) Smem {
   int2 seen[kPackTokens];           // packed: the rows that each token sees, from the unit's first
   long long out_at[kHeads];         // packed: a column's output (-1: no column)
   int end_unit, end_part;           // the CTA's last unit (-1: W has no part in its output), and its part (-1: the whole unit)
-  // trees: bit r of a tile's [token]: the token sees the tile's row r; [kPackTokens]: all tokens do.
+  // trees: bit r of a tile's [token]: the token sees the tile's row r; [kTreePack]: all tokens do.
   // L writes a tile's when W has taken the rows of four tiles before, so when X is done with eight before.
-  unsigned long long sees[2 * kAhead][kPackTokens + 1];
-  unsigned long long line[kPackTokens][kTreeWords + 1];  // a token's node and its ancestors (L's)
+  unsigned long long sees[2 * kAhead][kTreePack + 1];
+  unsigned long long line[kTreePack][kTreeWords + 1];  // a token's node and its ancestors (L's)
   int16_t parent[DS4X_TREE_MAX_NODES];                   // the sequence's (L's)
   TreeAt at0;                                            // unit0's
 };
@@ -703,8 +704,8 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
         if (A::packed()) {
           const unsigned long long all = ~warp_or(lane < count ? ~bits : 0);
           if (i >= kAhead) wait_bar(sm, &sm.lfree[i % kAhead], (i / kAhead - 1) & 1, hdr);
-          if (lane < kPackTokens) sm.sees[i % (2 * kAhead)][lane] = bits;
-          if (lane == 0) sm.sees[i % (2 * kAhead)][kPackTokens] = all;
+          sm.sees[i % (2 * kAhead)][lane] = bits;
+          if (lane == 0) sm.sees[i % (2 * kAhead)][kTreePack] = all;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -1176,7 +1177,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
               const int j = ((hb + 8 * (k >> 1) + (k & 1)) * g.per_head) >> 16;
-              if (j >= kPackTokens) break;
+              if (j >= (A::tree() ? kTreePack : kPackTokens)) break;
               if (A::tree()) {
                 if (rows & sm.sees[i % (2 * kAhead)][j]) wide |= 1u << k;
                 continue;
@@ -1209,11 +1210,11 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
         const int first = (w.off + (i - w.i0)) * kTile;
         if (A::tree()) {
           const unsigned long long *sees = sm.sees[i % (2 * kAhead)];
-          if (busy && ~sees[kPackTokens] != 0) {
+          if (busy && ~sees[kTreePack] != 0) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int j = ((hb + 8 * (k >> 2) + (k & 1)) * g.per_head) >> 16;
-              if (j < kPackTokens && !(sees[j] >> (r0 + 8 * ((k >> 1) & 1)) & 1)) d[k] = -INFINITY;
+              if (j < kTreePack && !(sees[j] >> (r0 + 8 * ((k >> 1) & 1)) & 1)) d[k] = -INFINITY;
             }
           }
         } else if (busy && (first < lo || first > hi - kTile)) {  // rows that some token does not see
@@ -1224,7 +1225,7 @@ __device__ __forceinline__ void role_x(const A &g, Smem &sm, Parts *parts, WsHea
           }
         }
         // a maximum is passed, or a first row sets one, however small
-        if (A::tree() && fresh == 0 && ~sm.sees[i % (2 * kAhead)][kPackTokens] == 0) {
+        if (A::tree() && fresh == 0 && ~sm.sees[i % (2 * kAhead)][kTreePack] == 0) {
           moves = over > kLazy;  // (every row counts, for every column)
         } else {
           moves = false;
@@ -1533,19 +1534,21 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tree_plan_kernel(PagedAttn
         const int64_t row0 = __ldcg(a.tree_row0 + s);
         int64_t lo = 0, hi = 0;
         bool odd = false;
-        int64_t begin[kPackTokens] = {};
-        if (a.row_begin != nullptr) {
+        for (int j0 = 0; j0 < count; j0 += 8) {
+          int64_t begin[8] = {};
+          if (a.row_begin != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kPackTokens; ++j)
-            if (j < count) begin[j] = __ldcg(a.row_begin + t + j);
-        }
+            for (int j = 0; j < 8; ++j)
+              if (j0 + j < count) begin[j] = __ldcg(a.row_begin + t + j0 + j);
+          }
 #pragma unroll
-        for (int j = 0; j < kPackTokens; ++j) {
-          if (j >= count) break;
-          const Rows r = tree_rows(a, t + j - from, begin[j], row0, &odd);
-          if (r.n == 0) continue;
-          lo = hi == 0 ? r.r0 : min(lo, r.r0);
-          hi = max(hi, r.r0 + r.n);
+          for (int j = 0; j < 8; ++j) {
+            if (j0 + j >= count) break;
+            const Rows r = tree_rows(a, t + j0 + j - from, begin[j], row0, &odd);
+            if (r.n == 0) continue;
+            lo = hi == 0 ? r.r0 : min(lo, r.r0);
+            hi = max(hi, r.r0 + r.n);
+          }
         }
         if (odd) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
         unit = 1;
@@ -2059,7 +2062,21 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   // 1 sequence x 2 tokens x 20 heads x 700 rows 17.1 / 12.2, 8 x 2 x 16 x 2000
   // 22.4 / 23.0, 24 x 5 x 20 x 4500 66 / 130, 1 x 512 x 16 x 4096 124 / 420.
   const bool tree = a.parent != nullptr;
-  const int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
+  int pack = kHeads / a.n_heads < kPackTokens ? kHeads / a.n_heads : kPackTokens;
+  if (tree && pack == kPackTokens) {
+    // Few heads: up to 32 nodes, no more than a draft has on average (columns that it leaves
+    // empty cost as much), and 32 columns where a CTA has few tiles, since a part's cost goes
+    // by its columns (8 drafts of 64 nodes over 8000 rows, 1 / 4 heads: 8 nodes a unit 101 /
+    // 106 us, 32 / 16 nodes 49 / 75; one such draft of 4 heads: 36, and 43 with 16 nodes).
+    const int64_t nodes = (int64_t(a.n_tokens) + a.c.n_seqs - 1) / a.c.n_seqs;
+    const auto up_to = [&](int64_t most) {
+      most = most < kTreePack ? most : kTreePack;
+      most = most < nodes ? most : nodes;
+      return most > kPackTokens ? int(most) : kPackTokens;
+    };
+    pack = up_to(kHeads / a.n_heads);
+    if ((a.n_tokens + pack - 1) / pack * ((rows + kTile - 1) / kTile) < 8 * int64_t(ctas)) pack = up_to(32 / a.n_heads);
+  }
   const bool packed = a.idx == nullptr && pack > 1 && a.n_tokens > a.c.n_seqs && most > 2 * ctas;
   Args g{a, packed || tree ? plan : nullptr, packed, groups, 0, 0, 0, 0, 0};
   g.few = int64_t(a.n_tokens) * g.groups <= kFewUnits;

@@ -315,3 +315,28 @@ def test_wide_tables(heads):
         pool = Pool(rows, 32, 79, extra_entries=extra)
         got, lse = run(pool, trees, row0, q)
         check(pool, trees, row0, qv, got, lse)
+
+
+@pytest.mark.parametrize("heads", [1, 2, 3, 5])
+@pytest.mark.parametrize("rows", [150, 9000])
+def test_few_heads_and_many_nodes_a_unit(heads, rows):
+    """Up to 32 nodes share a unit where heads are few: over few and many tiles,
+    with windows that differ by node and rows that some nodes do not see."""
+    rng = np.random.default_rng(80 + heads)
+    nodes = [70, 33, 0, 90, 31]
+    row0 = [rows, rows // 3, 5, rows - 40, 1]
+    trees = [D.tree(rng, n, s) if n else [] for n, s in zip(nodes, ["random", "level", "chain", "level", "forest"])]
+    pool = Pool([r + n for r, n in zip(row0, nodes)], 16, 81)
+    n = sum(nodes)
+    begin = np.empty(n, dtype=np.int64)
+    t = 0
+    for s, parent in enumerate(trees):
+        for j in range(len(parent)):
+            place = row0[s] + len(D.line(parent, j)) - 1
+            begin[t] = rng.choice([0, max(0, row0[s] - 70), row0[s] + 2, place, place + 1])
+            t += 1
+    q, qv = queries(n, heads, 82)
+    got, lse = run(pool, trees, row0, q, begin=begin)
+    check(pool, trees, row0, qv, got, lse, begin)
+    got, lse = run(pool, trees, row0, q)
+    check(pool, trees, row0, qv, got, lse)
