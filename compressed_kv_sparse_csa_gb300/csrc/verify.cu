@@ -221,25 +221,22 @@ __device__ __forceinline__ Pair2 two_sum(float2 a, float2 b) {
 }
 // What is left of the target's probabilities: all of them, max(p - q, 0) or max(p - t q, 0).
 enum class Rest { kAll, kOne, kAny };
-// As p - min(p, t q), so that the difference's rounding error comes in two operations (of
-// what is not larger) and nothing is compared where t is 1.
 template <Rest R>
 __device__ __forceinline__ Pair2 rest(float2 p, float2 q, Pair t) {
   if (R == Rest::kAll) return Pair2{p, make_float2(0.0f, 0.0f)};
-  float2 h = q, e = make_float2(0.0f, 0.0f);  // t q = h - e
-  if (R == Rest::kAny) {
-    const float2 minus = make_float2(-t.h, -t.h);
-    h = mul2(make_float2(t.h, t.h), q);
-    e = fma2(make_float2(-t.l, -t.l), q, fma2(minus, q, h));
+  if (R == Rest::kOne) {
+    // p - min(p, q): the rounding error of a difference from what is not larger takes two
+    // operations, and nothing has to be compared
+    const float2 m = make_float2(fminf(q.x, p.x), fminf(q.y, p.y)), s = sub2(p, m);
+    return Pair2{s, sub2(sub2(p, s), m)};
   }
-  const float2 m = make_float2(fminf(h.x, p.x), fminf(h.y, p.y)), s = sub2(p, m);
-  Pair2 d{s, sub2(sub2(p, s), m)};
-  if (R == Rest::kAny) {
-    d.lo = add2(d.lo, e);
-    // t q rounded is p or more: nothing is left but what the rounding took, if anything
-    if (!(s.x > 0.0f)) d.lo.x = h.x > p.x ? 0.0f : fmaxf(d.lo.x, 0.0f);
-    if (!(s.y > 0.0f)) d.lo.y = h.y > p.y ? 0.0f : fmaxf(d.lo.y, 0.0f);
-  }
+  const float2 minus = make_float2(-t.h, -t.h), h = mul2(minus, q);  // -th q = h + e
+  const float2 e = fma2(make_float2(-t.l, -t.l), q, fma2(minus, q, make_float2(-h.x, -h.y)));
+  Pair2 d = two_sum(p, h);
+  d.lo = add2(d.lo, e);
+  const float2 s = add2(d.hi, d.lo);
+  if (!(s.x > 0.0f)) d.hi.x = d.lo.x = 0.0f;
+  if (!(s.y > 0.0f)) d.hi.y = d.lo.y = 0.0f;
   return d;
 }
 
@@ -453,6 +450,13 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     summed = true;
   }
 
+  // (no block ends while another may still store into it: after a time-out not all stores have come)
+  if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const auto leave = [&]() {
+    __syncwarp();
+    if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+
   // ---- the last token ---------------------------------------------------------------------
   const Pair want = sm.u[0] * left;
   // the block in whose slice it lies, then its chunk
@@ -472,7 +476,10 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
       }
     }
   }
-  if (holder != int(rank)) return;
+  if (holder != int(rank)) {
+    leave();
+    return;
+  }
   if (warp == 0) {
     const int pick = first_past(sm.sums, c1 - c0, want, base, lane);
     if (lane == 0) {
@@ -533,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     if (tid == 0) sm.found = sm.chunk;
   }
   if (tid == 0) v.out[from + count - 1] = sm.found;
+  leave();
 }
 
 }  // namespace

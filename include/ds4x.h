@@ -706,6 +706,9 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  *              DS4X_EDEVICE)
  *   ws         the status header: 256 bytes, zero before first use
  *
+ * A sequence's blocks wait for one another's sums for 0.5 s at most; a wait that
+ * runs out sets DS4X_ETIMEOUT in ws, and the call's results are unspecified.
+ *
  * Probabilities need not sum to exactly 1 (the last draw is by their sum).
  * Negative ones and NaN count as zero.  Where all that is left is zero, the last
  * token is -1 and DS4X_EDEVICE is flagged.
