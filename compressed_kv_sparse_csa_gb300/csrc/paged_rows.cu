@@ -408,6 +408,7 @@ paged_keep_kernel(PagedCache c, const int64_t *__restrict__ row0, const int32_t 
       if ((moves >> k & 1) && lane < kRowWords)
         w[k] = __ldcg(reinterpret_cast<const uint4 *>(page + row_word(c, r, lane)));
     }
+    __syncwarp();
     if (blocks == 1)
       __syncthreads();
     else

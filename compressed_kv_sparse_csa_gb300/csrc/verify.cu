@@ -24,7 +24,7 @@
 // vocabulary each; every block walks by itself (the same numbers, the same order, so
 // the same decisions), and after a pass each gives its sum to all blocks by an
 // asynchronous store that counts on their barriers (a cluster barrier took 0.7 us
-// longer).  That wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which none
+// longer a pass).  That wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which none
 // blocks.
 #include <cuda_bf16.h>
 
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     sm.abort_flag = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   }
 
   // (no block ends while another may still store into it: after a time-out not all stores have come)
+  __syncwarp();
   if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const auto leave = [&]() {
     __syncwarp();
@@ -558,8 +560,8 @@ cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t str
   int blocks = 1;
   while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && blocks * kWarps < chunks) blocks *= 2;
   // Where each block may have half an SM a lane has all of its chunk on its way (one sequence
-  // of 131,072 tokens: 6.7 us, 7.3 with half of it), else half, and twice the blocks an SM (256
-  // sequences: 49 us, some 13 % more with all of it).
+  // of 131,072 tokens: 7.1 us, some 0.6 more with half of it), else half, and twice the blocks an
+  // SM (256 sequences: 50.7 us, some 13 % more with all of it).
   const bool wide = !bf16 && int64_t(blocks) * v.n_seqs <= 2 * int64_t(sms);
   auto *kernel = bf16 ? verify_kernel<true, 4> : wide ? verify_kernel<false, 8> : verify_kernel<false, 4>;
   std::atomic<uint64_t> &known = set[bf16 ? 0 : wide ? 1 : 2];
