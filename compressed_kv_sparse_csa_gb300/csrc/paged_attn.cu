@@ -316,6 +316,7 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
 // of count tokens from t0, head by head.
 struct Columns {
   int32_t t0, h0, n;
+  Columns() = default;
   template <class A>
   __device__ __forceinline__ Columns(const A &g, int unit) {
     if (g.packed()) {
@@ -1747,9 +1748,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(ArgsFor<P, T> g
 // blocks then read 9 or 10 parts a warp).  Sums go in a fixed order.
 constexpr int kJoinWarps = 16, kJoinThreads = 32 * kJoinWarps, kJoinFew = 16;
 
-// A tree's list comes from the plan, which was complete before the attention began: it is
-// made while the attention ends.
-template <bool T>
 __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, const Parts *__restrict__ parts,
                                                                          int ctas) {
   __shared__ int unit[2 * kMaxCtas];
@@ -1758,24 +1756,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
   __shared__ float wts[kJoinWarps][kMaxCtas];
   __shared__ float4 part_sum[kJoinWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (T) {
-    const Run *run = g.plan->run;
-    for (int c = tid; c < kMaxCtas; c += kJoinThreads) {
-      int goes_on = -1, begins = -1;
-      if (c < ctas && __ldcg(&run[c].total) > 0) {
-        const int2 at = __ldcg(reinterpret_cast<const int2 *>(&run[c]));
-        const int2 next = c + 1 < ctas ? __ldcg(reinterpret_cast<const int2 *>(&run[c + 1])) : make_int2(0, 0);
-        if (at.y > 0) goes_on = at.x;
-        if (next.y > 0 && (next.x != at.x || at.y == 0)) begins = next.x;
-      }
-      unit[2 * c] = goes_on;
-      unit[2 * c + 1] = begins;
-    }
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < 2 * kMaxCtas; i += kJoinThreads) unit[i] = i < 2 * ctas ? __ldcg(parts->unit + i) : -1;
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = tid; i < 2 * kMaxCtas; i += kJoinThreads) unit[i] = i < 2 * ctas ? __ldcg(parts->unit + i) : -1;
   __syncthreads();
   if (warp == 0) {
     constexpr int kWords = kMaxCtas / 32;
@@ -1827,10 +1810,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
     }
   }
   __syncthreads();
-  if (T) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  }
   const int items = item0[n_units];
   for (int item = blockIdx.x, e = 0; item < items; item += gridDim.x) {
     while (item >= item0[e + 1]) ++e;
@@ -1893,6 +1872,157 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_combine_kernel(Args g, 
       const int d = 8 * v_chunk_back(16 * quarter + (lane >> 1)) + 4 * (lane & 1);
       *reinterpret_cast<uint2 *>(g.a.out + col.at(g, h, g.a.out_stride, kDim) + d) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+    __syncwarp();  // wts is read
+  }
+}
+
+// The same for trees.  A warp takes all 512 dims of a head, so that its weights are formed
+// once, and reads four parts at a time; a block's 8 warps take eight heads, or, where the
+// unit has more than 8 parts, one, its parts dealt over them.  The list comes from the
+// plan, which was complete before the attention began: it is made while the attention ends.
+constexpr int kTreeJoinWarps = 8, kTreeJoinThreads = 32 * kTreeJoinWarps, kTreeJoinFew = 8;
+__global__ void __launch_bounds__(kTreeJoinThreads, 2) paged_tree_combine_kernel(Args g, const Parts *__restrict__ parts,
+                                                                                 int ctas) {
+  struct Joined {
+    Columns col;
+    int32_t c0, n, item0;  // the first CTA, the parts, the items before it
+  };
+  __shared__ int goes_on[kMaxCtas + 1];  // the unit that CTA c goes on with, or -1
+  __shared__ Joined list[kMaxCtas];
+  __shared__ int sum_units[kTreeJoinWarps], sum_items[kTreeJoinWarps];
+  __shared__ float wts[kTreeJoinWarps][kMaxCtas];
+  __shared__ float4 part_sum[kTreeJoinWarps][kDim / 4];
+  static_assert(kMaxCtas <= kTreeJoinThreads, "a thread a CTA");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int begins = -1;  // the unit that CTA tid begins and a later one ends
+  {
+    const Run *run = g.plan->run;
+    int mine = -1;
+    if (tid < ctas && __ldcg(&run[tid].total) > 0) {
+      const int2 at = __ldcg(reinterpret_cast<const int2 *>(&run[tid]));
+      const int2 next = tid + 1 < ctas ? __ldcg(reinterpret_cast<const int2 *>(&run[tid + 1])) : make_int2(0, 0);
+      if (at.y > 0) mine = at.x;
+      if (next.y > 0 && (next.x != at.x || at.y == 0)) begins = next.x;
+    }
+    if (tid <= kMaxCtas) goes_on[tid] = mine;
+  }
+  __syncthreads();
+  Joined u{};
+  int items = 0;
+  if (begins >= 0) {
+    u.col = Columns(g, begins);
+    u.c0 = tid;
+    u.n = 1;
+    for (int c = tid + 1; c < ctas && goes_on[c] == begins; ++c) ++u.n;
+    items = u.n <= kTreeJoinFew ? (u.col.n + kTreeJoinWarps - 1) / kTreeJoinWarps : u.col.n;
+  }
+  const uint32_t is = __ballot_sync(0xffffffffu, begins >= 0);
+  int incl = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) {
+    sum_units[warp] = __popc(is);
+    sum_items[warp] = incl;
+  }
+  __syncthreads();
+  int at = __popc(is & ((1u << lane) - 1)), all = 0;
+  u.item0 = incl - items;
+#pragma unroll
+  for (int k = 0; k < kTreeJoinWarps; ++k) {
+    if (k < warp) {
+      at += sum_units[k];
+      u.item0 += sum_items[k];
+    }
+    all += sum_items[k];
+  }
+  if (begins >= 0) list[at] = u;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int item = blockIdx.x, e = 0; item < all; item += gridDim.x) {
+    const auto end = [&](int k) {
+      const Joined &j = list[k];
+      return j.item0 + (j.n <= kTreeJoinFew ? (j.col.n + kTreeJoinWarps - 1) / kTreeJoinWarps : j.col.n);
+    };
+    while (item >= end(e)) ++e;
+    const Joined j = list[e];
+    const bool few = j.n <= kTreeJoinFew;
+    const int it = item - j.item0, h = few ? kTreeJoinWarps * it + warp : it;
+    const int k0 = few ? 0 : warp, step = few ? 1 : kTreeJoinWarps;
+    float4 o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < j.col.n) {  // (a block's warps differ in it only where few)
+      const auto slot = [&](int k) { return k == 0 ? 2 * j.c0 + 1 : 2 * (j.c0 + k); };
+      float4 v[4][4];
+      const auto load = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k + i * step < j.n) {
+            const float *po = &parts->o[slot(k + i * step)][h][4 * lane];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[i][q] = __ldcg(reinterpret_cast<const float4 *>(po + 128 * q));
+          }
+      };
+      load(k0);  // on their way while the weights are formed
+      float m = -INFINITY, s = 0.0f;
+      for (int k = lane; k < j.n; k += 32) m = fmaxf(m, wts[warp][k] = __ldcg(&parts->lse2[slot(k)][h]));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int k = lane; k < j.n; k += 32) {
+        const float x = wts[warp][k], w = x == -INFINITY ? 0.0f : exp2f(x - m);
+        wts[warp][k] = w;
+        s += w;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      __syncwarp();
+      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+      for (int k = k0;;) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k + i * step < j.n) {
+            const float w = wts[warp][k + i * step] * inv;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              o[q].x = fmaf(w, v[i][q].x, o[q].x);
+              o[q].y = fmaf(w, v[i][q].y, o[q].y);
+              o[q].z = fmaf(w, v[i][q].z, o[q].z);
+              o[q].w = fmaf(w, v[i][q].w, o[q].w);
+            }
+          }
+        k += 4 * step;
+        if (k >= j.n) break;
+        load(k);
+      }
+      if (lane == 0 && (few || warp == 0) && g.a.lse != nullptr)
+        g.a.lse[j.col.at(g, h, g.a.n_heads, 1)] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
+    }
+    if (!few) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part_sum[warp][32 * q + lane] = o[q];
+      __syncthreads();
+      if (warp == 0)
+        for (int k = 1; k < kTreeJoinWarps; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = part_sum[k][32 * q + lane];
+            o[q] = make_float4(o[q].x + v.x, o[q].y + v.y, o[q].z + v.z, o[q].w + v.w);
+          }
+      __syncthreads();
+    }
+    if (h < j.col.n && (few || warp == 0)) {
+      uint16_t *out = g.a.out + j.col.at(g, h, g.a.out_stride, kDim);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[q].x, o[q].y), hi = __floats2bfloat162_rn(o[q].z, o[q].w);
+        *reinterpret_cast<uint2 *>(out + 8 * v_chunk_back(16 * q + (lane >> 1)) + 4 * (lane & 1)) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+      }
     }
     __syncwarp();  // wts is read
   }
@@ -2109,7 +2239,10 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
   if (g.few)
     return launch_pdl(paged_combine_few_kernel, unsigned(a.n_tokens * g.groups * 2 * kHeads), unsigned(kFewThreads),
                       size_t(0), stream, g, static_cast<const Parts *>(parts));
-  return launch_pdl(tree ? paged_combine_kernel<true> : paged_combine_kernel<false>, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
+  if (tree)
+    return launch_pdl(paged_tree_combine_kernel, unsigned(2 * sms), unsigned(kTreeJoinThreads), size_t(0), stream, g,
+                      static_cast<const Parts *>(parts), ctas);
+  return launch_pdl(paged_combine_kernel, unsigned(2 * sms), unsigned(kJoinThreads), size_t(0), stream, g,
                     static_cast<const Parts *>(parts), ctas);
 }
 
