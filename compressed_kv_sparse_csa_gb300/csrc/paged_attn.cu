@@ -69,8 +69,8 @@
 // node's line over the parents in shared memory when it comes to the draft's first row, four
 // tiles ahead.  Units, tiles and cuts are made beforehand by one block
 // (paged_tree_plan_kernel), so the kernel begins with one load; cuts count what a unit's
-// start and end cost.  A draft of 255 nodes over 32,768 rows takes 1385 us (0.79 PFLOP/s,
-// 3170 cycles a tile), 26 nodes over 8192 rows 56 us, 6 over 777 rows 17 us.
+// start and end cost.  A draft of 255 nodes over 32,768 rows takes 1376 us (0.80 PFLOP/s,
+// 3150 cycles a tile), 26 nodes over 8192 rows 55.6 us, 6 over 777 rows 17 us.
 //
 // What bounds it.  Long histories and chunks: the chain of a tile, widen -> S ->
 // softmax -> O, about 3400 cycles a tile with the two V' buffers that shared memory

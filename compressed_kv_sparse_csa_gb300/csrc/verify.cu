@@ -26,6 +26,10 @@
 // asynchronous store that counts on their barriers (a cluster barrier took 0.7 us
 // longer a pass).  That wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which none
 // blocks.
+//
+// What bounds it.  Many sequences: DRAM, 256 chains of 8 over 131,072 tokens take 50.3 us
+// (5.3 TB/s), 8 us of them before and after the rows.  Few: latency, one chain of 6 takes
+// 7.1 us, 16 trees of 32 nodes 10.5 us.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
