@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   if (warp == 0) {
     const int pick = first_past(sm.sums, c1 - c0, want, base, lane);
     if (lane == 0) {
-      sm.chunk = c0 + pick;
+      sm.chunk = c0 + max(pick, 0);  // (after a time-out there may be none: no row is read before its start)
       sm.base = base;
       sm.found = INT32_MAX;
     }

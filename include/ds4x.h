@@ -710,8 +710,8 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  * runs out sets DS4X_ETIMEOUT in ws, and the call's results are unspecified.
  *
  * Probabilities need not sum to exactly 1 (the last draw is by their sum).
- * Negative ones and NaN count as zero.  Where all that is left is zero, the last
- * token is -1 and DS4X_EDEVICE is flagged.
+ * Negative ones and NaN count as zero; what an infinite one gives is unspecified.
+ * Where all that is left is zero, the last token is -1 and DS4X_EDEVICE is flagged.
  * Common errors as above; DS4X_EINVAL also for an output that overlaps another
  * array of the call.
  */
