@@ -19,7 +19,8 @@ struct WsHeader {
   uint32_t ticket;       // arrival counter of the fused scorer (self-resetting)
   uint32_t fallback;     // number of scorer calls that took the slow merge
   uint32_t wait_extra;   // arrivals the scorer's exchange waits for beyond its CTAs (0; a
-                         // nonzero value makes the bounded wait run out: the time-out test)
+                         // nonzero value makes the bounded wait run out: the time-out test;
+                         // likewise verification's wait for its blocks' sums)
   uint32_t pad[60];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");

@@ -24,8 +24,10 @@
 // vocabulary each; every block walks by itself (the same numbers, the same order, so
 // the same decisions), and after a pass each gives its sum to all blocks by an
 // asynchronous store that counts on their barriers (a cluster barrier took 0.7 us
-// longer a pass).  That wait is bounded (0.5 s): a time-out sets DS4X_ETIMEOUT, after which none
-// blocks.
+// longer a pass).  That wait is bounded (0.5 s).  Whether it ran out is agreed on by the
+// whole block, so that its warps never part: after a time-out (DS4X_ETIMEOUT) a block makes
+// no further pass, writes nothing and leaves with its cluster.  Another block may then
+// miss its sum, and runs out in its turn, once.
 //
 // What bounds it.  Many sequences: DRAM, 256 chains of 8 over 131,072 tokens take 50.3 us
 // (5.3 TB/s), 8 us of them before and after the rows.  Few: latency, one chain of 6 takes
@@ -46,6 +48,7 @@ constexpr int kMaxChunks = DS4X_VERIFY_MAX_VOCAB / kChunk;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = DS4X_TREE_MAX_NODES;
 constexpr unsigned long long kTimeoutNs = 500ull * 1000 * 1000;
+constexpr unsigned long long kDrainNs = 10ull * 1000 * 1000;
 
 // A number in two floats, hi + lo (|lo| at most half a step of hi).
 struct __align__(8) Pair {
@@ -153,24 +156,28 @@ __device__ __forceinline__ void give(Pair *p, unsigned long long *bar, uint32_t 
       : "memory");
 }
 
-__device__ __forceinline__ void wait_slowly(Shared &sm, uint32_t bar, uint32_t parity, WsHeader *hdr) {
-  unsigned long long t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+__device__ __forceinline__ unsigned long long globaltimer() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Whether the phase came in time (a thread's own finding: others may find otherwise).
+__device__ __forceinline__ bool wait_slowly(Shared &sm, uint32_t bar, uint32_t parity, WsHeader *hdr) {
+  const unsigned long long t0 = globaltimer();
   for (;;) {
     for (int k = 0; k < 64; ++k)
-      if (mbar_try_wait_sleep(bar, parity, 2000)) return;
-    if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    if (t - t0 > kTimeoutNs) {
+      if (mbar_try_wait_sleep(bar, parity, 2000)) return true;
+    if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return false;
+    if (globaltimer() - t0 > kTimeoutNs) {
       atomicExch(&hdr->status, int32_t(DS4X_ETIMEOUT));
       *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
-      return;
+      return false;
     }
   }
 }
-__device__ __forceinline__ void wait_bar(Shared &sm, unsigned long long *bar, uint32_t parity, WsHeader *hdr) {
+__device__ __forceinline__ bool wait_bar(Shared &sm, unsigned long long *bar, uint32_t parity, WsHeader *hdr) {
   const uint32_t b = smem_u32(bar);
-  if (!mbar_try_wait(b, parity)) wait_slowly(sm, b, parity, hdr);
+  return mbar_try_wait(b, parity) || wait_slowly(sm, b, parity, hdr);
 }
 
 // NaN and negative ones count as zero.
@@ -344,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
       p.w[0] = __ldcg(static_cast<const uint32_t *>(row) + y);
     return clean(__uint_as_float(BF16 ? p.w[0] << 16 : p.w[0]));
   };
+  // (bytes that no block gives: the time-out's test)
+  const uint32_t extra = tid == 0 && __ldcg(&hdr->wait_extra) != 0 ? 8u : 0u;
   bool odd = many;
   for (int i = tid; i < nodes; i += kThreads) {
     const int32_t up = __ldcg(v.parent + from + i);
@@ -375,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   const int chunks = (v.vocab + kChunk - 1) / kChunk, per = (chunks + int(blocks) - 1) / int(blocks);
   const int c0 = min(chunks, int(rank) * per), c1 = min(chunks, c0 + per);
   int passes = 0;
+  bool aborted = false;
   // sums of what is left at the node, by chunk, by block and in all
   Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}, Rest::kAll};
   const auto pass = [&](const Stand &at) {
@@ -385,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     // (a barrier is used again two passes on, when every warp here is past its first use: the one between)
     unsigned long long *given = &sm.given[passes & 1];
     Pair *total = sm.total[passes & 1];
-    if (tid == 0) mbar_arrive_expect_tx(smem_u32(given), 8 * blocks);
+    if (tid == 0) mbar_arrive_expect_tx(smem_u32(given), 8 * blocks + extra);
     Pair mine{0.0f, 0.0f};
     for (int c = c0 + warp; c < c1; c += kWarps) {
       const int tried = v.draft == nullptr ? at.last + 1 : 0;
@@ -401,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
       const Pair sum = warp_sum<kWarps>(sm.red[lane % kWarps]);
       if (lane < int(blocks)) give(&total[rank], given, uint32_t(lane), sum);
     }
-    wait_bar(sm, given, (passes >> 1) & 1, hdr);
+    const bool came = wait_bar(sm, given, (passes >> 1) & 1, hdr);
+    __syncwarp();
+    aborted = __syncthreads_or(!came) != 0;
     ++passes;
     return warp_sum<kMaxCluster>(lane % kMaxCluster < int(blocks) ? total[lane % kMaxCluster] : Pair{0.0f, 0.0f});
   };
@@ -450,18 +462,25 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     }
     if (ends && summed) break;
     left = pass(at);
-    if (ends) break;
+    if (ends || aborted) break;
     at.C = left;
     summed = true;
   }
 
-  // (no block ends while another may still store into it: after a time-out not all stores have come)
+  // (no block ends while another may still store into it)
   __syncwarp();
   if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const auto leave = [&]() {
     __syncwarp();
     if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   };
+  if (aborted) {
+    leave();
+    // Not all stores have come; none is begun any more.  One takes about a microsecond.
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < kDrainNs) __nanosleep(1000);
+    return;
+  }
 
   // ---- the last token ---------------------------------------------------------------------
   const Pair want = sm.u[0] * left;
@@ -489,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   if (warp == 0) {
     const int pick = first_past(sm.sums, c1 - c0, want, base, lane);
     if (lane == 0) {
-      sm.chunk = c0 + max(pick, 0);  // (after a time-out there may be none: no row is read before its start)
+      sm.chunk = c0 + max(pick, 0);  // (there is one, save where probabilities were infinite)
       sm.base = base;
       sm.found = INT32_MAX;
     }

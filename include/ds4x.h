@@ -111,8 +111,9 @@ int64_t ds4x_cache_bytes(int64_t context_tokens);
  * beyond the CTAs of the session.  It is 0 in normal use.  A nonzero value
  * makes the exchange's bounded wait run out (every CTA gives up after 0.5 s,
  * writes no output and sets DS4X_ETIMEOUT): it exists to test the time-out
- * path.  After a call that set DS4X_ETIMEOUT the workspace must be
- * zero-filled again before its next use.
+ * path.  The same bytes of a ds4x_verify_drafts workspace do the same to the
+ * waits of its blocks for one another.  After a call that set DS4X_ETIMEOUT
+ * the workspace must be zero-filled again before its next use.
  */
 int ds4x_workspace_init(void *ws, size_t ws_bytes, ds4x_stream_t stream);
 
@@ -135,7 +136,7 @@ int ds4x_copy_async(void *dst, const void *src, size_t bytes, ds4x_stream_t stre
  * after synchronising `stream`) into *status_host and clears it.  It is
  * DS4X_OK, or DS4X_EDEVICE when an attention call met an index outside
  * [-1, n_rows) (that row was skipped), or DS4X_ETIMEOUT when a bounded wait
- * inside the scorer gave up.  Returns DS4X_OK or DS4X_ECUDA.
+ * inside a kernel gave up.  Returns DS4X_OK or DS4X_ECUDA.
  */
 int ds4x_workspace_status(void *ws, ds4x_stream_t stream, int32_t *status_host);
 
@@ -707,7 +708,8 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  *   ws         the status header: 256 bytes, zero before first use
  *
  * A sequence's blocks wait for one another's sums for 0.5 s at most; a wait that
- * runs out sets DS4X_ETIMEOUT in ws, and the call's results are unspecified.
+ * runs out sets DS4X_ETIMEOUT in ws.  The call still ends, and that sequence's
+ * results are unspecified.
  *
  * Probabilities need not sum to exactly 1 (the last draw is by their sum).
  * Negative ones and NaN count as zero; what an infinite one gives is unspecified.
