@@ -6,6 +6,10 @@
 // renormalised: max(p - (t + C) q, 0) / C'.  So a node's whole history is the two
 // numbers t and C, and each rejection is one pass over the rows for the next C.
 // Without q the rest is p without the tokens tried, and C = 1 less theirs.
+// Exact rows leave nothing only where a rejection has probability 0.  Rounded ones do in
+// earnest (a bf16 probability from 0.998 up is 1, so p and q can be the same there and q larger
+// elsewhere): then the last token is drawn from p as it is, which takes a pass over q's row
+// (is it a distribution beside p?) and one over p's.
 //
 // What is read.  A child's decision needs p and q at one token: those of all
 // children are fetched at once, beforehand, so the walk runs in shared memory.
@@ -130,7 +134,7 @@ struct Shared {
   float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // of each node's token, after its parent
   int32_t token[kMaxNodes];           // outside the vocabulary: -1
   int16_t parent[kMaxNodes], path[kMaxNodes];
-  Pair base;
+  Pair base, drafted;                 // (drafted: the sum of a draft's whole row)
   int chunk, found, abort_flag;
   unsigned long long given[2];        // barriers of the totals
 };
@@ -230,6 +234,8 @@ __device__ __forceinline__ Pair2 two_sum(float2 a, float2 b) {
   const float2 s = add2(a, b), bb = sub2(s, a);
   return Pair2{s, add2(sub2(a, sub2(s, bb)), sub2(b, bb))};
 }
+// Where a node's sums are: to be made or made of what is left, or of the whole rows.
+enum class Sums { kNone, kLeft, kDraft, kTarget };
 // What is left of the target's probabilities: all of them, max(p - q, 0) or max(p - t q, 0).
 enum class Rest { kAll, kOne, kAny };
 template <Rest R>
@@ -387,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   bool aborted = false;
   // sums of what is left at the node, by chunk, by block and in all
   Rows rows{nullptr, nullptr, Pair{0.0f, 0.0f}, Rest::kAll};
-  const auto pass = [&](const Stand &at) {
-    rows.p = row_of(v.target, v.target_stride, at.cur);
+  const auto pass = [&](const Stand &at, Sums of) {
+    rows.p = of == Sums::kDraft ? row_of(v.draft, v.draft_stride, at.cur) : row_of(v.target, v.target_stride, at.cur);
     rows.kind = v.draft == nullptr || !some(at.t) ? Rest::kAll : at.t.h == 1.0f && at.t.l == 0.0f ? Rest::kOne : Rest::kAny;
     if (rows.kind != Rest::kAll) rows.q = row_of(v.draft, v.draft_stride, at.cur);
     rows.t = at.t;
@@ -421,12 +427,12 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   // ---- the walk, the same in every warp -------------------------------------------------
   Stand at{0, 0, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
   int count = 1;
-  bool summed = false;  // the sums are of what is left now
+  Sums sums = Sums::kNone;
   Pair left{0.0f, 0.0f};
   if (tid == 0) sm.path[0] = 0;
   for (;;) {
-    bool ends = false;
-    for (;;) {
+    bool ends = sums > Sums::kLeft;
+    while (!ends) {
       int j = -1;  // the next child
       for (int b = at.last + 1; b < nodes && j < 0; b += 32) {
         const int i = b + lane;
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
         if (tid == 0) sm.path[count] = int16_t(j);
         ++count;
         at = Stand{j, j, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
-        summed = false;
+        sums = Sums::kNone;
         continue;
       }
       at.last = j;
@@ -460,11 +466,19 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
       }
       at.C = at.C + -w;
     }
-    if (ends && summed) break;
-    left = pass(at);
-    if (ends || aborted) break;
-    at.C = left;
-    summed = true;
+    if (!ends || sums != Sums::kLeft) left = pass(at, sums);
+    if (aborted) break;
+    if (!ends) {
+      at.C = left;
+      sums = Sums::kLeft;
+      continue;
+    }
+    // nothing left after a rejection: the draft's row, then the target's
+    if (sums == Sums::kTarget || (sums != Sums::kDraft && (some(left) || at.last == at.cur))) break;
+    const bool draft = sums != Sums::kDraft && v.draft != nullptr;
+    if (tid == 0) sm.drafted = sums == Sums::kDraft ? left : Pair{0.0f, 0.0f};  // (read behind the next pass's barriers)
+    sums = draft ? Sums::kDraft : Sums::kTarget;
+    at = Stand{at.cur, at.cur, Pair{0.0f, 0.0f}, Pair{1.0f, 0.0f}};
   }
 
   // (no block ends while another may still store into it)
@@ -486,7 +500,9 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
   const Pair want = sm.u[0] * left;
   // the block in whose slice it lies, then its chunk
   Pair base{0.0f, 0.0f};
-  const int holder = first_past(sm.total[(passes - 1) & 1], int(blocks), want, base, lane);
+  // (the draft's sum twice the target's or more: no distribution beside it)
+  const bool none = sums == Sums::kTarget && !(left + left > sm.drafted);
+  const int holder = none ? -1 : first_past(sm.total[(passes - 1) & 1], int(blocks), want, base, lane);
   if (rank == 0) {
     __syncthreads();  // `path`
     for (int i = tid; i < nodes; i += kThreads) {

@@ -713,7 +713,12 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  *
  * Probabilities need not sum to exactly 1 (the last draw is by their sum).
  * Negative ones and NaN count as zero; what an infinite one gives is unspecified.
- * Where all that is left is zero, the last token is -1 and DS4X_EDEVICE is flagged.
+ * Rounded rows may leave nothing after a rejection (w is 0 everywhere: a bf16
+ * probability from 0.998 up is 1, and a target and a draft that are sure of the
+ * same token meet this in ordinary use); the last token is then drawn from the
+ * target's whole row, w = p.  Only where that is all zero, or the draft's row
+ * sums to twice the target's or more and so is no distribution beside it, the
+ * last token is -1 and DS4X_EDEVICE is flagged.
  * Common errors as above; DS4X_EINVAL also for an output that overlaps another
  * array of the call.
  */

@@ -58,6 +58,11 @@ def verify(parent, tokens, target, draft, u):
                 mass = p.sum()
         if took is None:
             c = np.cumsum(p)
+            if not c[-1] > 0 and cur in parent[cur + 1:]:
+                # rounded rows left nothing: the target's row as it is, if the draft's is one beside it
+                whole, drawn = np.cumsum(target[cur]), 0.0 if draft is None else draft[cur].sum()
+                if 2 * whole[-1] > drawn:
+                    p, c = target[cur], whole
             if not c[-1] > 0:
                 out.append(-1)
             else:
