@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
     sm.u[i] = __ldcg(v.u + from + i);
     const bool bad = up < -1 || up >= i;
     const int at = bad ? -1 : up;
-    odd = odd || bad;
     if (x < 0 || x >= v.vocab) x = -1;
+    odd = odd || bad || (x < 0 && i > 0);
     sm.parent[i] = int16_t(at);
     sm.token[i] = x;
     if (at >= 0 && x >= 0) {
@@ -442,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, AtOnce > 4 ? 2 : 4) verify_kernel(Ve
       ends = j < 0;
       if (ends) break;
       const int32_t x = sm.token[j];
-      if (x < 0 && rank == 0 && tid == 0) atomicExch(&hdr->status, int32_t(DS4X_EDEVICE));
       Pair w{sm.p[j], 0.0f}, bar = sm.u[j] * at.C;
       if (v.draft != nullptr) {
         const float q = sm.q[j];

@@ -689,7 +689,8 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  *   cu_tokens  i32 [n_seqs + 1], as above
  *   n_tokens   1 .. 2^31 - 1
  *   tokens     i32 [n_tokens]: the drafted tokens (node 0's is not looked at);
- *              one outside [0, vocab) is not accepted and flags DS4X_EDEVICE
+ *              one outside [0, vocab) is not accepted and flags DS4X_EDEVICE,
+ *              whether the walk comes to its node or not
  *   target     f32 or bf16 (type) [n_tokens][vocab]: row t is the target's
  *              distribution of the token after node t; target_stride
  *              elements from row to row (>= vocab, a multiple of 8 (bf16) or
