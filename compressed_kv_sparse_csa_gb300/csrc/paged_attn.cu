@@ -661,6 +661,8 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
       at_unit = TreeAt{v.x, v.y, v.z, v.w};
     }
     const int count = at_unit.count;
+    // (a unit may straddle the largest draft's end: the nodes behind see nothing)
+    const int placed = min(count, DS4X_TREE_MAX_NODES - (t - at_unit.from));
     bool fresh = true;
     // a list's entries are on their way a tile ahead
     int entry[2] = {0, 0};
@@ -698,7 +700,7 @@ __device__ __forceinline__ void role_l(const A &g, Smem &sm, WsHeader *hdr) {
           lines = true;
         }
         // (before the tree's first row no line is looked at)
-        unsigned long long bits = lane < count ? tree_sees(sm.line[lane], sight, first) : 0;
+        unsigned long long bits = lane < placed ? tree_sees(sm.line[lane], sight, first) : 0;
         if (w.n == 0) bits = 0;
         // a row that none of the unit's tokens sees is not there
         const unsigned long long any = A::packed() ? warp_or(bits) : __shfl_sync(0xffffffffu, bits, 0);
