@@ -2199,7 +2199,8 @@ cudaError_t launch_paged_attn(const PagedAttn &a, void *ws, cudaStream_t stream)
     // Few heads: up to 32 nodes, no more than a draft has on average (columns that it leaves
     // empty cost as much), and 32 columns where a CTA has few tiles, since a part's cost goes
     // by its columns (8 drafts of 64 nodes over 8000 rows, 1 / 4 heads: 8 nodes a unit 101 /
-    // 106 us, 32 / 16 nodes 49 / 75; one such draft of 4 heads: 36, and 43 with 16 nodes).
+    // 106 us, 32 / 16 nodes 49 / 75; one such draft of 4 heads: 36, and 43 with 16 nodes).  The
+    // drafts' own lengths are on the device, so a long one among many short ones has the short ones' units.
     const int64_t nodes = (int64_t(a.n_tokens) + a.c.n_seqs - 1) / a.c.n_seqs;
     const auto up_to = [&](int64_t most) {
       most = most < kTreePack ? most : kTreePack;

@@ -457,7 +457,9 @@ cudaError_t launch_paged_append(const PagedCache &c, const int64_t *row0, const 
 
 cudaError_t launch_paged_keep(const PagedCache &c, const int64_t *row0, const int32_t *path, const int32_t *n_path,
                               int64_t n, void *ws, cudaStream_t stream) {
-  // an accepted line has seldom half of a draft's nodes
+  // An accepted line has seldom half of a draft's nodes.  By the mean of the batch, since the
+  // lengths are on the device: a long draft among many short ones takes rounds of 16 rows
+  // (a line of 333 of 1000 nodes 5.5 us by itself, 20.3 beside 63 sequences of one node).
   const int64_t nodes = n / c.n_seqs;
   unsigned blocks = 1;
   while (blocks < 4 && int64_t(blocks) * 8 * kWarps < nodes / 2 && 2 * int64_t(blocks) * c.n_seqs < INT32_MAX) blocks *= 2;

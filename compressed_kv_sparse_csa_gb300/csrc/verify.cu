@@ -19,7 +19,8 @@
 //
 // Sums.  A token is chosen among up to 2^20 by where u falls between partial sums,
 // so those must be far better than fp32: pairs of floats, hi + lo, by error-free
-// additions (Knuth's two-sum) and products (by fma), good to 2^-44 or so.  Not fp64:
+// additions (Knuth's two-sum) and products (by fma), good to 2^-44 or so of what is
+// added, before t q is taken off.  Not fp64:
 // a warp's instruction takes some 50 cycles of an SM's one pipe.  256 sequences of
 // 131,072 tokens took 2.77 ms in fp64 throughout, and 206 us with fp64 from a warp's
 // 1024 on alone.
@@ -33,9 +34,10 @@
 // no further pass, writes nothing and leaves with its cluster.  Another block may then
 // miss its sum, and runs out in its turn, once.
 //
-// What bounds it.  Many sequences: DRAM, 256 chains of 8 over 131,072 tokens take 50.3 us
-// (5.3 TB/s), 8 us of them before and after the rows.  Few: latency, one chain of 6 takes
-// 7.1 us, 16 trees of 32 nodes 10.5 us.
+// What bounds it.  Many sequences: DRAM, 256 chains of 8 over 131,072 tokens take 49.2 us
+// (5.4 TB/s), 8 us of them before and after the rows; in bf16 36.2 us, the additions as
+// many for half the bytes; without a draft 32.5 us, in bf16 27.4.  Few: latency, one chain of
+// 6 takes 7.3 us, 16 trees of 32 nodes 10.4 us.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -593,13 +595,13 @@ cudaError_t launch_verify(const Verify &v, bool bf16, void *ws, cudaStream_t str
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // As many blocks a sequence as are resident at once and find a chunk for each warp (61
-  // sequences of 50,257 tokens: 20.3 us with 8 blocks each, some 8 % more with 4).
+  // sequences of 50,257 tokens: 20.1 us with 8 blocks each, some 8 % more with 4).
   const int chunks = (v.vocab + kChunk - 1) / kChunk;
   int blocks = 1;
   while (blocks < kMaxCluster && 2 * int64_t(blocks) * v.n_seqs <= 4 * int64_t(sms) && blocks * kWarps < chunks) blocks *= 2;
   // Where each block may have half an SM a lane has all of its chunk on its way (one sequence
-  // of 131,072 tokens: 7.1 us, some 0.6 more with half of it), else half, and twice the blocks an
-  // SM (256 sequences: 50.7 us, some 13 % more with all of it).
+  // of 131,072 tokens: 7.3 us, some 0.6 more with half of it), else half, and twice the blocks an
+  // SM (256 sequences: 49.2 us, some 13 % more with all of it).
   const bool wide = !bf16 && int64_t(blocks) * v.n_seqs <= 2 * int64_t(sms);
   auto *kernel = bf16 ? verify_kernel<true, 4> : wide ? verify_kernel<false, 8> : verify_kernel<false, 4>;
   std::atomic<uint64_t> &known = set[bf16 ? 0 : wide ? 1 : 2];

@@ -683,8 +683,11 @@ int ds4x_paged_tree_attn(const uint8_t *pages, int64_t n_pages, int32_t page_row
  *   sum_{z <= y} w(z) > u[node 0] sum_z w(z)
  *
  * (every probability where there were no children).  Comparisons and sums are
- * good to 2^-40 of the sum, so a result may differ from the exact one's only
- * where u is that near to a border.
+ * good to 2^-40 of the target's probabilities that go into them: of p(x), and of
+ * p's sum, not of the less that t q leaves of those.  A result may differ from
+ * the exact one's only where u is that near to a border (2^-40 where little is
+ * taken off, 2^-26 where 2^-14 of p is left).  Probabilities below 2^-100 count
+ * as far as FP32's least steps go.
  *
  *   cu_tokens  i32 [n_seqs + 1], as above
  *   n_tokens   1 .. 2^31 - 1

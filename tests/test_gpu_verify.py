@@ -1,8 +1,8 @@
 """ds4x_verify_drafts against the float64 walk of the oracle: the same nodes and
 tokens, whole.
 
-The kernel's comparisons are good to 2^-40 of what is compared (fp32 pairs and
-fp64).  The oracle says how near each walk's decisions came to their borders;
+The kernel's comparisons are good to 2^-40 of what is compared (pairs of floats
+throughout, about 2^-44 a sum).  The oracle says how near each walk's decisions came to their borders;
 inputs are seeded, and every compared walk keeps 2^-36 from its borders (which
 a sum's rounding cannot cross), save those of exact powers of two, whose sums
 are exact on both sides."""
